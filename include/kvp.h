@@ -15,7 +15,9 @@
  * kvp_chunk_compress (one step of chunked prefill-compress), kvp_rank_rows and
  * kvp_eviction_auc (static ranks; KVP's eviction-cost area of a ranking),
  * kvp_topk_cutoffs and kvp_sparse_lse_pass (KVpop's running top-k sparse
- * attention and its log-normalisers).
+ * attention and its log-normalisers), and the paged cache, in which a row holds
+ * only the pages its kept tokens need: kvp_paged_init, kvp_paged_append,
+ * kvp_paged_fork, kvp_paged_compact, kvp_paged_free and kvp_paged_decode_attn.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -446,6 +448,116 @@ int kvp_decode_attn(const void* q, const void* kc, const void* vc, int dtype, in
 int kvp_decode_attn_noalloc(const void* q, const void* kc, const void* vc, int dtype, int n_layers,
                             int h_q, int h_kv, int head_dim, int T_cap, const int32_t* len,
                             float sm_scale, float* out, kvp_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The paged cache.
+ *
+ * LKV, "LKV-H" (every KV head keeps its own budget b = floor(r * t)) and How
+ * much KV cache can you prune, "Conclusion" (a copy into a new tensor does not
+ * give the evicted entries' memory back while the old one lives): rows of very
+ * different lengths share one pool of pages, an eviction returns the pages it
+ * empties, and rows with a common prompt hold its pages once.
+ *
+ * A row is one (sequence or layer, KV head).  Its tokens 0 .. lens[r]-1 stand in
+ * pages of page_size tokens:
+ *
+ *   K of token t of row r = k_pool[table[r, t / page_size], t % page_size, :],  V likewise
+ *
+ * kvp_paged_cache is a HOST struct of DEVICE pointers; the caller owns every
+ * buffer and the calls below keep these books (kvp_paged_init sets them up):
+ * - live table entries of row r are j < ceil(lens[r] / page_size); the others are
+ *   not read, and are set to -1 when they are released;
+ * - refs[p] counts the live table entries that hold page p;
+ * - bit p % 32 of free_mask[p / 32] is set exactly when refs[p] = 0 (bits past
+ *   n_pages stay 0).
+ * score and pos (each nullable) hold a float and an int per slot of a row (the
+ * attention its token has received, its source position); they move with the
+ * tokens.
+ * Pages are taken in a fixed order: the i-th page that a call needs (rows in
+ * order, a row's pages in order) is the i-th lowest free one.  A row whose pages
+ * run past the free ones is left as it was and KVP_ERR_DEVICE_CHECK is raised, as
+ * it is for a page id, length, count or index out of range.
+ * page_size is a power of two in [16, 1024]; 16-byte aligned pools; strides are
+ * multiples of 16 bytes below 2^40 bytes.  max_pages * page_size <= 2^30,
+ * n_rows * max_pages < 2^31 and n_rows * max_pages * page_size <= 2^36.
+ * Calls that change a cache must be ordered with every other call on it (one
+ * stream, or events); decode calls without add_scores may overlap each other,
+ * each with its own workspace.
+ * ------------------------------------------------------------------------- */
+typedef struct kvp_paged_cache {
+  void* k_pool;          /* [n_pages, page_size, head_dim] dtype */
+  void* v_pool;          /* same shape and strides */
+  int64_t page_stride;   /* elements from page to page; 0 = dense */
+  int64_t token_stride;  /* elements from token to token of a page; 0 = head_dim */
+  int32_t* table;        /* [n_rows, max_pages] */
+  int32_t* lens;         /* [n_rows] */
+  int32_t* refs;         /* [n_pages] */
+  uint32_t* free_mask;   /* [ceil(n_pages / 32)] */
+  float* score;          /* [n_rows, max_pages * page_size] or NULL */
+  int32_t* pos;          /* [n_rows, max_pages * page_size] or NULL */
+  int dtype, head_dim, page_size, n_pages, n_rows, max_pages;
+} kvp_paged_cache;
+
+/* An empty cache: table -1, lens and refs 0, every page free. */
+int kvp_paged_init(const kvp_paged_cache* cache, kvp_stream_t stream);
+
+/* Append counts[r] (NULL: n_new) tokens to every row; 0 <= counts[r] <= n_new.
+ * new_k, new_v [n_rows / h_kv, h_kv, n_new, head_dim] dtype with element strides
+ * {batch, head, token} in the HOST arrays k_strides / v_strides (NULL = dense; a
+ * slice of a fused QKV projection is read in place).  A partly filled last page
+ * that other rows hold too is first copied to a fresh page.  The new slots get
+ * score 0 and pos new_pos[r] + i (new_pos NULL: the slot's index). */
+size_t kvp_paged_append_workspace_size(const kvp_paged_cache* cache, int n_new);
+int kvp_paged_append(const kvp_paged_cache* cache, const void* new_k, const void* new_v,
+                     const int64_t* k_strides, const int64_t* v_strides, int h_kv, int n_new,
+                     const int32_t* counts, const int32_t* new_pos, void* workspace,
+                     size_t workspace_bytes, kvp_stream_t stream);
+
+/* Give row r the tokens of row src[r] (src [n_rows] int32; negative: leave r).
+ * copy = 0: the pages are shared (refs grow, no token moves); copy = 1: they are
+ * copied to fresh pages.  Row r must be empty, and src[r] a row that is not itself
+ * given tokens by the same call. */
+size_t kvp_paged_fork_workspace_size(const kvp_paged_cache* cache, int copy);
+int kvp_paged_fork(const kvp_paged_cache* cache, const int32_t* src, int copy, void* workspace,
+                   size_t workspace_bytes, kvp_stream_t stream);
+
+/* Keep count[r] tokens of row r, in place (kvp_compact_kv's gather):
+ *
+ *   token m of row r = its token idx[r, m] before the call, for m < count[r]
+ *
+ * idx [n_rows, b_max] int32, ascending; count [n_rows] int32 in [0, min(b_max,
+ * lens[r])], negative: leave the row (kvp_select_topk's outputs).  A page that
+ * other rows hold too is replaced by a fresh one if its tokens change; pages the
+ * row no longer needs are released. */
+size_t kvp_paged_compact_workspace_size(const kvp_paged_cache* cache, int b_max);
+int kvp_paged_compact(const kvp_paged_cache* cache, const int32_t* idx, const int32_t* count,
+                      int b_max, void* workspace, size_t workspace_bytes, kvp_stream_t stream);
+
+/* Cut row r to its first keep[r] tokens (keep [n_rows] int32 <= lens[r]; negative:
+ * leave the row; NULL: empty every row) and release the pages behind them. */
+int kvp_paged_free(const kvp_paged_cache* cache, const int32_t* keep, kvp_stream_t stream);
+
+/* One-token decode attention over the paged rows (kvp_decode_attn's formula; row
+ * r = l * h_kv + h / G, n_layers = n_rows / h_kv):
+ *
+ *   out[l, h, :] = sum_{t < lens[r]} softmax_t(sm_scale * q[l, h] . k_t) v_t
+ *   lse[l, h]    = ln sum_{t < lens[r]} exp(sm_scale * q[l, h] . k_t)
+ *
+ * q [n_layers, h_q, head_dim] dtype, q_stride elements from layer to layer (0 =
+ * dense; multiple of 16 bytes); out [n_layers, h_q, head_dim] of out_dtype
+ * (KVP_F32 or the cache's dtype); lse [n_layers, h_q] float32 or NULL.  An empty
+ * row gives out 0 and lse -inf.  add_scores = 1 adds every token's probability,
+ * summed over the group's query heads, to cache->score.  G = h_q / h_kv <= 16.
+ * The work is split by the rows' lengths on the device, so one captured call
+ * serves a cache that grows and shrinks.  Slots behind a row's last token may
+ * hold anything.  workspace: kvp_paged_decode_attn_workspace_size() bytes,
+ * 256-byte aligned. */
+size_t kvp_paged_decode_attn_workspace_size(const kvp_paged_cache* cache, int h_q, int h_kv,
+                                            int add_scores);
+int kvp_paged_decode_attn(const void* q, int64_t q_stride, const kvp_paged_cache* cache, int h_q,
+                          int h_kv, float sm_scale, void* out, int out_dtype, float* lse,
+                          int add_scores, void* workspace, size_t workspace_bytes,
+                          kvp_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * Status and diagnostics.

@@ -50,6 +50,17 @@ SIGNATURES = {
     "kvp_decode_attn": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _F, _P, _P, _P, _I, _I, _P,
                              _SZ, _P]),
     "kvp_decode_attn_noalloc": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _F, _P, _P]),
+    # the first argument of the paged calls is a host kvp_paged_cache struct
+    "kvp_paged_init": (_I, [_P, _P]),
+    "kvp_paged_append_workspace_size": (_SZ, [_P, _I]),
+    "kvp_paged_append": (_I, [_P, _P, _P, _P, _P, _I, _I, _P, _P, _P, _SZ, _P]),
+    "kvp_paged_fork_workspace_size": (_SZ, [_P, _I]),
+    "kvp_paged_fork": (_I, [_P, _P, _I, _P, _SZ, _P]),
+    "kvp_paged_compact_workspace_size": (_SZ, [_P, _I]),
+    "kvp_paged_compact": (_I, [_P, _P, _P, _I, _P, _SZ, _P]),
+    "kvp_paged_free": (_I, [_P, _P, _P]),
+    "kvp_paged_decode_attn_workspace_size": (_SZ, [_P, _I, _I, _I]),
+    "kvp_paged_decode_attn": (_I, [_P, _I64, _P, _I, _I, _F, _P, _I, _P, _I, _P, _SZ, _P]),
     "kvp_status_string": (ctypes.c_char_p, [_I]),
     "kvp_last_error": (ctypes.c_char_p, []),
     "kvp_check_device_status": (_I, [_P]),

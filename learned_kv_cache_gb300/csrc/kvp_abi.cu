@@ -127,6 +127,84 @@ int use_tensor_cores(int dtype, bool* tc) {
   return KVP_OK;
 }
 
+// Checks a paged cache and fills in the strides that were left 0.
+int paged_view(const kvp_paged_cache* c, kvp::PagedView* out) {
+  if (!c) return fail(KVP_ERR_INVALID_ARG, "null cache");
+  if (c->dtype != KVP_F32 && c->dtype != KVP_BF16 && c->dtype != KVP_F16)
+    return fail(KVP_ERR_UNSUPPORTED, "dtype %d is not one of KVP_F32/KVP_BF16/KVP_F16", c->dtype);
+  if (c->head_dim != 64 && c->head_dim != 128) return fail(KVP_ERR_UNSUPPORTED, "head_dim=%d", c->head_dim);
+  if (c->page_size < 16 || c->page_size > 1024 || (c->page_size & (c->page_size - 1)))
+    return fail(KVP_ERR_UNSUPPORTED, "page_size=%d (a power of two in [16, 1024] is supported)", c->page_size);
+  if (c->n_pages < 1 || c->n_rows < 1 || c->max_pages < 1)
+    return fail(KVP_ERR_INVALID_ARG, "n_pages=%d n_rows=%d max_pages=%d must be >= 1", c->n_pages, c->n_rows,
+                c->max_pages);
+  const long long cap = (long long)c->max_pages * c->page_size;
+  if (cap > (1LL << 30) || cap * c->n_rows > (1LL << 36) || (long long)c->n_rows * c->max_pages > 0x7fffffffLL)
+    return fail(KVP_ERR_INVALID_ARG, "table too large: n_rows=%d max_pages=%d page_size=%d", c->n_rows,
+                c->max_pages, c->page_size);
+  if (!c->k_pool || !c->v_pool || !c->table || !c->lens || !c->refs || !c->free_mask)
+    return fail(KVP_ERR_INVALID_ARG, "null pointer in the cache");
+  if (!aligned16(c->k_pool) || !aligned16(c->v_pool))
+    return fail(KVP_ERR_INVALID_ARG, "k_pool/v_pool not 16-byte aligned");
+  kvp::PagedView v{};
+  v.k = c->k_pool;
+  v.v = c->v_pool;
+  v.token_stride = c->token_stride ? c->token_stride : c->head_dim;
+  v.page_stride = c->page_stride ? c->page_stride : v.token_stride * c->page_size;
+  const int elt = elem_size(c->dtype);
+  const int64_t st[2] = {v.page_stride, v.token_stride};
+  for (int i = 0; i < 2; ++i)
+    if (st[i] <= 0 || st[i] >= (1LL << 40) / elt || (st[i] * elt) % 16 != 0)
+      return fail(KVP_ERR_INVALID_ARG, "%s=%lld: strides must be positive multiples of 16 bytes below 2^40 bytes",
+                  i ? "token_stride" : "page_stride", (long long)st[i]);
+  if (v.token_stride < c->head_dim || v.page_stride < v.token_stride * (c->page_size - 1) + c->head_dim)
+    return fail(KVP_ERR_INVALID_ARG, "tokens or pages of a pool overlap: page_stride=%lld token_stride=%lld",
+                (long long)v.page_stride, (long long)v.token_stride);
+  v.table = c->table;
+  v.lens = c->lens;
+  v.refs = c->refs;
+  v.free_mask = c->free_mask;
+  v.score = c->score;
+  v.pos = c->pos;
+  v.dtype = c->dtype;
+  v.D = c->head_dim;
+  v.ps = c->page_size;
+  while ((1 << v.shift) < v.ps) ++v.shift;
+  v.n_pages = c->n_pages;
+  v.R = c->n_rows;
+  v.max_pages = c->max_pages;
+  v.cap = (int)cap;
+  *out = v;
+  return KVP_OK;
+}
+
+int check_workspace(const void* ws, size_t have, size_t need) {
+  if (need == 0) return KVP_OK;
+  if (!ws || have < need) return fail(KVP_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, have);
+  if (((uintptr_t)ws & 255u) != 0) return fail(KVP_ERR_INVALID_ARG, "workspace not 256-byte aligned");
+  return KVP_OK;
+}
+
+// Element strides {batch, head, token} of the tokens an append is given; NULL: dense.
+int new_token_strides(const char* name, const int64_t* given, const kvp::PagedView& v, int h_kv, int n_new,
+                      int64_t out[3]) {
+  out[2] = v.D;
+  out[1] = (int64_t)n_new * v.D;
+  out[0] = out[1] * h_kv;
+  if (!given) return KVP_OK;
+  const int elt = elem_size(v.dtype);
+  const int64_t extent[3] = {v.R / h_kv, h_kv, n_new};
+  for (int i = 0; i < 3; ++i) {
+    if (extent[i] <= 1) continue;
+    if (given[i] < 0 || given[i] >= (1LL << 40) / elt || (given[i] * elt) % 16 != 0)
+      return fail(KVP_ERR_INVALID_ARG,
+                  "%s[%d]=%lld: strides must be multiples of 16 bytes in [0, 2^40) bytes", name, i,
+                  (long long)given[i]);
+    out[i] = given[i];
+  }
+  return KVP_OK;
+}
+
 std::atomic<unsigned long long> g_launches{0};
 
 #define KVP_TRY(x)            \
@@ -612,6 +690,143 @@ int kvp_decode_attn_noalloc(const void* q, const void* kc, const void* vc, int d
   e = kvp::launch_decode(q, kc, vc, dtype, n_layers, h_q, h_kv, head_dim, T_cap, len, sm_scale, out,
                          nullptr, nullptr, 0, 0, plan, scratch, st, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "kvp_decode_attn_noalloc launch");
+  return KVP_OK;
+}
+
+int kvp_paged_init(const kvp_paged_cache* cache, kvp_stream_t stream) {
+  g_last_error.clear();
+  kvp::PagedView v;
+  KVP_TRY(paged_view(cache, &v));
+  cudaError_t e = kvp::launch_paged_init(v, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "kvp_paged_init launch");
+  return KVP_OK;
+}
+
+size_t kvp_paged_append_workspace_size(const kvp_paged_cache* cache, int n_new) {
+  kvp::PagedView v;
+  if (paged_view(cache, &v) != KVP_OK || n_new < 1) return 0;
+  return kvp::paged_append_workspace(v, n_new);
+}
+
+int kvp_paged_append(const kvp_paged_cache* cache, const void* new_k, const void* new_v,
+                     const int64_t* k_strides, const int64_t* v_strides, int h_kv, int n_new,
+                     const int32_t* counts, const int32_t* new_pos, void* workspace,
+                     size_t workspace_bytes, kvp_stream_t stream) {
+  g_last_error.clear();
+  kvp::PagedView v;
+  KVP_TRY(paged_view(cache, &v));
+  if (!new_k || !new_v) return fail(KVP_ERR_INVALID_ARG, "null new_k/new_v");
+  if (!aligned16(new_k) || !aligned16(new_v)) return fail(KVP_ERR_INVALID_ARG, "new_k/new_v not 16-byte aligned");
+  if (n_new < 1 || n_new > v.cap) return fail(KVP_ERR_INVALID_ARG, "n_new=%d outside [1, %d]", n_new, v.cap);
+  if (h_kv < 1 || v.R % h_kv) return fail(KVP_ERR_INVALID_ARG, "n_rows=%d not a multiple of h_kv=%d", v.R, h_kv);
+  if (new_pos && !v.pos) return fail(KVP_ERR_INVALID_ARG, "new_pos given, but the cache has no pos");
+  kvp::PagedNew a{};
+  a.k = new_k;
+  a.v = new_v;
+  KVP_TRY(new_token_strides("k_strides", k_strides, v, h_kv, n_new, a.ks));
+  KVP_TRY(new_token_strides("v_strides", v_strides, v, h_kv, n_new, a.vs));
+  a.h_kv = h_kv;
+  a.n_new = n_new;
+  a.counts = counts;
+  a.pos = new_pos;
+  KVP_TRY(check_workspace(workspace, workspace_bytes, kvp::paged_append_workspace(v, n_new)));
+  int* st = nullptr;
+  KVP_TRY(status_ptr(&st));
+  cudaError_t e = kvp::launch_paged_append(v, a, workspace, st, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "kvp_paged_append launch");
+  return KVP_OK;
+}
+
+size_t kvp_paged_fork_workspace_size(const kvp_paged_cache* cache, int copy) {
+  kvp::PagedView v;
+  if (paged_view(cache, &v) != KVP_OK) return 0;
+  return kvp::paged_fork_workspace(v, copy);
+}
+
+int kvp_paged_fork(const kvp_paged_cache* cache, const int32_t* src, int copy, void* workspace,
+                   size_t workspace_bytes, kvp_stream_t stream) {
+  g_last_error.clear();
+  kvp::PagedView v;
+  KVP_TRY(paged_view(cache, &v));
+  if (!src) return fail(KVP_ERR_INVALID_ARG, "null src");
+  if (copy != 0 && copy != 1) return fail(KVP_ERR_INVALID_ARG, "copy must be 0 or 1");
+  KVP_TRY(check_workspace(workspace, workspace_bytes, kvp::paged_fork_workspace(v, copy)));
+  int* st = nullptr;
+  KVP_TRY(status_ptr(&st));
+  cudaError_t e = kvp::launch_paged_fork(v, src, copy, workspace, st, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "kvp_paged_fork launch");
+  return KVP_OK;
+}
+
+size_t kvp_paged_compact_workspace_size(const kvp_paged_cache* cache, int b_max) {
+  kvp::PagedView v;
+  if (paged_view(cache, &v) != KVP_OK || b_max < 1) return 0;
+  return kvp::paged_compact_workspace(v, b_max);
+}
+
+int kvp_paged_compact(const kvp_paged_cache* cache, const int32_t* idx, const int32_t* count,
+                      int b_max, void* workspace, size_t workspace_bytes, kvp_stream_t stream) {
+  g_last_error.clear();
+  kvp::PagedView v;
+  KVP_TRY(paged_view(cache, &v));
+  if (!idx || !count) return fail(KVP_ERR_INVALID_ARG, "null idx/count");
+  if (b_max < 1 || b_max > (1 << 30)) return fail(KVP_ERR_INVALID_ARG, "b_max=%d outside [1, 2^30]", b_max);
+  KVP_TRY(check_workspace(workspace, workspace_bytes, kvp::paged_compact_workspace(v, b_max)));
+  int* st = nullptr;
+  KVP_TRY(status_ptr(&st));
+  cudaError_t e = kvp::launch_paged_compact(v, idx, count, b_max, workspace, st, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "kvp_paged_compact launch");
+  return KVP_OK;
+}
+
+int kvp_paged_free(const kvp_paged_cache* cache, const int32_t* keep, kvp_stream_t stream) {
+  g_last_error.clear();
+  kvp::PagedView v;
+  KVP_TRY(paged_view(cache, &v));
+  int* st = nullptr;
+  KVP_TRY(status_ptr(&st));
+  cudaError_t e = kvp::launch_paged_free(v, keep, st, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "kvp_paged_free launch");
+  return KVP_OK;
+}
+
+size_t kvp_paged_decode_attn_workspace_size(const kvp_paged_cache* cache, int h_q, int h_kv,
+                                            int add_scores) {
+  kvp::PagedView v;
+  if (paged_view(cache, &v) != KVP_OK || h_q < 1 || h_kv < 1 || h_q % h_kv || h_q / h_kv > 16) return 0;
+  return kvp::paged_decode_workspace(v, h_q, h_kv, add_scores);
+}
+
+int kvp_paged_decode_attn(const void* q, int64_t q_stride, const kvp_paged_cache* cache, int h_q,
+                          int h_kv, float sm_scale, void* out, int out_dtype, float* lse,
+                          int add_scores, void* workspace, size_t workspace_bytes,
+                          kvp_stream_t stream) {
+  g_last_error.clear();
+  kvp::PagedView v;
+  KVP_TRY(paged_view(cache, &v));
+  if (!q || !out) return fail(KVP_ERR_INVALID_ARG, "null q/out");
+  if (h_q < 1 || h_kv < 1) return fail(KVP_ERR_INVALID_ARG, "h_q=%d h_kv=%d must be >= 1", h_q, h_kv);
+  if (h_q % h_kv) return fail(KVP_ERR_INVALID_ARG, "h_q=%d not a multiple of h_kv=%d", h_q, h_kv);
+  if (v.R % h_kv) return fail(KVP_ERR_INVALID_ARG, "n_rows=%d not a multiple of h_kv=%d", v.R, h_kv);
+  if (h_q / h_kv > 16) return fail(KVP_ERR_UNSUPPORTED, "group size %d > 16", h_q / h_kv);
+  const int64_t dense = (int64_t)h_q * v.D;
+  if (q_stride == 0) q_stride = dense;
+  const int elt = elem_size(v.dtype);
+  if (q_stride < dense || q_stride >= (1LL << 40) / elt || (q_stride * elt) % 16 != 0)
+    return fail(KVP_ERR_INVALID_ARG, "q_stride=%lld: at least h_q * head_dim and a multiple of 16 bytes below 2^40 bytes",
+                (long long)q_stride);
+  if (!aligned16(q) || !aligned16(out)) return fail(KVP_ERR_INVALID_ARG, "q/out not 16-byte aligned");
+  if (out_dtype != KVP_F32 && out_dtype != v.dtype)
+    return fail(KVP_ERR_UNSUPPORTED, "out_dtype %d is neither KVP_F32 nor the cache's dtype", out_dtype);
+  if (!std::isfinite(sm_scale)) return fail(KVP_ERR_INVALID_ARG, "sm_scale not finite");
+  if (add_scores != 0 && add_scores != 1) return fail(KVP_ERR_INVALID_ARG, "add_scores must be 0 or 1");
+  if (add_scores && !v.score) return fail(KVP_ERR_INVALID_ARG, "add_scores given, but the cache has no score");
+  KVP_TRY(check_workspace(workspace, workspace_bytes, kvp::paged_decode_workspace(v, h_q, h_kv, add_scores)));
+  int* st = nullptr;
+  KVP_TRY(status_ptr(&st));
+  const kvp::PagedDecodeArgs a{q, q_stride, h_q, h_kv, sm_scale, out, out_dtype == KVP_F32, lse, add_scores};
+  cudaError_t e = kvp::launch_paged_decode(v, a, workspace, st, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "kvp_paged_decode_attn launch");
   return KVP_OK;
 }
 

@@ -8,6 +8,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "../../include/kvp.h"
+
 namespace kvp {
 
 // Host-side count of kernel launches made by the library (diagnostics).
@@ -178,5 +180,49 @@ cudaError_t launch_decode(const void* q, const void* kc, const void* vc, int dty
                           float scale, float* out, float* key_mass, const int32_t* key_pos,
                           int T_src, int accumulate, const DecodePlan& plan, void* ws,
                           int* status, cudaStream_t st);
+
+// ------------------------------------------------------------------ paged cache
+// A validated kvp_paged_cache with its strides filled in (elements).
+struct PagedView {
+  void *k, *v;
+  int64_t page_stride, token_stride;
+  int32_t *table, *lens, *refs;
+  uint32_t* free_mask;
+  float* score;
+  int32_t* pos;
+  int dtype, D, ps, shift, n_pages, R, max_pages;
+  int cap;               // max_pages * ps: slots of a row
+};
+// New tokens of an append: row r = b * h_kv + h, element strides {batch, head, token}.
+struct PagedNew {
+  const void *k, *v;
+  int64_t ks[3], vs[3];
+  int h_kv, n_new;
+  const int32_t *counts, *pos;
+};
+cudaError_t launch_paged_init(const PagedView& c, cudaStream_t st);
+size_t paged_append_workspace(const PagedView& c, int n_new);
+cudaError_t launch_paged_append(const PagedView& c, const PagedNew& a, void* ws, int* status, cudaStream_t st);
+size_t paged_fork_workspace(const PagedView& c, int copy);
+cudaError_t launch_paged_fork(const PagedView& c, const int32_t* src, int copy, void* ws, int* status,
+                              cudaStream_t st);
+size_t paged_compact_workspace(const PagedView& c, int b_max);
+cudaError_t launch_paged_compact(const PagedView& c, const int32_t* idx, const int32_t* count, int b_max,
+                                 void* ws, int* status, cudaStream_t st);
+cudaError_t launch_paged_free(const PagedView& c, const int32_t* keep, int* status, cudaStream_t st);
+
+struct PagedDecodeArgs {
+  const void* q;
+  int64_t q_stride;
+  int h_q, h_kv;
+  float scale;
+  void* out;
+  int out_f32;
+  float* lse;
+  int add_scores;
+};
+size_t paged_decode_workspace(const PagedView& c, int h_q, int h_kv, int add_scores);
+cudaError_t launch_paged_decode(const PagedView& c, const PagedDecodeArgs& a, void* ws, int* status,
+                                cudaStream_t st);
 
 }  // namespace kvp

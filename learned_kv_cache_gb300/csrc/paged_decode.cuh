@@ -1,0 +1,128 @@
+// What the paged decode kernels share: how the rows' key tiles are dealt to the CTAs, and the
+// layout of the partial results that the join kernel puts together.
+//
+// The rows' lengths are known on the device only, differ by an order of magnitude under head-wise
+// budgets, and say nothing of the table's width.  So the host fixes the number of CTAs and the
+// device the split: the tiles of TILE keys of all rows form one sequence, and CTA c of the P active
+// ones takes [c * total / P, (c + 1) * total / P) of it.  A row that lies inside one CTA's range is
+// finished there; of a longer one every CTA leaves a partial (maximum, sum, output) that the join
+// kernel merges in CTA order, so results do not depend on timing.
+#pragma once
+
+#include "kvp_common.cuh"
+#include "kvp_launch.h"
+
+namespace kvp {
+namespace paged {
+
+constexpr int TILE = 64;                 // keys per tile
+constexpr int MIN_TILES = 4;             // tiles per CTA below which fewer CTAs are active
+
+// Range of one CTA in the tile sequence, kept for the join kernel.
+struct Range {
+  int begin, end;        // tiles
+  int row, tile;         // row and tile within the row at `begin`
+  int total, active;     // tiles of all rows; CTAs that take part
+  int pad[2];
+};
+
+struct Params {
+  PagedView c;
+  int G, Hq, Hkv;
+  int64_t q_stride;
+  float c2;              // scale * log2 e
+  int ctas;              // launched
+  float* part;           // [ctas][2][pstride]: m[GP], l[GP], o[GP][D]; slot 0: the row began in an
+  int pstride;           //   earlier CTA, slot 1: it goes on in the next one
+  Range* range;          // [ctas]
+  float* lse2;           // [R][GP] base-2 LSE of the rows finished in one CTA (scores only)
+  float* logits;         // [R * cap][GP] base-2 logits (scores only)
+  void* out;
+  int out_f32;
+  float* lse;
+  int* status;
+};
+
+__device__ __forceinline__ int row_len(const Params& p, int r) {
+  const int n = p.c.lens[r];
+  return n < 0 ? 0 : (n > p.c.cap ? p.c.cap : n);
+}
+__device__ __forceinline__ int tiles_of(int n) { return (n + TILE - 1) / TILE; }
+
+__device__ __forceinline__ int cta_begin(int c, int total, int active) {
+  return (int)((long long)c * total / active);
+}
+// CTA that owns tile x.
+__device__ __forceinline__ int cta_of(int x, int total, int active) {
+  return (int)((((long long)x + 1) * active - 1) / total);
+}
+
+// This CTA's range.  Every thread of the block calls it; `sh` holds 33 + 8 ints.  Each thread sums the
+// tiles of a run of consecutive rows; a block scan gives every run its place in the sequence.
+__device__ __forceinline__ Range find_range(const Params& p, int cta, int* sh) {
+  const int nt = blockDim.x, tid = threadIdx.x;
+  const int per = (p.c.R + nt - 1) / nt, r0 = min(tid * per, p.c.R), r1 = min(r0 + per, p.c.R);
+  int mine = 0;
+  for (int r = r0; r < r1; ++r) mine += tiles_of(row_len(p, r));
+  int total;
+  const int before = block_exclusive_scan(mine, sh, &total);
+  int active = (total + MIN_TILES - 1) / MIN_TILES;
+  if (active > p.ctas) active = p.ctas;
+  Range g{};
+  g.total = total;
+  g.active = active;
+  if (cta < active) {
+    g.begin = cta_begin(cta, total, active);
+    g.end = cta_begin(cta + 1, total, active);
+    if (g.begin >= before && g.begin < before + mine) {
+      int at = before, r = r0;
+      for (; r < r1; ++r) {
+        const int t = tiles_of(row_len(p, r));
+        if (g.begin < at + t) break;
+        at += t;
+      }
+      sh[33] = r;
+      sh[34] = g.begin - at;
+    }
+  }
+  __syncthreads();
+  if (cta < active) {
+    g.row = sh[33];
+    g.tile = sh[34];
+  }
+  if (tid == 0) p.range[cta] = g;
+  return g;
+}
+
+// Weight of a state whose maximum is m in a merge whose maximum is M.  A state that has seen no finite
+// logit weighs 0 (its sum is 0, or NaN, which 0 * NaN carries on).
+__device__ __forceinline__ float weight(float m, float M) { return m == -INFINITY ? 0.f : fast_exp2(m - M); }
+
+template <typename T>
+__device__ __forceinline__ void store_out(const Params& p, size_t i, float x) {
+  if (p.out_f32) {
+    reinterpret_cast<float*>(p.out)[i] = x;
+  } else {
+    // the one rounding of the result: to the type the model goes on with, when the caller asks for it
+    if constexpr (sizeof(T) == 4) reinterpret_cast<float*>(p.out)[i] = x;
+    else if constexpr (std::is_same<T, __half>::value) reinterpret_cast<__half*>(p.out)[i] = __float2half_rn(x);
+    else reinterpret_cast<__nv_bfloat16*>(p.out)[i] = __float2bfloat16_rn(x);
+  }
+}
+
+// Rows without tokens have no tile: the CTAs share them out by index.
+template <typename T, int D>
+__device__ __forceinline__ void empty_rows(const Params& p, int cta) {
+  for (int r = cta; r < p.c.R; r += p.ctas) {
+    const int n = p.c.lens[r];
+    if ((n < 0 || n > p.c.cap) && threadIdx.x == 0) raise_status(p.status, KVP_ERR_DEVICE_CHECK);
+    if (n > 0) continue;
+    const size_t head = (size_t)(r / p.Hkv) * p.Hq + (size_t)(r % p.Hkv) * p.G;
+    for (int e = threadIdx.x; e < p.G * D; e += blockDim.x) store_out<T>(p, head * D + e, 0.f);
+    if (p.lse)
+      for (int g = threadIdx.x; g < p.G; g += blockDim.x) p.lse[head + g] = -INFINITY;
+  }
+}
+
+}  // namespace paged
+}  // namespace kvp

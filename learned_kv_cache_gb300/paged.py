@@ -1,0 +1,264 @@
+"""The paged cache: rows of any length on one pool of pages (see include/kvp.h).
+
+A row is one (sequence or layer, KV head), as in the dense caches; its tokens live in pages that a
+row of ``table`` names.  :class:`PagedCache` wraps the buffers and the functions beside it are the
+C ABI's calls on them, with the checks of shapes, types and devices that need no look at the data.
+What only the device can see (a length or page out of range, no free page left) is raised by
+:func:`kvp_check_device_status`.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+
+import torch
+
+from ._lib import _DTYPE, KVP_F32, _check, _dtype, _need, load
+
+_NOTHING = contextlib.nullcontext()
+
+
+class _Desc(ctypes.Structure):
+    """kvp_paged_cache."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_pool", "v_pool")] + \
+               [(n, ctypes.c_int64) for n in ("page_stride", "token_stride")] + \
+               [(n, ctypes.c_void_p) for n in ("table", "lens", "refs", "free_mask", "score", "pos")] + \
+               [(n, ctypes.c_int) for n in ("dtype", "head_dim", "page_size", "n_pages", "n_rows", "max_pages")]
+
+
+class PagedCache:
+    """The buffers of a paged cache, checked once.
+
+    k_pool, v_pool [n_pages, page_size, head_dim] (views with a contiguous last axis and equal
+    strides will do: ``kv[:, 0]`` and ``kv[:, 1]`` of one [n_pages, 2, page_size, head_dim] buffer);
+    table int32 [n_rows, max_pages]; lens int32 [n_rows]; refs int32 [n_pages]; free_mask int32
+    [ceil(n_pages / 32)]; score float32 and pos int32 [n_rows, max_pages * page_size], each optional.
+    The buffers hold a cache's books already, or :func:`kvp_paged_init` empties them;
+    :meth:`empty` allocates a new cache.
+    """
+
+    def __init__(self, k_pool, v_pool, table, lens, refs, free_mask, score=None, pos=None):
+        for name, t in (("k_pool", k_pool), ("v_pool", v_pool)):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name} must be a torch.Tensor")
+            if not t.is_cuda or t.dim() != 3:
+                raise ValueError(f"{name} must be a CUDA tensor [n_pages, page_size, head_dim]")
+            if t.stride(2) != 1:
+                raise ValueError(f"{name}: the head_dim axis must be contiguous")
+        if v_pool.shape != k_pool.shape or v_pool.dtype != k_pool.dtype or v_pool.stride() != k_pool.stride():
+            raise ValueError("k_pool and v_pool must have the same shape, dtype and strides")
+        n_pages, page_size, head_dim = k_pool.shape
+        _need(table, "table", torch.int32)
+        if table.dim() != 2:
+            raise ValueError("table must be [n_rows, max_pages]")
+        n_rows, max_pages = table.shape
+        _need(lens, "lens", torch.int32, (n_rows,))
+        _need(refs, "refs", torch.int32, (n_pages,))
+        _need(free_mask, "free_mask", torch.int32, ((n_pages + 31) // 32,))
+        if score is not None:
+            _need(score, "score", torch.float32, (n_rows, max_pages * page_size))
+        if pos is not None:
+            _need(pos, "pos", torch.int32, (n_rows, max_pages * page_size))
+        self.device = k_pool.device
+        for name, t in (("v_pool", v_pool), ("table", table), ("lens", lens), ("refs", refs),
+                        ("free_mask", free_mask), ("score", score), ("pos", pos)):
+            if t is not None and t.device != self.device:
+                raise ValueError(f"{name} must be on {self.device}, got {t.device}")
+        self.k_pool, self.v_pool, self.table, self.lens = k_pool, v_pool, table, lens
+        self.refs, self.free_mask, self.score, self.pos = refs, free_mask, score, pos
+        self.dtype, self.n_rows, self.max_pages = k_pool.dtype, n_rows, max_pages
+        self.n_pages, self.page_size, self.head_dim = n_pages, page_size, head_dim
+        # strides of one-page (one-token) pools say nothing: 0 takes the dense ones
+        self._desc = _Desc(k_pool.data_ptr(), v_pool.data_ptr(),
+                           k_pool.stride(0) if n_pages > 1 else 0, k_pool.stride(1) if page_size > 1 else 0,
+                           table.data_ptr(), lens.data_ptr(), refs.data_ptr(), free_mask.data_ptr(),
+                           None if score is None else score.data_ptr(), None if pos is None else pos.data_ptr(),
+                           _dtype(k_pool), head_dim, page_size, n_pages, n_rows, max_pages)
+        self._ref = ctypes.byref(self._desc)
+        self._sizes = {}
+
+    @classmethod
+    def empty(cls, n_rows, max_pages, n_pages, page_size, head_dim, dtype=torch.bfloat16, device="cuda",
+              scores=False, positions=False):
+        """A new, empty cache; ``scores`` / ``positions``: with the per-slot arrays."""
+        def make(*shape, dtype=torch.int32):
+            return torch.empty(*shape, dtype=dtype, device=device)
+        cap = max_pages * page_size
+        c = cls(make(n_pages, page_size, head_dim, dtype=dtype), make(n_pages, page_size, head_dim, dtype=dtype),
+                make(n_rows, max_pages), make(n_rows), make(n_pages), make((n_pages + 31) // 32),
+                make(n_rows, cap, dtype=torch.float32).zero_() if scores else None,
+                make(n_rows, cap).zero_() if positions else None)
+        kvp_paged_init(c)
+        return c
+
+    def rows(self, start, stop):
+        """The rows [start, stop) (one layer's, say) as a cache on the same pages and books."""
+        if not 0 <= start < stop <= self.n_rows:
+            raise ValueError(f"rows [{start}, {stop}) of {self.n_rows}")
+        cut = (lambda t: None if t is None else t[start:stop])
+        return PagedCache(self.k_pool, self.v_pool, self.table[start:stop], self.lens[start:stop], self.refs,
+                          self.free_mask, cut(self.score), cut(self.pos))
+
+    def _workspace(self, fn, *args):
+        """A workspace for one call (from the caching allocator: calls that overlap have their own)."""
+        key = (fn, args)
+        n = self._sizes.get(key)
+        if n is None:
+            n = self._sizes[key] = int(getattr(load(), fn + "_workspace_size")(self._ref, *args))
+        return torch.empty(n, dtype=torch.uint8, device=self.device) if n else None
+
+    def _need(self, t, name, dtype, shape):
+        _need(t, name, dtype, shape)
+        if t.device != self.device:
+            raise ValueError(f"{name} must be on {self.device}, got {t.device}")
+
+
+def _on(cache, stream):
+    """The cache's device and the stream to launch on, made current: temporaries then belong to it."""
+    if stream is not None:
+        return torch.cuda.stream(stream)
+    if torch.cuda.current_device() != cache.device.index:
+        return torch.cuda.device(cache.device)
+    return _NOTHING
+
+
+def _raw_stream(cache):
+    return torch.cuda.current_stream(cache.device).cuda_stream
+
+
+def _cache(c):
+    if not isinstance(c, PagedCache):
+        raise TypeError("cache must be a PagedCache")
+    return c
+
+
+def kvp_paged_init(cache, stream=None):
+    """Empty the cache: no row holds a page."""
+    with _on(_cache(cache), stream):
+        _check("kvp_paged_init", load().kvp_paged_init(cache._ref, _raw_stream(cache)))
+
+
+def _new_tokens(cache, t, name, like=None):
+    """[R, n_new, D] or [B, h_kv, n_new, D] with a contiguous last axis: (4-d view, strides or None)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != cache.device:
+        raise ValueError(f"{name} must be on {cache.device}, got {t.device}")
+    if t.dim() == 3:
+        t = t.unsqueeze(0)
+    if t.dim() != 4 or t.shape[0] * t.shape[1] != cache.n_rows or t.shape[3] != cache.head_dim:
+        raise ValueError(f"{name} must be [{cache.n_rows}, n_new, {cache.head_dim}] or [batch, h_kv, n_new, "
+                         f"{cache.head_dim}] with batch * h_kv = {cache.n_rows}, got {tuple(t.shape)}")
+    if t.dtype != cache.dtype:
+        raise ValueError(f"{name} must be {cache.dtype}, got {t.dtype}")
+    if like is not None and t.shape != like.shape:
+        raise ValueError(f"{name} must have shape {tuple(like.shape)}, got {tuple(t.shape)}")
+    if t.is_contiguous():
+        return t, None
+    if t.stride(3) != 1:
+        raise ValueError(f"{name}: the head_dim axis must be contiguous")
+    return t, (ctypes.c_int64 * 3)(t.stride(0), t.stride(1), t.stride(2))
+
+
+def kvp_paged_append(cache, new_k, new_v, counts=None, new_pos=None, stream=None):
+    """Append ``counts`` (int32 [R]; None: all) of the new tokens to every row: new_k, new_v
+    [R, n_new, D] or [batch, h_kv, n_new, D] (strided views are read in place).  new_pos int32 [R]:
+    the source position of each row's first new token, for a cache with ``pos``."""
+    k, ks = _new_tokens(_cache(cache), new_k, "new_k")
+    v, vs = _new_tokens(cache, new_v, "new_v", k)
+    if counts is not None:
+        cache._need(counts, "counts", torch.int32, (cache.n_rows,))
+    if new_pos is not None:
+        cache._need(new_pos, "new_pos", torch.int32, (cache.n_rows,))
+    n_new = k.shape[2]
+    with _on(cache, stream):
+        ws = cache._workspace("kvp_paged_append", n_new)
+        rc = load().kvp_paged_append(cache._ref, k.data_ptr(), v.data_ptr(), ks, vs, k.shape[1], n_new,
+                                     None if counts is None else counts.data_ptr(),
+                                     None if new_pos is None else new_pos.data_ptr(),
+                                     None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
+                                     _raw_stream(cache))
+    _check("kvp_paged_append", rc)
+
+
+def kvp_paged_fork(cache, src, copy=False, stream=None):
+    """Give every row r with src[r] >= 0 (int32 [R]) the tokens of row src[r]: on the same pages, or
+    (copy) on fresh ones."""
+    _cache(cache)._need(src, "src", torch.int32, (cache.n_rows,))
+    copy = int(bool(copy))
+    with _on(cache, stream):
+        ws = cache._workspace("kvp_paged_fork", copy)
+        rc = load().kvp_paged_fork(cache._ref, src.data_ptr(), copy, None if ws is None else ws.data_ptr(),
+                                   0 if ws is None else ws.numel(), _raw_stream(cache))
+    _check("kvp_paged_fork", rc)
+
+
+def kvp_paged_compact(cache, idx, count, stream=None):
+    """Keep, in place, the tokens idx [R, b_max] (int32, ascending) of every row, count [R] of them
+    (negative: leave the row), and release the pages that empties."""
+    _cache(cache)._need(idx, "idx", torch.int32, None)
+    if idx.dim() != 2 or idx.shape[0] != cache.n_rows:
+        raise ValueError(f"idx must be [{cache.n_rows}, b_max], got {tuple(idx.shape)}")
+    cache._need(count, "count", torch.int32, (cache.n_rows,))
+    b_max = idx.shape[1]
+    with _on(cache, stream):
+        ws = cache._workspace("kvp_paged_compact", b_max)
+        rc = load().kvp_paged_compact(cache._ref, idx.data_ptr(), count.data_ptr(), b_max,
+                                      None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
+                                      _raw_stream(cache))
+    _check("kvp_paged_compact", rc)
+
+
+def kvp_paged_free(cache, keep=None, stream=None):
+    """Cut every row r to keep[r] tokens (int32 [R]; negative: leave the row; None: empty all rows)."""
+    if keep is not None:
+        _cache(cache)._need(keep, "keep", torch.int32, (cache.n_rows,))
+    with _on(_cache(cache), stream):
+        rc = load().kvp_paged_free(cache._ref, None if keep is None else keep.data_ptr(), _raw_stream(cache))
+    _check("kvp_paged_free", rc)
+
+
+def kvp_paged_decode_attn(q, cache, sm_scale=None, out=None, out_dtype=None, lse=None, return_lse=False,
+                          add_scores=False, workspace=None, stream=None):
+    """One-token attention over the paged rows: q [L, H_q, D] (the layer axis may be strided), rows
+    r = l * h_kv + h -> out [L, H_q, D] float32 (or ``out_dtype`` = the cache's dtype); with
+    ``return_lse`` (out, lse float32 [L, H_q]).  ``add_scores`` adds every token's probability,
+    summed over its group, to ``cache.score``."""
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    if q.device != _cache(cache).device:
+        raise ValueError(f"q must be on {cache.device}, got {q.device}")
+    if q.dim() != 3 or q.dtype != cache.dtype or q.shape[2] != cache.head_dim:
+        raise ValueError(f"q must be {cache.dtype} [n_layers, h_q, {cache.head_dim}], got {q.dtype} {tuple(q.shape)}")
+    L, Hq, D = q.shape
+    if L < 1 or cache.n_rows % L:
+        raise ValueError("the cache's rows must be n_layers * h_kv")
+    if not q.is_contiguous() and (q.stride(2) != 1 or (q.stride(1) != D and Hq > 1)):
+        raise ValueError("q: the head and head_dim axes must be contiguous")
+    q_stride = q.stride(0) if L > 1 else 0
+    if q_stride == 0 and L > 1:
+        raise ValueError("q: the layer axis must not be broadcast")
+    if sm_scale is None:
+        sm_scale = D ** -0.5
+    with _on(cache, stream):
+        if out is None:
+            out = torch.empty(L, Hq, D, dtype=torch.float32 if out_dtype is None else out_dtype, device=cache.device)
+        else:
+            cache._need(out, "out", out_dtype, (L, Hq, D))
+        if out.dtype not in _DTYPE:
+            raise ValueError(f"unsupported out dtype {out.dtype}")
+        if lse is not None:
+            cache._need(lse, "lse", torch.float32, (L, Hq))
+        elif return_lse:
+            lse = torch.empty(L, Hq, dtype=torch.float32, device=cache.device)
+        if workspace is None:
+            workspace = cache._workspace("kvp_paged_decode_attn", Hq, cache.n_rows // L, int(bool(add_scores)))
+        else:
+            cache._need(workspace, "workspace", torch.uint8, None)
+        rc = load().kvp_paged_decode_attn(q.data_ptr(), q_stride, cache._ref, Hq, cache.n_rows // L, float(sm_scale),
+                                          out.data_ptr(), KVP_F32 if out.dtype == torch.float32 else _DTYPE[out.dtype],
+                                          None if lse is None else lse.data_ptr(), int(bool(add_scores)),
+                                          None if workspace is None else workspace.data_ptr(),
+                                          0 if workspace is None else workspace.numel(), _raw_stream(cache))
+    _check("kvp_paged_decode_attn", rc)
+    return (out, lse) if return_lse else out

@@ -25,6 +25,8 @@ Functions and the passages they follow:
 * :func:`fenwick_cutoffs`, :func:`sparse_mask`, :func:`sparse_row_lse` -- KVpop, "Efficient
   Online Pruning", "Fenwick-tree cut-off computation (Algorithm 2)" and "Delayed Memory
   Scoring" (the sparse log-normalisers).
+* :mod:`oracle.paged` -- LKV, "LKV-H" and How much KV cache can you prune, "Conclusion" (rows of
+  different budgets on one pool of pages).
 * :func:`soft_topk`, :func:`head_budgets` -- LKV, "The Differentiable Soft-TopK
   Operator" and "LKV-H".
 
@@ -32,6 +34,7 @@ Every function is pinned by the ``-m "not gpu"`` tests (brute force through
 library softmax/logsumexp on tiny inputs, closed forms, invariants and the
 pages' worked examples).
 """
+from . import paged
 from .attention_mass import future_attn_mass, future_attn_mass_per_head, kvpop_target, row_lse
 from .budgets import head_budgets, soft_topk
 from .decode import decode_attn
@@ -45,5 +48,5 @@ __all__ = [
     "row_lse", "future_attn_mass", "future_attn_mass_per_head", "kvpop_target", "select_topk", "select_row", "effective_budget",
     "compact_kv", "decode_attn", "soft_topk", "head_budgets", "ring_insert", "ring_victim",
     "fenwick_cutoffs", "sparse_mask", "sparse_row_lse", "chunk_compress_step", "chunked_prefill_compress",
-    "rank_by_scores", "eviction_cost_curve", "eviction_auc", "optimal_auc", "normalized_auc",
+    "paged", "rank_by_scores", "eviction_cost_curve", "eviction_auc", "optimal_auc", "normalized_auc",
 ]
