@@ -501,7 +501,8 @@ typedef struct kvp_paged_cache {
 /* An empty cache: table -1, lens and refs 0, every page free. */
 int kvp_paged_init(const kvp_paged_cache* cache, kvp_stream_t stream);
 
-/* Append counts[r] (NULL: n_new) tokens to every row; 0 <= counts[r] <= n_new.
+/* Append counts[r] (NULL: n_new) tokens to every row; 0 <= counts[r] <= n_new,
+ * n_rows * n_new < 2^31.
  * new_k, new_v [n_rows / h_kv, h_kv, n_new, head_dim] dtype with element strides
  * {batch, head, token} in the HOST arrays k_strides / v_strides (NULL = dense; a
  * slice of a fused QKV projection is read in place).  A partly filled last page
@@ -544,7 +545,8 @@ int kvp_paged_free(const kvp_paged_cache* cache, const int32_t* keep, kvp_stream
  *   lse[l, h]    = ln sum_{t < lens[r]} exp(sm_scale * q[l, h] . k_t)
  *
  * q [n_layers, h_q, head_dim] dtype, q_stride elements from layer to layer (0 =
- * dense; multiple of 16 bytes); out [n_layers, h_q, head_dim] of out_dtype
+ * dense; multiple of 16 bytes); sm_scale is a double (1 / sqrt(128) is no float, and
+ * its rounding is the same for every logit of a row, so it does not average out); out [n_layers, h_q, head_dim] of out_dtype
  * (KVP_F32 or the cache's dtype); lse [n_layers, h_q] float32 or NULL.  An empty
  * row gives out 0 and lse -inf.  add_scores = 1 adds every token's probability,
  * summed over the group's query heads, to cache->score.  G = h_q / h_kv <= 16.
@@ -555,7 +557,7 @@ int kvp_paged_free(const kvp_paged_cache* cache, const int32_t* keep, kvp_stream
 size_t kvp_paged_decode_attn_workspace_size(const kvp_paged_cache* cache, int h_q, int h_kv,
                                             int add_scores);
 int kvp_paged_decode_attn(const void* q, int64_t q_stride, const kvp_paged_cache* cache, int h_q,
-                          int h_kv, float sm_scale, void* out, int out_dtype, float* lse,
+                          int h_kv, double sm_scale, void* out, int out_dtype, float* lse,
                           int add_scores, void* workspace, size_t workspace_bytes,
                           kvp_stream_t stream);
 

@@ -718,6 +718,8 @@ int kvp_paged_append(const kvp_paged_cache* cache, const void* new_k, const void
   if (!new_k || !new_v) return fail(KVP_ERR_INVALID_ARG, "null new_k/new_v");
   if (!aligned16(new_k) || !aligned16(new_v)) return fail(KVP_ERR_INVALID_ARG, "new_k/new_v not 16-byte aligned");
   if (n_new < 1 || n_new > v.cap) return fail(KVP_ERR_INVALID_ARG, "n_new=%d outside [1, %d]", n_new, v.cap);
+  if ((long long)n_new * v.R > 0x7fffffffLL)
+    return fail(KVP_ERR_INVALID_ARG, "n_rows=%d * n_new=%d tokens in one call (append fewer rows at a time)", v.R, n_new);
   if (h_kv < 1 || v.R % h_kv) return fail(KVP_ERR_INVALID_ARG, "n_rows=%d not a multiple of h_kv=%d", v.R, h_kv);
   if (new_pos && !v.pos) return fail(KVP_ERR_INVALID_ARG, "new_pos given, but the cache has no pos");
   kvp::PagedNew a{};
@@ -798,7 +800,7 @@ size_t kvp_paged_decode_attn_workspace_size(const kvp_paged_cache* cache, int h_
 }
 
 int kvp_paged_decode_attn(const void* q, int64_t q_stride, const kvp_paged_cache* cache, int h_q,
-                          int h_kv, float sm_scale, void* out, int out_dtype, float* lse,
+                          int h_kv, double sm_scale, void* out, int out_dtype, float* lse,
                           int add_scores, void* workspace, size_t workspace_bytes,
                           kvp_stream_t stream) {
   g_last_error.clear();

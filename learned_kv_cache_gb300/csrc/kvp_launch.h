@@ -215,7 +215,7 @@ struct PagedDecodeArgs {
   const void* q;
   int64_t q_stride;
   int h_q, h_kv;
-  float scale;
+  double scale;
   void* out;
   int out_f32;
   float* lse;

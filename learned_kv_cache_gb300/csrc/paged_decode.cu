@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(PD_WARPS * 32) paged_decode_kernel(const T* __
           for (int t = 0; t < EV; ++t) a = fmaf(qf[h][t], kf[t], a);
 #pragma unroll
           for (int off = LPK / 2; off > 0; off >>= 1) a += __shfl_xor_sync(0xffffffffu, a, off);
-          a *= p.c2;
+          a = paged::base2(p, a);
           if (!ok[s]) continue;
           if (p.logits && dl == 0) p.logits[((size_t)r * c.cap + m) * GP + h] = a;
           if (a > mx[h]) {
@@ -285,9 +285,14 @@ size_t layout(const PagedView& c, int G, int add_scores, Params* p, void* ws) {
 
 template <typename T, int D, int GP>
 cudaError_t run(const Params& p, const PagedDecodeArgs& a, cudaStream_t st) {
-  count_launches(1);
-  cudaError_t e = launch_with_pdl(paged_decode_kernel<T, D, GP>, dim3((unsigned)p.ctas), dim3(PD_WARPS * 32), 0, st,
-                                  (const T*)a.q, p);
+  cudaError_t e;
+  if constexpr (sizeof(T) == 2) {
+    e = launch_paged_decode_mma(p, a.q, st);
+  } else {
+    count_launches(1);
+    e = launch_with_pdl(paged_decode_kernel<T, D, GP>, dim3((unsigned)p.ctas), dim3(PD_WARPS * 32), 0, st,
+                        (const T*)a.q, p);
+  }
   if (e != cudaSuccess) return e;
   // a row of one tile is never shared, and without scores nothing is left to do
   if (!a.add_scores && p.c.cap <= TILE) return cudaSuccess;
@@ -312,7 +317,9 @@ cudaError_t launch_paged_decode(const PagedView& c, const PagedDecodeArgs& a, vo
   p.Hkv = a.h_kv;
   p.G = a.h_q / a.h_kv;
   p.q_stride = a.q_stride;
-  p.c2 = a.scale * KVP_LOG2E;
+  const double c2 = a.scale * 1.4426950408889634;
+  p.c2 = (float)c2;
+  p.c2_low = (float)(c2 - (double)p.c2);
   p.out = a.out;
   p.out_f32 = a.out_f32;
   p.lse = a.lse;

@@ -9,6 +9,8 @@
 // kernel merges in CTA order, so results do not depend on timing.
 #pragma once
 
+#include <type_traits>
+
 #include "kvp_common.cuh"
 #include "kvp_launch.h"
 
@@ -30,7 +32,7 @@ struct Params {
   PagedView c;
   int G, Hq, Hkv;
   int64_t q_stride;
-  float c2;              // scale * log2 e
+  float c2, c2_low;      // scale * log2 e, and what the float leaves of it
   int ctas;              // launched
   float* part;           // [ctas][2][pstride]: m[GP], l[GP], o[GP][D]; slot 0: the row began in an
   int pstride;           //   earlier CTA, slot 1: it goes on in the next one
@@ -47,6 +49,9 @@ __device__ __forceinline__ int row_len(const Params& p, int r) {
   const int n = p.c.lens[r];
   return n < 0 ? 0 : (n > p.c.cap ? p.c.cap : n);
 }
+// Base-2 logit of a dot product, with one rounding: a long row's weights differ by powers of e, and an
+// error of the factor common to all logits grows with their difference.
+__device__ __forceinline__ float base2(const Params& p, float s) { return fmaf(s, p.c2, s * p.c2_low); }
 __device__ __forceinline__ int tiles_of(int n) { return (n + TILE - 1) / TILE; }
 
 __device__ __forceinline__ int cta_begin(int c, int total, int active) {
@@ -125,4 +130,8 @@ __device__ __forceinline__ void empty_rows(const Params& p, int cta) {
 }
 
 }  // namespace paged
+
+// The tensor-core path of bf16 / f16 caches (paged_decode_mma.cu).
+cudaError_t launch_paged_decode_mma(const paged::Params& p, const void* q, cudaStream_t st);
+
 }  // namespace kvp

@@ -6,10 +6,11 @@
 //
 // Which page a row gets must not depend on the order in which threads run, so pages are not taken
 // with atomics: the needs of the rows are summed in row order, the free pages enumerated in
-// ascending order (a bit per page, so 32768 pages are 4 KB), and the i-th need gets the i-th free
-// page.  One cluster does that ("plan": needs in parallel, the two scans in its first CTA, the books
-// in parallel again, cluster barriers between); the tokens then move in a kernel of their own, which
-// fills the GPU.  References are counted with integer atomics, whose order changes nothing.
+// ascending order (a bit per page, so 131072 pages are 16 KB), and the i-th need gets the i-th free
+// page.  One CTA does that (the "plan"): it is a chain of dependent reads and two block scans, and
+// the rows' and pages' numbers go straight from registers into them.  What is wide -- tokens, table
+// entries, counts of the pages taken -- is left to the kernel behind it, which fills the GPU.
+// References are counted with integer atomics, whose order changes nothing.
 #include <cooperative_groups.h>
 
 #include "kvp_common.cuh"
@@ -20,8 +21,8 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int PLAN_THREADS = 512;
-constexpr int PLAN_CTAS = 8;               // the portable cluster size
+constexpr int PLAN_THREADS = 1024;
+constexpr int PLAN_WORDS = 4;              // words of the free mask per thread and step
 
 enum { PLAN_APPEND = 0, PLAN_COPY = 1, PLAN_COMPACT = 2 };
 
@@ -41,7 +42,7 @@ struct PlanArgs {
   int32_t* tail;         // [R] append: the shared tail page that is copied, or -1
   int32_t* list;         // the pages taken, ascending
   int32_t* owner;        // copy: the row of each page in list
-  int32_t* dmap;         // compact: [R, W] page of each kept page
+  int32_t* dmap;         // compact: [R, W] the page itself, or -2 - i: the row's i-th page of list
   int32_t* used;         // [1] pages taken
   int* status;
 };
@@ -66,30 +67,33 @@ __device__ __forceinline__ void release_page(const PagedView& c, int p, int* sta
   }
 }
 
-// Pages row r needs, and what the later phases have to know of it.
+// What the plan finds out about a row: the pages it needs, and what the kernel behind it has to know.
+struct RowPlan {
+  int start, need, tail, cnt;
+};
+
 template <int MODE>
-__device__ __forceinline__ void row_need(const PagedView& c, const PlanArgs& a, int r) {
-  int start = -1, need = 0;
+__device__ __forceinline__ RowPlan row_plan(const PagedView& c, const PlanArgs& a, int r) {
+  RowPlan w{-1, 0, -1, 0};
   if (MODE == PLAN_APPEND) {
-    const int n = c.lens[r], cnt = a.counts ? a.counts[r] : a.n_new;
-    int tail = -1;
-    bool ok = n >= 0 && n <= c.cap && cnt >= 0 && cnt <= a.n_new && cnt <= c.cap - n;
-    if (ok && cnt > 0) {
+    const int n = c.lens[r];
+    w.cnt = a.counts ? a.counts[r] : a.n_new;
+    bool ok = n >= 0 && n <= c.cap && w.cnt >= 0 && w.cnt <= a.n_new && w.cnt <= c.cap - n;
+    if (ok && w.cnt > 0) {
       int first = pages_of(n, c);
       if (n & (c.ps - 1)) {
         const int p = table_row(c, r)[n >> c.shift];
         ok = page_ok(p, c);
         if (ok && c.refs[p] > 1) {
-          tail = p;
+          w.tail = p;
           first = n >> c.shift;
         }
       }
       if (ok) {
-        start = n;
-        need = pages_of(n + cnt, c) - first;
+        w.start = n;
+        w.need = pages_of(n + w.cnt, c) - first;
       }
     }
-    a.tail[r] = tail;
     if (!ok) raise_status(a.status, KVP_ERR_DEVICE_CHECK);
   } else if (MODE == PLAN_COPY) {
     const int s = a.src[r];
@@ -99,203 +103,241 @@ __device__ __forceinline__ void row_need(const PagedView& c, const PlanArgs& a, 
       if (n < 0 || n > c.cap) {
         raise_status(a.status, KVP_ERR_DEVICE_CHECK);
       } else if (n > 0) {
-        start = n;
-        need = pages_of(n, c);
+        w.start = n;
+        w.need = pages_of(n, c);
       }
     }
+  } else {                                   // compact_need_kernel has been here
+    w.start = a.start[r];
+    w.need = a.need[r];
   }
-  a.start[r] = start;
-  a.need[r] = need;
+  return w;
 }
 
-// The kept pages of row r: -2 where a fresh page is needed (the tokens change and somebody else
-// holds the page), else the page the row has there.
-__device__ __forceinline__ void compact_page(const PagedView& c, const PlanArgs& a, long long e) {
-  const int r = (int)(e / a.W), j = (int)(e % a.W);
-  const int cnt = a.count[r];
-  int d = -1;
-  if (cnt > 0 && cnt <= a.b_max && cnt <= c.lens[r] && c.lens[r] <= c.cap && j < pages_of(cnt, c)) {
-    const int p = table_row(c, r)[j];
-    if (page_ok(p, c)) {
-      const int last = min((j + 1) << c.shift, cnt) - 1;   // ascending indices: all before it moved too, or none
-      d = (c.refs[p] > 1 && a.idx[(size_t)r * a.b_max + last] != last) ? -2 : p;
-    } else {
-      raise_status(a.status, KVP_ERR_DEVICE_CHECK);
+// Which of a row's kept pages have to be fresh ones: those whose tokens change and that somebody
+// else holds too.  One CTA per row.
+constexpr int NEED_THREADS = 128;
+
+__global__ void __launch_bounds__(NEED_THREADS) compact_need_kernel(const PagedView c, const PlanArgs a) {
+  __shared__ int scan_sh[33];
+  wait_prior_grid();
+  const int r = blockIdx.x, tid = threadIdx.x;
+  const int cnt = a.count[r], n = c.lens[r];
+  const bool ok = n >= 0 && n <= c.cap && cnt <= n && cnt <= a.b_max;
+  int need = 0;
+  const int pages = ok && cnt > 0 ? pages_of(cnt, c) : 0;
+  for (int j0 = 0; j0 < pages; j0 += NEED_THREADS) {
+    const int j = j0 + tid;
+    int d = -1;
+    if (j < pages) {
+      const int p = table_row(c, r)[j];
+      const int last = min((j + 1) << c.shift, cnt) - 1;   // ascending indices: if it stays, so do all before it
+      const bool moved = a.idx[(size_t)r * a.b_max + last] != last;
+      if (page_ok(p, c)) d = moved && c.refs[p] > 1 ? -2 : p;
+      else raise_status(a.status, KVP_ERR_DEVICE_CHECK);
     }
+    int all;
+    const int before = block_exclusive_scan(d == -2, scan_sh, &all);
+    if (j < pages) a.dmap[(size_t)r * a.W + j] = d == -2 ? -2 - (need + before) : d;
+    need += all;
   }
-  a.dmap[e] = d;
+  if (tid == 0) {
+    if (!ok) raise_status(a.status, KVP_ERR_DEVICE_CHECK);
+    a.start[r] = ok && cnt >= 0 ? cnt : -1;
+    a.need[r] = need;
+  }
 }
 
+// The plan.  A thread has a row (several in turn above 1024 rows) and PLAN_WORDS words of the mask.
 template <int MODE>
 __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const PagedView c, const PlanArgs a) {
-  cg::cluster_group cluster = cg::this_cluster();
-  const int rank = (int)cluster.block_rank(), nranks = (int)cluster.num_blocks();
-  const int tid = threadIdx.x, gid = rank * PLAN_THREADS + tid, total = nranks * PLAN_THREADS;
-  const int lane = tid & 31, gwarp = gid >> 5, nwarps = total >> 5;
   __shared__ int scan_sh[33];
   __shared__ int used_sh;
+  wait_prior_grid();
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int words = (c.n_pages + 31) >> 5;
+  const bool one = c.R <= PLAN_THREADS;      // every row stays in its thread's registers
+  // the first words are on their way while the rows are looked at
+  uint32_t mask[PLAN_WORDS];
+#pragma unroll
+  for (int k = 0; k < PLAN_WORDS; ++k) mask[k] = PLAN_WORDS * tid + k < words ? c.free_mask[PLAN_WORDS * tid + k] : 0u;
+  if (tid == 0) used_sh = 0;
 
-  // -- needs
-  if (MODE == PLAN_COMPACT) {
-    const long long items = (long long)c.R * a.W;
-    for (long long e = gid; e < items; e += total) compact_page(c, a, e);
-    cluster.sync();
-    for (int r = gwarp; r < c.R; r += nwarps) {
-      const int cnt = a.count[r], n = c.lens[r];
-      const bool ok = n >= 0 && n <= c.cap && cnt <= n && cnt <= a.b_max;
-      int need = 0;
-      if (ok && cnt > 0)
-        for (int j = lane; j < pages_of(cnt, c); j += 32) need += a.dmap[(size_t)r * a.W + j] == -2;
-      need = __reduce_add_sync(0xffffffffu, need);
-      if (lane == 0) {
-        if (!ok) raise_status(a.status, KVP_ERR_DEVICE_CHECK);
-        a.start[r] = ok && cnt >= 0 ? cnt : -1;
-        a.need[r] = need;
+  RowPlan w{-1, 0, -1, 0};
+  int off = 0, want = 0;
+  for (int base = 0; base < c.R; base += PLAN_THREADS) {
+    const int r = base + tid;
+    w = r < c.R ? row_plan<MODE>(c, a, r) : RowPlan{-1, 0, -1, 0};
+    int all;
+    off = want + block_exclusive_scan(w.need, scan_sh, &all);
+    want += all;
+    if (r < c.R) {
+      a.off[r] = off;
+      if (MODE != PLAN_COMPACT && !one) {
+        a.start[r] = w.start;
+        a.need[r] = w.need;
+        if (MODE == PLAN_APPEND) a.tail[r] = w.tail;
       }
     }
-  } else {
-    for (int r = gid; r < c.R; r += total) row_need<MODE>(c, a, r);
   }
-  cluster.sync();
 
-  // -- which pages: two scans, in the first CTA
-  if (rank == 0) {
-    int want = 0;
-    for (int base = 0; base < c.R; base += PLAN_THREADS) {
-      const int r = base + tid;
-      int all;
-      const int before = block_exclusive_scan(r < c.R ? a.need[r] : 0, scan_sh, &all);
-      if (r < c.R) a.off[r] = want + before;
-      want += all;
-    }
-    int found = 0;
-    const int words = (c.n_pages + 31) >> 5;
-    for (int base = 0; base < words && found < want; base += 4 * PLAN_THREADS) {
-      uint32_t m[4];
-      int mine = 0;
+  // the lowest free pages, in order, out of the mask and into the list
+  int found = 0;
+  for (int base = 0; base < words && found < want; base += PLAN_WORDS * PLAN_THREADS) {
+    int mine = 0;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int w = base + 4 * tid + k;
-        m[k] = w < words ? c.free_mask[w] : 0u;
-        mine += __popc(m[k]);
+    for (int k = 0; k < PLAN_WORDS; ++k) {
+      const int x = base + PLAN_WORDS * tid + k;
+      if (base > 0) mask[k] = x < words ? c.free_mask[x] : 0u;
+      mine += __popc(mask[k]);
+    }
+    int all;
+    int at = found + block_exclusive_scan(mine, scan_sh, &all);
+#pragma unroll
+    for (int k = 0; k < PLAN_WORDS; ++k) {
+      const int x = base + PLAN_WORDS * tid + k;
+      uint32_t v = mask[k];
+      for (; v && at < want; v &= v - 1, ++at) a.list[at] = x * 32 + __ffs(v) - 1;
+      if (v != mask[k]) c.free_mask[x] = v;
+    }
+    found += all;
+  }
+  found = min(found, want);
+
+  // rows whose pages run past the free ones are left alone; the others have them
+  __syncthreads();
+  int used = 0;
+  for (int base = 0; base < c.R; base += PLAN_THREADS) {
+    const int r = base + tid;
+    if (r < c.R) {
+      if (!one) {
+        off = a.off[r];
+        w.start = a.start[r];
+        w.need = a.need[r];
+        if (MODE == PLAN_APPEND) {
+          w.tail = a.tail[r];
+          w.cnt = a.counts ? a.counts[r] : a.n_new;
+        }
       }
-      int all;
-      int at = found + block_exclusive_scan(mine, scan_sh, &all);
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        for (uint32_t v = m[k]; v && at < want; v &= v - 1, ++at)
-          a.list[at] = (base + 4 * tid + k) * 32 + __ffs(v) - 1;
-      found += all;
-    }
-    // rows whose pages run past the free ones are left alone; the pages of the others are taken
-    if (tid == 0) used_sh = 0;
-    __syncthreads();
-    int used = 0;
-    for (int r = tid; r < c.R; r += PLAN_THREADS) {
-      const int need = a.need[r];
-      if (need == 0) continue;
-      if (a.off[r] + need <= found) {
-        used = max(used, a.off[r] + need);
-      } else {
-        a.start[r] = -1;
+      if (w.need > 0 && off + w.need > found) {
+        w.start = -1;
+        w.need = 0;
         raise_status(a.status, KVP_ERR_DEVICE_CHECK);
       }
-    }
-    used = __reduce_max_sync(0xffffffffu, used);
-    if (lane == 0 && used > 0) atomicMax(&used_sh, used);
-    __syncthreads();
-    if (tid == 0) *a.used = used_sh;
-  }
-  cluster.sync();
-
-  // -- the books
-  const int used = *reinterpret_cast<volatile int32_t*>(a.used);
-  for (int i = gid; i < used; i += total) {
-    const int p = a.list[i];
-    c.refs[p] = 1;
-    if (i == 0 || (a.list[i - 1] >> 5) != (p >> 5)) {      // the first page of its word clears the word's bits
-      uint32_t m = 0;
-      for (int k = i; k < used && (a.list[k] >> 5) == (p >> 5); ++k) m |= 1u << (a.list[k] & 31);
-      atomicAnd(c.free_mask + (p >> 5), ~m);
-    }
-  }
-  for (int r = gwarp; r < c.R; r += nwarps) {
-    const int start = a.start[r];
-    if (start < 0) continue;
-    const int need = a.need[r], off = a.off[r];
-    if (MODE == PLAN_APPEND) {
-      const int tail = a.tail[r];
-      const int first = tail >= 0 ? start >> c.shift : pages_of(start, c);
-      for (int k = lane; k < need; k += 32) table_row(c, r)[first + k] = a.list[off + k];
-      if (lane == 0) {
-        c.lens[r] = start + (a.counts ? a.counts[r] : a.n_new);
-        if (tail >= 0) release_page(c, tail, a.status);
+      if (w.need > 0) used = max(used, off + w.need);
+      a.start[r] = w.start;
+      if (MODE == PLAN_APPEND) {
+        a.tail[r] = w.tail;
+        if (w.start >= 0) {
+          c.lens[r] = w.start + w.cnt;
+          if (w.tail >= 0) release_page(c, w.tail, a.status);   // its tokens are copied before anyone can take it
+        }
+      } else if (MODE == PLAN_COPY && w.start >= 0) {
+        c.lens[r] = w.start;
       }
-    } else if (MODE == PLAN_COPY) {
-      for (int k = lane; k < need; k += 32) {
-        table_row(c, r)[k] = a.list[off + k];
-        a.owner[off + k] = r;
-      }
-      if (lane == 0) c.lens[r] = start;
-    } else if (need > 0) {
-      int taken = 0;
-      for (int j0 = 0; j0 < pages_of(start, c); j0 += 32) {
-        const int j = j0 + lane;
-        int32_t* d = a.dmap + (size_t)r * a.W + j;
-        const bool fresh = j < pages_of(start, c) && *d == -2;
-        const uint32_t b = __ballot_sync(0xffffffffu, fresh);
-        if (fresh) *d = a.list[off + taken + __popc(b & ((1u << lane) - 1u))];
-        taken += __popc(b);
+    }
+    if (MODE == PLAN_COPY) {                 // the owner of each page, a warp per row
+      for (int i = 0; i < 32; ++i) {
+        const int need = __shfl_sync(0xffffffffu, r < c.R ? w.need : 0, i), o = __shfl_sync(0xffffffffu, off, i);
+        for (int k = lane; k < need; k += 32) a.owner[o + k] = base + (tid & ~31) + i;
       }
     }
   }
+  used = __reduce_max_sync(0xffffffffu, used);
+  if (lane == 0 && used > 0) atomicMax(&used_sh, used);
+  __syncthreads();
+  used = used_sh;
+  if (tid == 0) *a.used = used;
+  // pages that were found for a row that was left alone go back
+  for (int i = used + tid; i < found; i += PLAN_THREADS) atomicOr(c.free_mask + (a.list[i] >> 5), 1u << (a.list[i] & 31));
 }
 
 // ------------------------------------------------------------------ moving tokens
 // 16-byte vectors throughout: VPR of them make one token's K (or V); consecutive threads take
 // consecutive vectors of a token.
 
+// Division by a number that the launch fixes: q = (x * mul) >> (32 + shift), exact for x < 2^31.
+struct FastDiv {
+  uint32_t mul, shift, by;
+};
+FastDiv fast_div(uint32_t by) {
+  FastDiv d{0, 0, by};
+  if (by == 1) return d;                     // handled apart: the multiplier would need 33 bits
+  while ((1u << d.shift) < by) ++d.shift;    // 2^(shift-1) < by <= 2^shift
+  --d.shift;
+  d.mul = (uint32_t)(((1ull << (32 + d.shift)) + by - 1) / by);
+  return d;
+}
+__device__ __forceinline__ uint32_t div_by(uint32_t x, const FastDiv& d) {
+  return d.by == 1 ? x : __umulhi(x, d.mul) >> d.shift;
+}
+
+// New tokens to their slots, and the books of the pages taken for them: a page's entry and count are
+// written by the thread of the first new token in it.  Each thread has four vectors of K and of V in
+// flight.
+constexpr int AC_UNROLL = 4;
+
 template <int VPR>
 __global__ void __launch_bounds__(256) append_copy_kernel(const PagedView c, const PagedNew a, const PlanArgs w,
-                                                          int elt) {
+                                                          int elt, FastDiv by_new, FastDiv by_heads, long long tokens) {
   wait_prior_grid();
   const int64_t ts = c.token_stride * elt, pgs = c.page_stride * elt;
-  char* pool[2] = {(char*)c.k, (char*)c.v};
-  const long long stride = (long long)gridDim.x * blockDim.x;
-  const long long gid = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-  const long long items = (long long)c.R * a.n_new * VPR;
-  for (long long e = gid; e < items; e += stride) {
-    const int v = (int)(e % VPR);
-    const long long ri = e / VPR;
-    const int r = (int)(ri / a.n_new), i = (int)(ri % a.n_new);
-    const int start = w.start[r];
-    if (start < 0 || i >= (a.counts ? a.counts[r] : a.n_new)) continue;
-    const int t = start + i, b = r / a.h_kv, h = r % a.h_kv;
-    const int p = table_row(c, r)[t >> c.shift];
-    if (!page_ok(p, c)) continue;
-    const int64_t to = p * pgs + (t & (c.ps - 1)) * ts + v * 16;
-    const uint4 k = ld_stream16((const char*)a.k + (b * a.ks[0] + h * a.ks[1] + i * a.ks[2]) * elt + v * 16);
-    const uint4 x = ld_stream16((const char*)a.v + (b * a.vs[0] + h * a.vs[1] + i * a.vs[2]) * elt + v * 16);
-    *reinterpret_cast<uint4*>(pool[0] + to) = k;
-    *reinterpret_cast<uint4*>(pool[1] + to) = x;
-    if (v == 0) {
-      if (c.score) c.score[(size_t)r * c.cap + t] = 0.f;
-      if (c.pos) c.pos[(size_t)r * c.cap + t] = a.pos ? a.pos[r] + i : t;
+  char* pk = (char*)c.k;
+  char* pv = (char*)c.v;
+  constexpr int TOK = 256 / VPR;             // tokens per CTA and pass
+  const int v = threadIdx.x % VPR;
+  const long long step = (long long)gridDim.x * TOK;
+  for (long long x0 = (long long)blockIdx.x * TOK + threadIdx.x / VPR; x0 < tokens; x0 += step * AC_UNROLL) {
+    uint4 k[AC_UNROLL], y[AC_UNROLL];
+    int row[AC_UNROLL], tok[AC_UNROLL];
+#pragma unroll
+    for (int u = 0; u < AC_UNROLL; ++u) {
+      const long long x = x0 + u * step;
+      row[u] = -1;
+      if (x >= tokens) continue;
+      const int r = (int)div_by((uint32_t)x, by_new), i = (int)((uint32_t)x - (uint32_t)r * by_new.by);
+      if (i >= (a.counts ? a.counts[r] : a.n_new)) continue;
+      const int b = (int)div_by((uint32_t)r, by_heads), h = r - b * a.h_kv;
+      row[u] = r;
+      tok[u] = i;
+      k[u] = ld_stream16((const char*)a.k + (b * a.ks[0] + h * a.ks[1] + i * a.ks[2]) * elt + v * 16);
+      y[u] = ld_stream16((const char*)a.v + (b * a.vs[0] + h * a.vs[1] + i * a.vs[2]) * elt + v * 16);
+    }
+#pragma unroll
+    for (int u = 0; u < AC_UNROLL; ++u) {
+      const int r = row[u], i = tok[u];
+      if (r < 0) continue;
+      const int start = w.start[r];
+      if (start < 0) continue;
+      const int t = start + i, j = t >> c.shift, o = t & (c.ps - 1);
+      const int first = w.tail[r] >= 0 ? start >> c.shift : pages_of(start, c);
+      const int p = j >= first ? w.list[w.off[r] + j - first] : table_row(c, r)[j];
+      if (!page_ok(p, c)) continue;
+      const int64_t to = p * pgs + o * ts + v * 16;
+      *reinterpret_cast<uint4*>(pk + to) = k[u];
+      *reinterpret_cast<uint4*>(pv + to) = y[u];
+      if (v == 0) {
+        if (j >= first && (i == 0 || o == 0)) {
+          table_row(c, r)[j] = p;
+          c.refs[p] = 1;
+        }
+        if (c.score) c.score[(size_t)r * c.cap + t] = 0.f;
+        if (c.pos) c.pos[(size_t)r * c.cap + t] = a.pos ? a.pos[r] + i : t;
+      }
     }
   }
-  // tokens of shared tail pages, to the pages that replace them
-  const long long tails = (long long)c.R * c.ps * VPR;
-  for (long long e = gid; e < tails; e += stride) {
-    const int v = (int)(e % VPR);
-    const long long ro = e / VPR;
-    const int r = (int)(ro >> c.shift), o = (int)(ro & (c.ps - 1));
-    const int start = w.start[r], from = w.tail[r];
-    if (start < 0 || from < 0 || o >= (start & (c.ps - 1))) continue;
-    const int p = table_row(c, r)[start >> c.shift];
-    const int64_t at = o * ts + v * 16;
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-      *reinterpret_cast<uint4*>(pool[x] + p * pgs + at) = *reinterpret_cast<const uint4*>(pool[x] + from * pgs + at);
+  // tokens of shared tail pages, to the pages that replace them: a CTA per row
+  for (int r = blockIdx.x; r < c.R; r += gridDim.x) {
+    const int from = w.tail[r], start = w.start[r];
+    if (start < 0 || from < 0) continue;
+    const int p = w.list[w.off[r]], n = (start & (c.ps - 1)) * VPR;
+    for (int e = threadIdx.x; e < n; e += 256) {
+      const int64_t at = (e / VPR) * ts + (e % VPR) * 16;
+      const uint4 x = *reinterpret_cast<const uint4*>(pk + from * pgs + at);
+      const uint4 z = *reinterpret_cast<const uint4*>(pv + from * pgs + at);
+      *reinterpret_cast<uint4*>(pk + p * pgs + at) = x;
+      *reinterpret_cast<uint4*>(pv + p * pgs + at) = z;
+    }
   }
 }
 
@@ -308,6 +350,10 @@ __global__ void __launch_bounds__(256) pages_copy_kernel(const PagedView c, cons
   for (int i = blockIdx.x; i < used; i += gridDim.x) {
     const int r = w.owner[i], s = w.src[r], k = i - w.off[r];
     const int from = table_row(c, s)[k], to = w.list[i];
+    if (threadIdx.x == 0) {
+      c.table[(size_t)r * c.max_pages + k] = to;
+      c.refs[to] = 1;
+    }
     if (!page_ok(from, c)) {
       if (threadIdx.x == 0) raise_status(w.status, KVP_ERR_DEVICE_CHECK);
       continue;
@@ -328,78 +374,158 @@ __global__ void __launch_bounds__(256) pages_copy_kernel(const PagedView c, cons
   }
 }
 
-// Kept tokens of one row, in place.  idx is ascending, so idx[m] >= m: once every load of the
-// tokens below some m has landed, the slots below m are written without touching a token that is
-// still to be read.  A chunk of tokens is therefore read by the whole CTA, a barrier, then written;
-// the columns of a token (16-byte vectors of K and of V) do not depend on each other, so a cluster
-// of CTAs shares a row by columns.  At the end the cluster gives the row its new pages.
-constexpr int CC_THREADS = 256;
-constexpr int CC_UNROLL = 4;
+// Kept tokens of one row, in place.  idx is ascending, so idx[m] >= m: once every load of the tokens
+// up to some m has landed, the slots up to m can be written without touching a token that is still
+// to be read, and the loads of later tokens may be under way at any time.  So chunks of tokens stream
+// through a ring in shared memory (cp.async), written in order, one barrier per chunk: loads of
+// CP_STAGES - 1 chunks are in flight while one is stored.  Where a token lies takes two dependent reads
+// (index, table); they run two chunks ahead of the copies, in registers.  The columns of a token
+// (16-byte vectors of K and of V) do not depend on each other, so a cluster of CTAs shares a row by
+// columns.  At the end the cluster gives the row its new pages.
+constexpr int CP_THREADS = 256;
+constexpr int CP_TOK = 128;                // tokens per chunk: a thread of each half of the CTA looks one up
+constexpr int CP_STAGES = 4;
 
 template <int VPS>   // 16-byte vectors of a token per CTA
-__global__ void __launch_bounds__(CC_THREADS) compact_pages_kernel(const PagedView c, const PlanArgs w, int elt,
+struct Cp {
+  static constexpr int STAGE = CP_TOK * VPS * 16;
+  static constexpr int SLOTS = CP_STAGES + 2;              // chunks whose places are kept
+  static constexpr int OFF_FROM = CP_STAGES * STAGE;       // int64 [SLOTS][CP_TOK] source and target offsets
+  static constexpr int OFF_TO = OFF_FROM + SLOTS * CP_TOK * 8;
+  static constexpr int OFF_SIDE = OFF_TO + SLOTS * CP_TOK * 8;   // [CP_STAGES][CP_TOK] 4 bytes
+  static constexpr int SMEM = OFF_SIDE + CP_STAGES * CP_TOK * 4;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(__cvta_generic_to_global(src)) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(__cvta_generic_to_global(src)) : "memory");
+}
+
+template <int VPS>
+__global__ void __launch_bounds__(CP_THREADS) compact_pages_kernel(const PagedView c, const PlanArgs w, int elt,
                                                                   int per_tensor) {
+  using C = Cp<VPS>;
+  extern __shared__ __align__(16) uint8_t smem[];
   wait_prior_grid();
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank(), nranks = (int)cluster.num_blocks();
   const int r = blockIdx.x / nranks, tid = threadIdx.x;
   const int cnt = w.start[r];
   if (cnt < 0) return;                       // the whole cluster
-  const int n = c.lens[r];
+  const int n = c.lens[r], off = w.off[r];
   const int64_t ts = c.token_stride * elt, pgs = c.page_stride * elt;
-  constexpr int TOK = CC_THREADS / VPS;      // tokens per pass
-  char* base = (char*)(rank < per_tensor ? c.k : c.v) + (rank % per_tensor) * VPS * 16 + (tid % VPS) * 16;
+  char* base = (char*)(rank < per_tensor ? c.k : c.v) + (rank % per_tensor) * VPS * 16;
   const int32_t* idx = w.idx + (size_t)r * w.b_max;
   const int32_t* dmap = w.dmap + (size_t)r * w.W;
   const int32_t* table = table_row(c, r);
-  float* side = rank == 0 ? c.score : nullptr;
-  int32_t* iside = rank == nranks - 1 ? c.pos : nullptr;
+  // scores move with the first CTA's columns, positions with the last one's
+  char* side = rank == 0 ? (char*)c.score : rank == nranks - 1 ? (char*)c.pos : nullptr;
+  if (side) side += (size_t)r * c.cap * 4;
+  int64_t* from = reinterpret_cast<int64_t*>(smem + C::OFF_FROM);
+  int64_t* to = reinterpret_cast<int64_t*>(smem + C::OFF_TO);
+  uint32_t* side_sh = reinterpret_cast<uint32_t*>(smem + C::OFF_SIDE);
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem);
+  const uint32_t side_ring = ring + C::OFF_SIDE;
+  const int chunks = (cnt + CP_TOK - 1) / CP_TOK;
+  const int tok = tid & (CP_TOK - 1);
+  const bool finds = tid < CP_TOK;           // this thread finds a token's source (the others: its target)
   bool bad = false;
-  for (int m0 = 0; m0 < cnt; m0 += TOK * CC_UNROLL) {
-    uint4 x[CC_UNROLL];
-    char* to[CC_UNROLL];
-    float sc[CC_UNROLL];
-    int32_t po[CC_UNROLL];
-    int at[CC_UNROLL];
-#pragma unroll
-    for (int u = 0; u < CC_UNROLL; ++u) {
-      const int m = m0 + u * TOK + tid / VPS;
-      to[u] = nullptr;
-      at[u] = -1;
-      if (m >= cnt) continue;
-      const int j = idx[m], d = dmap[m >> c.shift];
-      const int p = j >= m && j < n && (m == 0 || j > idx[m - 1]) ? table[j >> c.shift] : -1;
+
+  // Two reads behind each other, a chunk apart: first(m) then second(m).
+  int key = 0;                               // source: idx[m]; target: dmap of its page
+  bool fine = false;
+  int page = -1, key2 = 0;
+  const auto first = [&](int chunk) {
+    const int m = chunk * CP_TOK + tok;
+    fine = false;
+    if (m >= cnt) return;
+    if (finds) {
+      key = idx[m];
+      const int before = m > 0 ? idx[m - 1] : -1;
       // a page whose last kept token stays was planned as unchanged (it may be shared): none may move
       const int last = min(((m >> c.shift) + 1) << c.shift, cnt) - 1;
-      if (!page_ok(p, c) || !page_ok(d, c) || (j != m && idx[last] == last)) {
-        bad = true;
-        continue;
+      fine = key >= m && key < n && key > before && (key == m || idx[last] != last);
+      if (!fine) bad = true;
+    } else {
+      key = dmap[m >> c.shift];
+      fine = true;
+    }
+  };
+  const auto second = [&]() {
+    key2 = key;
+    page = -1;
+    if (!fine) return;
+    if (finds) page = table[key >> c.shift];
+    else page = key <= -2 ? w.list[off - 2 - key] : key;
+  };
+  const auto place = [&](int chunk) {        // what second() found, for everybody
+    const int m = chunk * CP_TOK + tok;
+    if (m >= cnt) page = -1;
+    else if (!page_ok(page, c)) bad = true;
+    const int o = finds ? key2 & (c.ps - 1) : m & (c.ps - 1);
+    (finds ? from : to)[(chunk % C::SLOTS) * CP_TOK + tok] = page_ok(page, c) ? page * pgs + o * ts : -1;
+  };
+
+  first(0);
+  second();
+  first(1);
+  place(0);
+  second();
+  first(2);
+  __syncthreads();
+  for (int i = 0; i < chunks + CP_STAGES - 1; ++i) {
+    if (i + 1 < chunks) place(i + 1);
+    second();
+    first(i + 3);
+    if (i < chunks) {
+      const int64_t* f = from + (i % C::SLOTS) * CP_TOK;
+      const int64_t* t = to + (i % C::SLOTS) * CP_TOK;
+      const uint32_t dst = ring + (i % CP_STAGES) * C::STAGE;
+#pragma unroll
+      for (int e = tid; e < CP_TOK * VPS; e += CP_THREADS) {
+        const int64_t a = f[e / VPS], b = t[e / VPS];
+        if (a >= 0 && b >= 0 && a != b) cp_async16(dst + e * 16, base + a + (e % VPS) * 16);
       }
-      const int64_t f = p * pgs + (j & (c.ps - 1)) * ts, t = d * pgs + (m & (c.ps - 1)) * ts;
-      if (f != t) {
-        x[u] = *reinterpret_cast<const uint4*>(base + f);
-        to[u] = base + t;
-      }
-      if (tid % VPS == 0 && j != m) {
-        at[u] = m;
-        if (side) sc[u] = side[(size_t)r * c.cap + j];
-        if (iside) po[u] = iside[(size_t)r * c.cap + j];
+      if (side && finds) {
+        const int m = i * CP_TOK + tok;
+        if (f[tok] >= 0 && t[tok] >= 0 && idx[m] != m)
+          cp_async4(side_ring + ((i % CP_STAGES) * CP_TOK + tok) * 4, side + (size_t)idx[m] * 4);
       }
     }
-    __syncthreads();
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    asm volatile("cp.async.wait_group %0;" ::"n"(CP_STAGES - 1) : "memory");
+    __syncthreads();                         // everybody's loads of the chunk below have landed
+    const int d = i - (CP_STAGES - 1);
+    if (d >= 0) {
+      const int64_t* f = from + (d % C::SLOTS) * CP_TOK;
+      const int64_t* t = to + (d % C::SLOTS) * CP_TOK;
+      const uint8_t* src_sh = smem + (d % CP_STAGES) * C::STAGE;
 #pragma unroll
-    for (int u = 0; u < CC_UNROLL; ++u) {
-      if (to[u]) *reinterpret_cast<uint4*>(to[u]) = x[u];
-      if (at[u] >= 0 && side) side[(size_t)r * c.cap + at[u]] = sc[u];
-      if (at[u] >= 0 && iside) iside[(size_t)r * c.cap + at[u]] = po[u];
+      for (int e = tid; e < CP_TOK * VPS; e += CP_THREADS) {
+        const int64_t a = f[e / VPS], b = t[e / VPS];
+        if (a >= 0 && b >= 0 && a != b)
+          *reinterpret_cast<uint4*>(base + b + (e % VPS) * 16) = *reinterpret_cast<const uint4*>(src_sh + e * 16);
+      }
+      if (side && finds) {
+        const int m = d * CP_TOK + tok;
+        if (f[tok] >= 0 && t[tok] >= 0 && idx[m] != m)
+          *reinterpret_cast<uint32_t*>(side + (size_t)m * 4) = side_sh[(d % CP_STAGES) * CP_TOK + tok];
+      }
     }
   }
   if (bad) raise_status(w.status, KVP_ERR_DEVICE_CHECK);
   cluster.sync();                            // every CTA has read the row's table and length
   const int old_pages = pages_of(n, c), new_pages = pages_of(cnt, c);
-  for (int j = rank * CC_THREADS + tid; j < old_pages; j += nranks * CC_THREADS) {
-    const int p = table[j], d = j < new_pages ? dmap[j] : -1;
+  for (int j = rank * CP_THREADS + tid; j < old_pages; j += nranks * CP_THREADS) {
+    const int p = table[j];
+    int d = j < new_pages ? dmap[j] : -1;
     if (p == d) continue;
+    if (d <= -2) {
+      d = w.list[off - 2 - d];
+      c.refs[d] = 1;
+    }
     c.table[(size_t)r * c.max_pages + j] = d;
     release_page(c, p, w.status);
   }
@@ -498,20 +624,8 @@ int compact_pages_of(const PagedView& c, int b_max) {
 
 template <int MODE>
 cudaError_t launch_plan(const PagedView& c, const PlanArgs& a, cudaStream_t st) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(PLAN_CTAS);
-  cfg.blockDim = dim3(PLAN_THREADS);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = PLAN_CTAS;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   count_launches(1);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_plan_kernel<MODE>, c, a);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return launch_with_pdl(paged_plan_kernel<MODE>, dim3(1), dim3(PLAN_THREADS), 0, st, c, a);
 }
 
 int sm_count() {
@@ -530,9 +644,13 @@ unsigned blocks_for(long long items, int per_sm) {
 
 template <int VPS>
 cudaError_t launch_compact_pages(const PagedView& c, const PlanArgs& a, int elt, int per_tensor, cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(compact_pages_kernel<VPS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       Cp<VPS>::SMEM);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(c.R * 2 * per_tensor));
-  cfg.blockDim = dim3(CC_THREADS);
+  cfg.blockDim = dim3(CP_THREADS);
+  cfg.dynamicSmemBytes = Cp<VPS>::SMEM;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -543,7 +661,7 @@ cudaError_t launch_compact_pages(const PagedView& c, const PlanArgs& a, int elt,
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   count_launches(1);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, compact_pages_kernel<VPS>, c, a, elt, per_tensor);
+  e = cudaLaunchKernelEx(&cfg, compact_pages_kernel<VPS>, c, a, elt, per_tensor);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -569,13 +687,15 @@ cudaError_t launch_paged_append(const PagedView& c, const PagedNew& n, void* ws,
   cudaError_t e = launch_plan<PLAN_APPEND>(c, a, st);
   if (e != cudaSuccess) return e;
   const int elt = c.dtype == KVP_F32 ? 4 : 2, vpr = c.D * elt / 16;
-  const long long tokens = n.n_new > c.ps ? n.n_new : c.ps;
-  const dim3 grid(blocks_for(tokens * c.R * vpr, 8));
+  const long long tokens = (long long)n.n_new * c.R;
+  const FastDiv by_new = fast_div((uint32_t)n.n_new), by_heads = fast_div((uint32_t)n.h_kv);
+  // small appends: a block per row for the shared tails, a thread per vector for the new tokens
+  const dim3 grid(blocks_for(tokens * vpr > 256LL * c.R ? tokens * vpr : 256LL * c.R, 8));
   count_launches(1);
   switch (vpr) {
-    case 8: return launch_with_pdl(append_copy_kernel<8>, grid, dim3(256), 0, st, c, n, a, elt);
-    case 16: return launch_with_pdl(append_copy_kernel<16>, grid, dim3(256), 0, st, c, n, a, elt);
-    default: return launch_with_pdl(append_copy_kernel<32>, grid, dim3(256), 0, st, c, n, a, elt);
+    case 8: return launch_with_pdl(append_copy_kernel<8>, grid, dim3(256), 0, st, c, n, a, elt, by_new, by_heads, tokens);
+    case 16: return launch_with_pdl(append_copy_kernel<16>, grid, dim3(256), 0, st, c, n, a, elt, by_new, by_heads, tokens);
+    default: return launch_with_pdl(append_copy_kernel<32>, grid, dim3(256), 0, st, c, n, a, elt, by_new, by_heads, tokens);
   }
 }
 
@@ -621,7 +741,10 @@ cudaError_t launch_paged_compact(const PagedView& c, const int32_t* idx, const i
   a.count = count;
   a.b_max = b_max;
   a.status = status;
-  cudaError_t e = launch_plan<PLAN_COMPACT>(c, a, st);
+  count_launches(1);
+  cudaError_t e = launch_with_pdl(compact_need_kernel, dim3((unsigned)c.R), dim3(NEED_THREADS), 0, st, c, a);
+  if (e != cudaSuccess) return e;
+  e = launch_plan<PLAN_COMPACT>(c, a, st);
   if (e != cudaSuccess) return e;
   const int elt = c.dtype == KVP_F32 ? 4 : 2, vpr = c.D * elt / 16;
   // 128 bytes of a token per CTA: a full line, and up to four CTAs share K (or V) of a row

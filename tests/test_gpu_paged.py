@@ -154,6 +154,100 @@ def test_rows_that_find_no_pages_stay_as_they_were(kvp):
     check_same(c, o, "compact")
 
 
+def test_many_rows_and_pages(kvp):
+    """More rows than the plan has threads, more pages than it looks at in one step: the i-th page that is
+    needed is the i-th lowest free one."""
+    R, ps, n_pages, D = 2600, 16, 150001, 64
+    rng = np.random.default_rng(7)
+    c = kvp.PagedCache.empty(R, 60, n_pages, ps, D, torch.float16)
+    refs = torch.from_numpy((rng.random(n_pages) < 0.3).astype(np.int32))      # pages other rows hold
+    refs[:131200] = 1
+    refs[::5000] = 0
+    c.refs.copy_(refs)
+    c.free_mask.copy_(torch.from_numpy(paged.free_mask({"refs": refs.numpy()})))
+    free = np.nonzero(refs.numpy() == 0)[0]
+    lens = np.zeros(R, np.int64)
+    table = np.full((R, 60), -1)
+    at = 0
+    for n_new in (40, 1, 33):
+        cnt = rng.integers(0, n_new + 1, R)
+        new = torch.randn(2, R, n_new, D, device="cuda").half()
+        kvp.kvp_paged_append(c, new[0], new[1], counts=i32(cnt))
+        kvp.kvp_check_device_status()
+        for r in range(R):
+            for j in range(-(-lens[r] // ps), -(-(lens[r] + cnt[r]) // ps)):
+                table[r, j] = free[at]
+                at += 1
+        held = c.table.long()
+        t = torch.from_numpy(lens).cuda()[:, None] + torch.arange(n_new, device="cuda")
+        live = torch.arange(n_new, device="cuda") < i32(cnt)[:, None]
+        page = held.gather(1, (t // ps).clamp(max=59))
+        for pool, x in ((c.k_pool, new[0]), (c.v_pool, new[1])):
+            assert torch.equal(pool[page.clamp(min=0), t % ps][live], x[live])
+        lens += cnt
+        assert (c.table.cpu().numpy() == table).all() and (c.lens.cpu().numpy() == lens).all()
+    src = np.full(R, -1)
+    kvp.kvp_paged_free(c, i32(np.where(np.arange(R) % 3, -1, 0)))
+    src[::3] = np.arange(R)[1::3][:len(src[::3])]
+    kvp.kvp_paged_fork(c, i32(src), copy=True)
+    kvp.kvp_check_device_status()
+    got, n = c.table.cpu().numpy(), lens.copy()
+    n[::3] = lens[src[::3]]
+    assert (c.lens.cpu().numpy() == n).all()
+    rows = rows_of(c)
+    for r in range(0, R, 3):
+        assert torch.equal(rows[0][r], rows[0][src[r]]) and torch.equal(rows[1][r], rows[1][src[r]])
+        assert not set(got[r, :-(-n[r] // ps)]) & set(got[src[r], :-(-n[r] // ps)])
+    used = np.concatenate([got[r, :-(-n[r] // ps)] for r in range(R)])
+    assert len(set(used)) == len(used)
+    own = refs.numpy().copy()
+    own[used] += 1
+    assert (c.refs.cpu().numpy() == own).all()
+    assert (c.free_mask.cpu().numpy() == paged.free_mask({"refs": own})).all()
+
+
+@pytest.mark.parametrize("dtype,D,R", [("f16", 128, 5), ("f32", 128, 3), ("f32", 64, 40), ("bf16", 64, 9)])
+def test_compact_long_rows(kvp, dtype, D, R):
+    """Rows of many chunks, kept in long runs, single tokens and none; half of them share pages with others."""
+    rng = np.random.default_rng(D + R)
+    ps, T = 32, 2500
+    c = kvp.PagedCache.empty(2 * R, 81, R * 81 + 2 * R * 81, ps, D, DT[dtype], scores=True, positions=True)
+    new = torch.randn(2, 2 * R, T, D, device="cuda").to(DT[dtype])
+    kvp.kvp_paged_append(c, new[0], new[1], counts=i32([T - 7 * r for r in range(R)] + [0] * R))
+    kvp.kvp_paged_fork(c, i32([-1] * R + [r if r % 2 else -1 for r in range(R)]))
+    c.score.copy_(torch.rand(c.score.shape, device="cuda"))
+    score, lens = c.score.clone(), c.lens.tolist()
+    idx, cnt = np.full((2 * R, 2000), -1), []
+    for r in range(2 * R):
+        n = min(lens[r], 2000)
+        share = (0.02, 0.5, 0.97, 1.0, 0.3)[r % 5]
+        kept = np.nonzero(rng.random(lens[r]) < share)[0][:2000] if lens[r] else np.zeros(0, int)
+        if r % 4 == 1:
+            kept = np.concatenate([np.arange(n // 3), kept[kept >= n // 3]])[:2000]
+        if r % 7 == 6:
+            kept = kept[:0]
+        idx[r, :len(kept)] = kept
+        cnt.append(len(kept))
+    kvp.kvp_paged_compact(c, i32(idx), i32(cnt))
+    kvp.kvp_check_device_status()
+    rows = rows_of(c)
+    assert c.lens.tolist() == cnt
+    held = torch.zeros(c.n_pages, dtype=torch.int64)
+    for r in range(2 * R):
+        kept = torch.from_numpy(idx[r, :cnt[r]])
+        s = r if r < R else r - R
+        assert torch.equal(rows[0][r], new[0, s].cpu()[kept]), r
+        assert torch.equal(rows[1][r], new[1, s].cpu()[kept]), r
+        assert torch.equal(c.score[r, :cnt[r]], score[r][kept.cuda()])
+        if r < R:
+            assert torch.equal(c.pos[r, :cnt[r]].cpu(), kept.int())
+        pages = -(-cnt[r] // ps)
+        held[c.table[r, :pages].cpu().long()] += 1
+        assert (c.table[r, pages:] == -1).all()
+    assert torch.equal(held.int(), c.refs.cpu())
+    assert torch.equal(c.free_mask.cpu(), torch.from_numpy(paged.free_mask({"refs": held.numpy()})))
+
+
 def filled(kvp, lens, ps, D, dtype, seed, spare=3, scores=False, stale=float("nan"), interleaved=False, key_scale=1.0):
     """A cache whose rows' pages lie in any order; slots behind the rows' ends hold ``stale``."""
     gen = torch.Generator().manual_seed(seed)
