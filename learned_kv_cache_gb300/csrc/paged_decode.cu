@@ -176,38 +176,108 @@ __global__ void __launch_bounds__(PD_WARPS * 32) paged_decode_kernel(const T* __
 // scores once the rows' log-sum-exps are known.  Block (c, y) belongs to CTA c of the decode kernel:
 // it merges the row that continues from CTA c - 1 if that CTA held its first tiles, and scores c's
 // own keys; y shares out the outputs and the tiles.
-constexpr int JOIN_THREADS = 128;
+constexpr int JOIN_THREADS = 256;
+
+// Base-2 log-sum-exp of every head of a row whose parts CTAs [lo, hi] hold, and (weights not null) what
+// each part weighs in it: a warp per head, a lane per part, the reads of all parts in flight at once.
+// Ends with a barrier.
+template <int GP>
+__device__ __forceinline__ void join_states(const Params& p, int lo, int hi, float* lse_sh, float* weights) {
+  const int lane = threadIdx.x & 31, n = hi - lo + 1;
+  // part i of the row: CTA lo has it in slot 1, the others in slot 0
+  const auto at = [&](int i) { return p.part + ((size_t)(lo + i) * 2 + (i == 0 ? 1 : 0)) * p.pstride; };
+  for (int h = threadIdx.x >> 5; h < p.G; h += JOIN_THREADS / 32) {
+    constexpr int K = 4;                     // parts per lane and step
+    float M = -INFINITY, L = 0.f, m[K], l[K];
+    for (int i0 = 0; i0 < n; i0 += 32 * K) {
+      float top = M;
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int i = i0 + 32 * k + lane;
+        m[k] = i < n ? at(i)[h] : -INFINITY;
+        l[k] = i < n ? at(i)[GP + h] : 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < K; ++k) top = fmaxf(top, m[k]);
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+      float s = 0.f;
+#pragma unroll
+      for (int k = 0; k < K; ++k) s = fmaf(l[k], paged::weight(m[k], top), s);
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+      L = fmaf(L, paged::weight(M, top), s);
+      M = top;
+    }
+    if (lane == 0) lse_sh[h] = L == 0.f ? -INFINITY : M + log2f(L);
+    if (weights)
+      for (int i = lane, k = 0; i < n; i += 32, ++k) {
+        const float mi = n <= 32 ? m[0] : at(i)[h];
+        weights[i * GP + h] = L == 0.f ? 0.f : paged::weight(mi, M) / L;
+      }
+  }
+  __syncthreads();
+}
 
 template <typename T, int D, int GP>
 __global__ void __launch_bounds__(JOIN_THREADS) paged_join_kernel(const Params p, int add_scores) {
-  wait_prior_grid();
-  const int cta = blockIdx.x, y = blockIdx.y, ny = gridDim.y, tid = threadIdx.x;
+  extern __shared__ float weights[];         // [ctas][GP]
   __shared__ float lse_sh[GP];
+  __shared__ float4 sum_sh[JOIN_THREADS];
+  wait_prior_grid();
+  allow_next_grid();                         // few, short blocks: the next kernel may take its places beside them
+  const int cta = blockIdx.x, y = blockIdx.y, ny = gridDim.y, tid = threadIdx.x;
   const Range g = p.range[cta];
   if (cta >= g.active) return;
   const PagedView& c = p.c;
-  const auto part = [&](int i, int first) {   // partial of CTA i of a row whose first tiles CTA `first` has
-    return p.part + ((size_t)i * 2 + (i == first ? 1 : 0)) * p.pstride;
-  };
-  if (g.tile > 0) {
-    const int x0 = g.begin - g.tile, c_lo = paged::cta_of(x0, g.total, g.active);
-    if (c_lo == cta - 1) {
-      const int nt = paged::tiles_of(paged::row_len(p, g.row));
-      const int c_hi = paged::cta_of(x0 + nt - 1, g.total, g.active);
-      const size_t head0 = (size_t)(g.row / p.Hkv) * p.Hq + (size_t)(g.row % p.Hkv) * p.G;
-      for (int e = y * JOIN_THREADS + tid; e < p.G * D; e += ny * JOIN_THREADS) {
-        const int h = e / D;
-        float M = -INFINITY;
-        for (int i = c_lo; i <= c_hi; ++i) M = fmaxf(M, part(i, c_lo)[h]);
-        float L = 0.f, O = 0.f;
-        for (int i = c_lo; i <= c_hi; ++i) {
-          const float* q = part(i, c_lo);
-          const float f = paged::weight(q[h], M);
-          L = fmaf(q[GP + h], f, L);
-          O = fmaf(q[2 * GP + e], f, O);
-        }
-        paged::store_out<T>(p, head0 * D + e, L == 0.f ? 0.f : O / L);
-        if (p.lse && e % D == 0) p.lse[head0 + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * KVP_LN2;
+  if (g.tile > 0 && g.lo == cta - 1) {
+    const int lo = g.lo, hi = g.hi;
+    const size_t head0 = (size_t)(g.row / p.Hkv) * p.Hq + (size_t)(g.row % p.Hkv) * p.G;
+    // a thread per quad of outputs and eight parts; with more parts, several threads per quad
+    int lanes = JOIN_THREADS;                // quads per block
+    while (lanes > 32 && (hi - lo + 1) > 8 * (JOIN_THREADS / lanes)) lanes >>= 1;
+    const int split = JOIN_THREADS / lanes, grp = tid / lanes, quads = p.G * D / 4;
+    bool ready = false;
+    for (int q0 = y * lanes; q0 < quads; q0 += ny * lanes) {
+      const int e = 4 * (q0 + tid % lanes), h = e / D;
+      const bool mine = e < p.G * D;
+      const auto out_of = [&](int i) {
+        return *reinterpret_cast<const float4*>(p.part + ((size_t)(lo + i) * 2 + (i == 0 ? 1 : 0)) * p.pstride +
+                                                2 * GP + e);
+      };
+      // the first outputs are fetched beside the states that weigh them
+      float4 early[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        early[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (mine && grp + k * split <= hi - lo) early[k] = out_of(grp + k * split);
+      }
+      if (!ready) join_states<GP>(p, lo, hi, lse_sh, weights);
+      ready = true;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      const auto add = [&](const float4& x, float f) {
+        o.x = fmaf(x.x, f, o.x);
+        o.y = fmaf(x.y, f, o.y);
+        o.z = fmaf(x.z, f, o.z);
+        o.w = fmaf(x.w, f, o.w);
+      };
+      if (mine) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (grp + k * split <= hi - lo) add(early[k], weights[(grp + k * split) * GP + h]);
+#pragma unroll 8
+        for (int i = grp + 8 * split; i <= hi - lo; i += split) add(out_of(i), weights[i * GP + h]);
+      }
+      if (split > 1) {
+        __syncthreads();                     // the quads before have been summed
+        sum_sh[tid] = o;
+        __syncthreads();
+        if (grp == 0)
+          for (int k = 1; k < split; ++k) add(sum_sh[k * lanes + tid], 1.f);
+      }
+      if (grp == 0 && mine) {
+        paged::store_out4<T>(p, head0 * D + e, o);
+        if (p.lse && e % D == 0) p.lse[head0 + h] = lse_sh[h] * KVP_LN2;
       }
     }
   }
@@ -221,32 +291,32 @@ __global__ void __launch_bounds__(JOIN_THREADS) paged_join_kernel(const Params p
       continue;
     }
     const int u1 = min(nt, u + (g.end - x));
-    const bool whole = u == 0 && u1 == nt;
-    __syncthreads();
-    if (tid < p.G) {
-      if (whole) {
-        lse_sh[tid] = p.lse2[(size_t)r * GP + tid];
-      } else {
-        const int x0 = x - u;
-        const int c_lo = paged::cta_of(x0, g.total, g.active), c_hi = paged::cta_of(x0 + nt - 1, g.total, g.active);
-        float M = -INFINITY, L = 0.f;
-        for (int i = c_lo; i <= c_hi; ++i) M = fmaxf(M, part(i, c_lo)[tid]);
-        for (int i = c_lo; i <= c_hi; ++i) {
-          const float* q = part(i, c_lo);
-          L = fmaf(q[GP + tid], paged::weight(q[tid], M), L);
-        }
-        lse_sh[tid] = L == 0.f ? -INFINITY : M + log2f(L);
-      }
+    __syncthreads();                         // the row before is done with lse_sh
+    if (u == 0 && u1 == nt) {
+      if (tid < p.G) lse_sh[tid] = p.lse2[(size_t)r * GP + tid];
+      __syncthreads();
+    } else {
+      join_states<GP>(p, paged::cta_of(x - u, g.total, g.active), paged::cta_of(x - u + nt - 1, g.total, g.active),
+                      lse_sh, nullptr);
     }
-    __syncthreads();
+    float lse[GP];
+#pragma unroll
+    for (int h = 0; h < GP; ++h) lse[h] = h < p.G ? lse_sh[h] : 0.f;
     const int hi = min(n, u1 * TILE);
     for (int m = u * TILE + y * JOIN_THREADS + tid; m < hi; m += ny * JOIN_THREADS) {
-      const float* lg = p.logits + ((size_t)r * c.cap + m) * GP;
+      const float4* lg = reinterpret_cast<const float4*>(p.logits + ((size_t)r * c.cap + m) * GP);
+      float* score = c.score + (size_t)r * c.cap + m;
+      const float before = *score;
       float s = 0.f;
 #pragma unroll
-      for (int h = 0; h < GP; ++h)
-        if (h < p.G && lg[h] != -INFINITY) s += fast_exp2(lg[h] - lse_sh[h]);
-      c.score[(size_t)r * c.cap + m] += s;
+      for (int k = 0; k < GP / 4; ++k) {
+        const float4 w = lg[k];
+        const float z[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (4 * k + i < p.G && z[i] != -INFINITY) s += fast_exp2(z[i] - lse[4 * k + i]);
+      }
+      *score = before + s;
     }
     x += u1 - u;
     ++r;
@@ -296,10 +366,18 @@ cudaError_t run(const Params& p, const PagedDecodeArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   // a row of one tile is never shared, and without scores nothing is left to do
   if (!a.add_scores && p.c.cap <= TILE) return cudaSuccess;
-  const int slices = (p.G * D + JOIN_THREADS - 1) / JOIN_THREADS;
+  // Blocks per CTA of the decode kernel.  Rows of which there are many have few parts each (one block
+  // joins 1024 outputs of up to 8 parts in one go); of a few long rows the outputs are dealt out
+  // further, and so are the scores of long ranges.
+  int slices = (p.G * D + 1023) / 1024;
+  if (8LL * p.c.R < p.ctas) slices = (p.G * D + 127) / 128;
+  if (a.add_scores) {
+    const long long keys = (long long)p.c.R * p.c.cap / p.ctas;
+    while (slices < 8 && keys > 4LL * JOIN_THREADS * slices) slices *= 2;
+  }
   count_launches(1);
-  return launch_with_pdl(paged_join_kernel<T, D, GP>, dim3((unsigned)p.ctas, (unsigned)slices), dim3(JOIN_THREADS), 0,
-                         st, p, a.add_scores);
+  return launch_with_pdl(paged_join_kernel<T, D, GP>, dim3((unsigned)p.ctas, (unsigned)slices), dim3(JOIN_THREADS),
+                         (size_t)p.ctas * GP * sizeof(float), st, p, a.add_scores);
 }
 
 }  // namespace

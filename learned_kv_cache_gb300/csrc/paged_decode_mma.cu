@@ -46,7 +46,8 @@ struct Pm {
   static constexpr int HALVES = D / 64;                    // 128-byte swizzle spans per token
   static constexpr int HALF_BYTES = TILE * 128;
   static constexpr int TILE_BYTES = HALVES * HALF_BYTES;   // K (or V) of a tile
-  static constexpr int Q_BYTES = GP * D * 2;
+  static constexpr int Q_ROW = D * 2 + 16;                 // padded: the fragment loads hit distinct banks
+  static constexpr int Q_BYTES = GP * Q_ROW;
   static constexpr int STAGES = D == 128 ? (GP == 8 ? 3 : 2) : (GP == 8 ? 5 : 4);
   static constexpr int KSTEPS = D / 16;
   static constexpr int NT = GP / 8;                        // n8 tiles of query heads
@@ -54,10 +55,12 @@ struct Pm {
   static constexpr int OFF_Q = STAGES * 2 * TILE_BYTES;
   static constexpr int OFF_O = OFF_Q + STAGES * Q_BYTES;   // [2][GP][OSTR]
   static constexpr int OFF_ML = OFF_O + 2 * GP * OSTR * 4; // [2 rows in turn][m, l][4 warps][GP]
-  static constexpr int OFF_BAR = OFF_ML + 2 * 2 * PM_CWARPS * GP * 4;
+  static constexpr int OFF_INV = OFF_ML + 2 * 2 * PM_CWARPS * GP * 4;   // [2 rows in turn][GP]
+  static constexpr int OFF_BAR = OFF_INV + 2 * GP * 4;
   static constexpr int OFF_FLAG = OFF_BAR + 16 * STAGES;
   static constexpr int OFF_SCAN = OFF_FLAG + 16;
   static constexpr int SMEM = OFF_SCAN + 48 * 4 + 1024;    // + alignment slack
+  static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two CTAs per SM");
 };
 
 // Shared address of the 16-byte chunk holding (key, d..d+7) of a swizzled tile.
@@ -187,9 +190,9 @@ __global__ void __launch_bounds__(PM_THREADS, 2)
           const uint32_t dst = sbase + (2 * s + v) * C::TILE_BYTES + h * C::HALF_BYTES + k * box * 128;
           ptx::tma_load_3d(dst, v ? &tmV : &tmK, bar, 64 * h, k == 0 ? (u * TILE) & (p.c.ps - 1) : 0, pg);
         }
-        if (lane == 31 && with_q)
-          bulk_load(sbase + C::OFF_Q + s * C::Q_BYTES, q + (r / p.Hkv) * p.q_stride + (size_t)(r % p.Hkv) * p.G * D,
-                    p.G * D * 2, bar);
+        if (with_q && lane >= 16 && lane - 16 < p.G)       // boxes take 16 lanes at most
+          bulk_load(sbase + C::OFF_Q + s * C::Q_BYTES + (lane - 16) * C::Q_ROW,
+                    q + (r / p.Hkv) * p.q_stride + (size_t)((r % p.Hkv) * p.G + lane - 16) * D, D * 2, bar);
         __syncwarp();
         ++li;
         if (i == min(C::STAGES, a.count) - 1) next = look_ahead(p, row, tile, left);
@@ -215,7 +218,11 @@ __global__ void __launch_bounds__(PM_THREADS, 2)
     float* sm_m = reinterpret_cast<float*>(smem + C::OFF_ML) + turn * 2 * PM_CWARPS * GP;
     float* sm_l = sm_m + PM_CWARPS * GP;
     float* sm_o = reinterpret_cast<float*>(smem + C::OFF_O);
+    float* sm_inv = reinterpret_cast<float*>(smem + C::OFF_INV) + turn * GP;
     turn ^= 1;                   // the other half may still be read
+    const bool whole = u0 == 0 && u1 == nt;
+    float* part = p.part + ((size_t)cta * 2 + (u0 > 0 ? 0 : 1)) * p.pstride;
+    const size_t head0 = (size_t)(r / p.Hkv) * p.Hq + (size_t)(r % p.Hkv) * p.G;
 #pragma unroll
     for (int x = 0; x < C::NT; ++x) {
       float l0 = ls[x][0], l1 = ls[x][1];
@@ -232,6 +239,22 @@ __global__ void __launch_bounds__(PM_THREADS, 2)
       }
     }
     asm volatile("bar.sync 1, %0;" ::"n"(PM_CWARPS * 32) : "memory");
+    if (threadIdx.x < p.G) {     // a head's merged state, while warps 2 and 3 write below
+      const int h = threadIdx.x;
+      const float M = fmaxf(fmaxf(sm_m[h], sm_m[GP + h]), fmaxf(sm_m[2 * GP + h], sm_m[3 * GP + h]));
+      float L = 0.f;
+#pragma unroll
+      for (int w = 0; w < PM_CWARPS; ++w) L = fmaf(sm_l[w * GP + h], paged::weight(sm_m[w * GP + h], M), L);
+      if (whole) {
+        const float l2 = L == 0.f ? -INFINITY : M + log2f(L);
+        if (p.lse) p.lse[head0 + h] = l2 * KVP_LN2;
+        if (p.lse2) p.lse2[(size_t)r * GP + h] = l2;
+      } else {
+        part[h] = M;
+        part[GP + h] = L;
+      }
+      sm_inv[h] = !whole ? 1.f : L == 0.f ? 0.f : 1.f / L;
+    }
     // warps 2 and 3 hand their scaled outputs to warps 0 and 1
     float* ow = sm_o + (warp & 1) * GP * C::OSTR;
 #pragma unroll
@@ -258,30 +281,14 @@ __global__ void __launch_bounds__(PM_THREADS, 2)
       }
       asm volatile("bar.sync 1, %0;" ::"n"(PM_CWARPS * 32) : "memory");
     }
-    const bool whole = u0 == 0 && u1 == nt;
-    float* part = p.part + ((size_t)cta * 2 + (u0 > 0 ? 0 : 1)) * p.pstride;
-    const size_t head0 = (size_t)(r / p.Hkv) * p.Hq + (size_t)(r % p.Hkv) * p.G;
-    for (int e = threadIdx.x; e < p.G * D; e += PM_CWARPS * 32) {
+    for (int e = 4 * threadIdx.x; e < p.G * D; e += 4 * PM_CWARPS * 32) {
       const int h = e / D, d = e % D;
-      const float M = fmaxf(fmaxf(sm_m[h], sm_m[GP + h]), fmaxf(sm_m[2 * GP + h], sm_m[3 * GP + h]));
-      float L = 0.f;
-#pragma unroll
-      for (int w = 0; w < PM_CWARPS; ++w) L = fmaf(sm_l[w * GP + h], paged::weight(sm_m[w * GP + h], M), L);
-      const float O = sm_o[h * C::OSTR + d] + sm_o[(GP + h) * C::OSTR + d];
-      if (whole) {
-        paged::store_out<T>(p, head0 * D + e, L == 0.f ? 0.f : O / L);
-        if (d == 0) {
-          const float l2 = L == 0.f ? -INFINITY : M + log2f(L);
-          if (p.lse) p.lse[head0 + h] = l2 * KVP_LN2;
-          if (p.lse2) p.lse2[(size_t)r * GP + h] = l2;
-        }
-      } else {
-        part[2 * GP + e] = O;
-        if (d == 0) {
-          part[h] = M;
-          part[GP + h] = L;
-        }
-      }
+      const float4 a = *reinterpret_cast<const float4*>(sm_o + h * C::OSTR + d);
+      const float4 b = *reinterpret_cast<const float4*>(sm_o + (GP + h) * C::OSTR + d);
+      const float f = sm_inv[h];
+      const float4 z = make_float4((a.x + b.x) * f, (a.y + b.y) * f, (a.z + b.z) * f, (a.w + b.w) * f);
+      if (whole) paged::store_out4<T>(p, head0 * D + e, z);
+      else *reinterpret_cast<float4*>(part + 2 * GP + e) = z;
     }
   };
 
@@ -307,7 +314,7 @@ __global__ void __launch_bounds__(PM_THREADS, 2)
 #pragma unroll
         for (int y = 0; y < C::NT; ++y) {
           const bool live = 8 * y + hg < p.G;
-          const uint8_t* qr = qs + (8 * y + hg) * D * 2;
+          const uint8_t* qr = qs + (8 * y + hg) * C::Q_ROW;
 #pragma unroll
           for (int ks = 0; ks < C::KSTEPS; ++ks)
 #pragma unroll
@@ -422,6 +429,7 @@ __global__ void __launch_bounds__(PM_THREADS, 2)
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bar_empty + 8 * s);
     }
+    if (x + (u1 - u0) >= g.end) allow_next_grid();   // the join kernel's CTAs may take their places
     if (u1 > u0) finish(r, u0, u1, nt);
     x += u1 - u0;
     ++r;

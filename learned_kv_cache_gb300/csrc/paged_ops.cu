@@ -67,6 +67,25 @@ __device__ __forceinline__ void release_page(const PagedView& c, int p, int* sta
   }
 }
 
+// Releases what `pages` gives for j = first, first + step, ... < end (-1: nothing): four counts of a
+// thread are under way at a time.
+template <typename F>
+__device__ __forceinline__ void release_pages(const PagedView& c, int first, int end, int step, int* status, F pages) {
+  for (int j0 = first; j0 < end; j0 += 4 * step) {
+    int p[4], old[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) p[u] = j0 + u * step < end ? pages(j0 + u * step) : -1;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) old[u] = p[u] >= 0 && p[u] < c.n_pages ? atomicSub(c.refs + p[u], 1) : 2;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (old[u] == 1) atomicOr(c.free_mask + (p[u] >> 5), 1u << (p[u] & 31));
+      if (old[u] <= 0) atomicAdd(c.refs + p[u], 1);            // nobody held it: put the count back
+      if (old[u] <= 0 || p[u] >= c.n_pages || p[u] < -1) raise_status(status, KVP_ERR_DEVICE_CHECK);
+    }
+  }
+}
+
 // What the plan finds out about a row: the pages it needs, and what the kernel behind it has to know.
 struct RowPlan {
   int start, need, tail, cnt;
@@ -153,6 +172,8 @@ template <int MODE>
 __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const PagedView c, const PlanArgs a) {
   __shared__ int scan_sh[33];
   __shared__ int used_sh;
+  __shared__ uint32_t word_sh[PLAN_WORDS * PLAN_THREADS];
+  __shared__ int rank_sh[PLAN_WORDS * PLAN_THREADS];
   wait_prior_grid();
   const int tid = threadIdx.x, lane = tid & 31;
   const int words = (c.n_pages + 31) >> 5;
@@ -193,12 +214,28 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const PagedVie
     }
     int all;
     int at = found + block_exclusive_scan(mine, scan_sh, &all);
+    // the words change hands: consecutive ones to consecutive warps, a lane per page within a warp, so
+    // that a run of free pages is written by the whole CTA, in consecutive entries of the list
 #pragma unroll
     for (int k = 0; k < PLAN_WORDS; ++k) {
-      const int x = base + PLAN_WORDS * tid + k;
-      uint32_t v = mask[k];
-      for (; v && at < want; v &= v - 1, ++at) a.list[at] = x * 32 + __ffs(v) - 1;
-      if (v != mask[k]) c.free_mask[x] = v;
+      word_sh[PLAN_WORDS * tid + k] = mask[k];
+      rank_sh[PLAN_WORDS * tid + k] = at;
+      at += __popc(mask[k]);
+    }
+    __syncthreads();
+    for (int i = 0; i < PLAN_WORDS; ++i) {
+      const int mine_x = (i * 32 + lane) * (PLAN_THREADS / 32) + (tid >> 5);
+      uint32_t some = __ballot_sync(0xffffffffu, word_sh[mine_x] != 0 && rank_sh[mine_x] < want);
+      while (some) {
+        const int x = (i * 32 + __ffs(some) - 1) * (PLAN_THREADS / 32) + (tid >> 5);
+        some &= some - 1;
+        const uint32_t v = word_sh[x];
+        const int to = rank_sh[x] + __popc(v & ((1u << lane) - 1u));
+        const bool taken = ((v >> lane) & 1u) && to < want;
+        if (taken) a.list[to] = (base + x) * 32 + lane;
+        const uint32_t gone = __ballot_sync(0xffffffffu, taken);
+        if (lane == 0) c.free_mask[base + x] = v & ~gone;
+      }
     }
     found += all;
   }
@@ -273,11 +310,9 @@ __device__ __forceinline__ uint32_t div_by(uint32_t x, const FastDiv& d) {
 }
 
 // New tokens to their slots, and the books of the pages taken for them: a page's entry and count are
-// written by the thread of the first new token in it.  Each thread has four vectors of K and of V in
-// flight.
-constexpr int AC_UNROLL = 4;
-
-template <int VPR>
+// written by the thread of the first new token in it.  UN tokens per thread are in flight: four where
+// there is more than one pass of work for the GPU, one where there is less (a decode step).
+template <int VPR, int UN>
 __global__ void __launch_bounds__(256) append_copy_kernel(const PagedView c, const PagedNew a, const PlanArgs w,
                                                           int elt, FastDiv by_new, FastDiv by_heads, long long tokens) {
   wait_prior_grid();
@@ -286,43 +321,51 @@ __global__ void __launch_bounds__(256) append_copy_kernel(const PagedView c, con
   char* pv = (char*)c.v;
   constexpr int TOK = 256 / VPR;             // tokens per CTA and pass
   const int v = threadIdx.x % VPR;
-  const long long step = (long long)gridDim.x * TOK;
-  for (long long x0 = (long long)blockIdx.x * TOK + threadIdx.x / VPR; x0 < tokens; x0 += step * AC_UNROLL) {
-    uint4 k[AC_UNROLL], y[AC_UNROLL];
-    int row[AC_UNROLL], tok[AC_UNROLL];
+  const long long step = (long long)gridDim.x * TOK * UN;
+  for (long long x0 = (long long)blockIdx.x * TOK * UN + threadIdx.x / VPR; x0 < tokens; x0 += step) {
+    uint4 k[UN], y[UN];
+    int row[UN], slot[UN], page[UN], new_page[UN];
 #pragma unroll
-    for (int u = 0; u < AC_UNROLL; ++u) {
-      const long long x = x0 + u * step;
+    for (int u = 0; u < UN; ++u) {
+      const long long x = x0 + u * TOK;
       row[u] = -1;
       if (x >= tokens) continue;
       const int r = (int)div_by((uint32_t)x, by_new), i = (int)((uint32_t)x - (uint32_t)r * by_new.by);
-      if (i >= (a.counts ? a.counts[r] : a.n_new)) continue;
+      if (i >= (a.counts ? __ldg(a.counts + r) : a.n_new)) continue;
       const int b = (int)div_by((uint32_t)r, by_heads), h = r - b * a.h_kv;
-      row[u] = r;
-      tok[u] = i;
       k[u] = ld_stream16((const char*)a.k + (b * a.ks[0] + h * a.ks[1] + i * a.ks[2]) * elt + v * 16);
       y[u] = ld_stream16((const char*)a.v + (b * a.vs[0] + h * a.vs[1] + i * a.vs[2]) * elt + v * 16);
+      row[u] = r;
+      slot[u] = i;
     }
 #pragma unroll
-    for (int u = 0; u < AC_UNROLL; ++u) {
-      const int r = row[u], i = tok[u];
+    for (int u = 0; u < UN; ++u) {
+      page[u] = -1;
+      new_page[u] = 0;
+      const int r = row[u];
       if (r < 0) continue;
-      const int start = w.start[r];
+      const int start = __ldg(w.start + r), tail = __ldg(w.tail + r), off = __ldg(w.off + r);
       if (start < 0) continue;
-      const int t = start + i, j = t >> c.shift, o = t & (c.ps - 1);
-      const int first = w.tail[r] >= 0 ? start >> c.shift : pages_of(start, c);
-      const int p = j >= first ? w.list[w.off[r] + j - first] : table_row(c, r)[j];
-      if (!page_ok(p, c)) continue;
-      const int64_t to = p * pgs + o * ts + v * 16;
+      const int i = slot[u], t = start + i, j = t >> c.shift;
+      const int first = tail >= 0 ? start >> c.shift : pages_of(start, c);
+      page[u] = j >= first ? __ldg(w.list + off + j - first) : table_row(c, r)[j];
+      new_page[u] = j >= first && (i == 0 || (t & (c.ps - 1)) == 0);
+      slot[u] = t;
+      if (v == 0 && c.pos) c.pos[(size_t)r * c.cap + t] = a.pos ? __ldg(a.pos + r) + i : t;
+    }
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+      if (!page_ok(page[u], c)) continue;
+      const int r = row[u], t = slot[u], p = page[u];
+      const int64_t to = p * pgs + (t & (c.ps - 1)) * ts + v * 16;
       *reinterpret_cast<uint4*>(pk + to) = k[u];
       *reinterpret_cast<uint4*>(pv + to) = y[u];
       if (v == 0) {
-        if (j >= first && (i == 0 || o == 0)) {
-          table_row(c, r)[j] = p;
+        if (new_page[u]) {
+          table_row(c, r)[t >> c.shift] = p;
           c.refs[p] = 1;
         }
         if (c.score) c.score[(size_t)r * c.cap + t] = 0.f;
-        if (c.pos) c.pos[(size_t)r * c.cap + t] = a.pos ? a.pos[r] + i : t;
       }
     }
   }
@@ -392,7 +435,8 @@ struct Cp {
   static constexpr int SLOTS = CP_STAGES + 2;              // chunks whose places are kept
   static constexpr int OFF_FROM = CP_STAGES * STAGE;       // int64 [SLOTS][CP_TOK] source and target offsets
   static constexpr int OFF_TO = OFF_FROM + SLOTS * CP_TOK * 8;
-  static constexpr int OFF_SIDE = OFF_TO + SLOTS * CP_TOK * 8;   // [CP_STAGES][CP_TOK] 4 bytes
+  static constexpr int OFF_INDEX = OFF_TO + SLOTS * CP_TOK * 8;  // int32 [SLOTS][CP_TOK] source tokens
+  static constexpr int OFF_SIDE = OFF_INDEX + SLOTS * CP_TOK * 4;   // [CP_STAGES][CP_TOK] 4 bytes
   static constexpr int SMEM = OFF_SIDE + CP_STAGES * CP_TOK * 4;
 };
 
@@ -425,6 +469,7 @@ __global__ void __launch_bounds__(CP_THREADS) compact_pages_kernel(const PagedVi
   if (side) side += (size_t)r * c.cap * 4;
   int64_t* from = reinterpret_cast<int64_t*>(smem + C::OFF_FROM);
   int64_t* to = reinterpret_cast<int64_t*>(smem + C::OFF_TO);
+  int32_t* index_sh = reinterpret_cast<int32_t*>(smem + C::OFF_INDEX);
   uint32_t* side_sh = reinterpret_cast<uint32_t*>(smem + C::OFF_SIDE);
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem);
   const uint32_t side_ring = ring + C::OFF_SIDE;
@@ -433,51 +478,53 @@ __global__ void __launch_bounds__(CP_THREADS) compact_pages_kernel(const PagedVi
   const bool finds = tid < CP_TOK;           // this thread finds a token's source (the others: its target)
   bool bad = false;
 
-  // Two reads behind each other, a chunk apart: first(m) then second(m).
-  int key = 0;                               // source: idx[m]; target: dmap of its page
-  bool fine = false;
+  // Two reads behind each other, an iteration apart: what first() loads, second() looks at, and what
+  // second() loads, place() writes down.  Nothing is waited for in the iteration that asks for it.
+  int key = 0, before = 0, last_key = 0;     // source: idx[m], idx[m - 1], idx at the end of the page; target: dmap
   int page = -1, key2 = 0;
   const auto first = [&](int chunk) {
     const int m = chunk * CP_TOK + tok;
-    fine = false;
     if (m >= cnt) return;
     if (finds) {
       key = idx[m];
-      const int before = m > 0 ? idx[m - 1] : -1;
-      // a page whose last kept token stays was planned as unchanged (it may be shared): none may move
-      const int last = min(((m >> c.shift) + 1) << c.shift, cnt) - 1;
-      fine = key >= m && key < n && key > before && (key == m || idx[last] != last);
-      if (!fine) bad = true;
+      before = m > 0 ? idx[m - 1] : -1;
+      last_key = idx[min(((m >> c.shift) + 1) << c.shift, cnt) - 1];
     } else {
       key = dmap[m >> c.shift];
-      fine = true;
     }
   };
-  const auto second = [&]() {
-    key2 = key;
+  const auto second = [&](int chunk) {
+    const int m = chunk * CP_TOK + tok;
     page = -1;
-    if (!fine) return;
-    if (finds) page = table[key >> c.shift];
-    else page = key <= -2 ? w.list[off - 2 - key] : key;
+    if (m >= cnt) return;
+    key2 = key;
+    if (finds) {
+      // a page whose last kept token stays was planned as unchanged (it may be shared): none may move
+      const int last = min(((m >> c.shift) + 1) << c.shift, cnt) - 1;
+      if (key >= m && key < n && key > before && (key == m || last_key != last)) page = table[key >> c.shift];
+    } else {
+      page = key <= -2 ? w.list[off - 2 - key] : key;
+    }
   };
-  const auto place = [&](int chunk) {        // what second() found, for everybody
+  const auto place = [&](int chunk) {
     const int m = chunk * CP_TOK + tok;
     if (m >= cnt) page = -1;
     else if (!page_ok(page, c)) bad = true;
-    const int o = finds ? key2 & (c.ps - 1) : m & (c.ps - 1);
-    (finds ? from : to)[(chunk % C::SLOTS) * CP_TOK + tok] = page_ok(page, c) ? page * pgs + o * ts : -1;
+    const int at = (chunk % C::SLOTS) * CP_TOK + tok, o = finds ? key2 & (c.ps - 1) : m & (c.ps - 1);
+    (finds ? from : to)[at] = page_ok(page, c) ? page * pgs + o * ts : -1;
+    if (finds) index_sh[at] = key2;
   };
 
   first(0);
-  second();
+  second(0);
   first(1);
   place(0);
-  second();
+  second(1);
   first(2);
   __syncthreads();
   for (int i = 0; i < chunks + CP_STAGES - 1; ++i) {
     if (i + 1 < chunks) place(i + 1);
-    second();
+    second(i + 2);
     first(i + 3);
     if (i < chunks) {
       const int64_t* f = from + (i % C::SLOTS) * CP_TOK;
@@ -489,9 +536,9 @@ __global__ void __launch_bounds__(CP_THREADS) compact_pages_kernel(const PagedVi
         if (a >= 0 && b >= 0 && a != b) cp_async16(dst + e * 16, base + a + (e % VPS) * 16);
       }
       if (side && finds) {
-        const int m = i * CP_TOK + tok;
-        if (f[tok] >= 0 && t[tok] >= 0 && idx[m] != m)
-          cp_async4(side_ring + ((i % CP_STAGES) * CP_TOK + tok) * 4, side + (size_t)idx[m] * 4);
+        const int m = i * CP_TOK + tok, j = index_sh[(i % C::SLOTS) * CP_TOK + tok];
+        if (f[tok] >= 0 && t[tok] >= 0 && j != m)
+          cp_async4(side_ring + ((i % CP_STAGES) * CP_TOK + tok) * 4, side + (size_t)j * 4);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -510,7 +557,7 @@ __global__ void __launch_bounds__(CP_THREADS) compact_pages_kernel(const PagedVi
       }
       if (side && finds) {
         const int m = d * CP_TOK + tok;
-        if (f[tok] >= 0 && t[tok] >= 0 && idx[m] != m)
+        if (f[tok] >= 0 && t[tok] >= 0 && index_sh[(d % C::SLOTS) * CP_TOK + tok] != m)
           *reinterpret_cast<uint32_t*>(side + (size_t)m * 4) = side_sh[(d % CP_STAGES) * CP_TOK + tok];
       }
     }
@@ -518,17 +565,17 @@ __global__ void __launch_bounds__(CP_THREADS) compact_pages_kernel(const PagedVi
   if (bad) raise_status(w.status, KVP_ERR_DEVICE_CHECK);
   cluster.sync();                            // every CTA has read the row's table and length
   const int old_pages = pages_of(n, c), new_pages = pages_of(cnt, c);
-  for (int j = rank * CP_THREADS + tid; j < old_pages; j += nranks * CP_THREADS) {
+  release_pages(c, rank * CP_THREADS + tid, old_pages, nranks * CP_THREADS, w.status, [&](int j) {
     const int p = table[j];
     int d = j < new_pages ? dmap[j] : -1;
-    if (p == d) continue;
+    if (p == d) return j < new_pages ? -1 : c.n_pages;         // the page stays; or no page where one should be
     if (d <= -2) {
       d = w.list[off - 2 - d];
       c.refs[d] = 1;
     }
     c.table[(size_t)r * c.max_pages + j] = d;
-    release_page(c, p, w.status);
-  }
+    return p == -1 ? c.n_pages : p;
+  });
   if (rank == 0 && tid == 0) c.lens[r] = cnt;
 }
 
@@ -560,7 +607,7 @@ __global__ void __launch_bounds__(256) fork_kernel(const PagedView c, const int3
 }
 
 // Row r keeps its first keep[r] tokens; one CTA per row.
-__global__ void __launch_bounds__(256) free_kernel(const PagedView c, const int32_t* __restrict__ keep, int* status) {
+__global__ void __launch_bounds__(512) free_kernel(const PagedView c, const int32_t* __restrict__ keep, int* status) {
   wait_prior_grid();
   const int r = blockIdx.x;
   const int kept = keep ? keep[r] : 0;
@@ -571,10 +618,12 @@ __global__ void __launch_bounds__(256) free_kernel(const PagedView c, const int3
     return;
   }
   __syncthreads();                           // every thread has read the length
-  for (int j = pages_of(kept, c) + threadIdx.x; j < pages_of(n, c); j += blockDim.x) {
-    release_page(c, table_row(c, r)[j], status);
-    table_row(c, r)[j] = -1;
-  }
+  int32_t* table = table_row(c, r);
+  release_pages(c, pages_of(kept, c) + threadIdx.x, pages_of(n, c), blockDim.x, status, [&](int j) {
+    const int p = table[j];
+    table[j] = -1;
+    return p == -1 ? c.n_pages : p;          // a live entry names a page
+  });
   if (threadIdx.x == 0) c.lens[r] = kept;
 }
 
@@ -689,13 +738,17 @@ cudaError_t launch_paged_append(const PagedView& c, const PagedNew& n, void* ws,
   const int elt = c.dtype == KVP_F32 ? 4 : 2, vpr = c.D * elt / 16;
   const long long tokens = (long long)n.n_new * c.R;
   const FastDiv by_new = fast_div((uint32_t)n.n_new), by_heads = fast_div((uint32_t)n.h_kv);
-  // small appends: a block per row for the shared tails, a thread per vector for the new tokens
+  // a block per row at least, for the shared tails
+  const bool wide = tokens * vpr > 8LL * 256 * sm_count();
   const dim3 grid(blocks_for(tokens * vpr > 256LL * c.R ? tokens * vpr : 256LL * c.R, 8));
   count_launches(1);
+  const auto go = [&](auto kernel) {
+    return launch_with_pdl(kernel, grid, dim3(256), 0, st, c, n, a, elt, by_new, by_heads, tokens);
+  };
   switch (vpr) {
-    case 8: return launch_with_pdl(append_copy_kernel<8>, grid, dim3(256), 0, st, c, n, a, elt, by_new, by_heads, tokens);
-    case 16: return launch_with_pdl(append_copy_kernel<16>, grid, dim3(256), 0, st, c, n, a, elt, by_new, by_heads, tokens);
-    default: return launch_with_pdl(append_copy_kernel<32>, grid, dim3(256), 0, st, c, n, a, elt, by_new, by_heads, tokens);
+    case 8: return wide ? go(append_copy_kernel<8, 4>) : go(append_copy_kernel<8, 1>);
+    case 16: return wide ? go(append_copy_kernel<16, 4>) : go(append_copy_kernel<16, 1>);
+    default: return wide ? go(append_copy_kernel<32, 4>) : go(append_copy_kernel<32, 1>);
   }
 }
 
@@ -747,13 +800,13 @@ cudaError_t launch_paged_compact(const PagedView& c, const int32_t* idx, const i
   e = launch_plan<PLAN_COMPACT>(c, a, st);
   if (e != cudaSuccess) return e;
   const int elt = c.dtype == KVP_F32 ? 4 : 2, vpr = c.D * elt / 16;
-  // 128 bytes of a token per CTA: a full line, and up to four CTAs share K (or V) of a row
+  // 128 bytes of a token per CTA
   return launch_compact_pages<8>(c, a, elt, vpr / 8, st);
 }
 
 cudaError_t launch_paged_free(const PagedView& c, const int32_t* keep, int* status, cudaStream_t st) {
   count_launches(1);
-  return launch_with_pdl(free_kernel, dim3((unsigned)c.R), dim3(256), 0, st, c, keep, status);
+  return launch_with_pdl(free_kernel, dim3((unsigned)c.R), dim3(512), 0, st, c, keep, status);
 }
 
 }  // namespace kvp
