@@ -139,6 +139,7 @@ constexpr int NEED_THREADS = 128;
 
 __global__ void __launch_bounds__(NEED_THREADS) compact_need_kernel(const PagedView c, const PlanArgs a) {
   __shared__ int scan_sh[33];
+  allow_next_grid();                         // the plan and the copies wait for their turn on the GPU already
   wait_prior_grid();
   const int r = blockIdx.x, tid = threadIdx.x;
   const int cnt = a.count[r], n = c.lens[r];
@@ -172,8 +173,9 @@ template <int MODE>
 __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const PagedView c, const PlanArgs a) {
   __shared__ int scan_sh[33];
   __shared__ int used_sh;
-  __shared__ uint32_t word_sh[PLAN_WORDS * PLAN_THREADS];
-  __shared__ int rank_sh[PLAN_WORDS * PLAN_THREADS];
+  // a word of padding per 32: below, the lanes of a warp read words 32 apart
+  __shared__ uint32_t word_sh[PLAN_WORDS * PLAN_THREADS * 33 / 32];
+  __shared__ int rank_sh[PLAN_WORDS * PLAN_THREADS * 33 / 32];
   wait_prior_grid();
   const int tid = threadIdx.x, lane = tid & 31;
   const int words = (c.n_pages + 31) >> 5;
@@ -218,23 +220,38 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const PagedVie
     // that a run of free pages is written by the whole CTA, in consecutive entries of the list
 #pragma unroll
     for (int k = 0; k < PLAN_WORDS; ++k) {
-      word_sh[PLAN_WORDS * tid + k] = mask[k];
-      rank_sh[PLAN_WORDS * tid + k] = at;
+      const int x = PLAN_WORDS * tid + k;
+      word_sh[x + (x >> 5)] = mask[k];
+      rank_sh[x + (x >> 5)] = at;
       at += __popc(mask[k]);
     }
     __syncthreads();
+#pragma unroll 1
     for (int i = 0; i < PLAN_WORDS; ++i) {
       const int mine_x = (i * 32 + lane) * (PLAN_THREADS / 32) + (tid >> 5);
-      uint32_t some = __ballot_sync(0xffffffffu, word_sh[mine_x] != 0 && rank_sh[mine_x] < want);
-      while (some) {
-        const int x = (i * 32 + __ffs(some) - 1) * (PLAN_THREADS / 32) + (tid >> 5);
+      const uint32_t v = word_sh[mine_x + (mine_x >> 5)];
+      const int to = rank_sh[mine_x + (mine_x >> 5)];
+      const bool mine_taken = v != 0 && to < want;
+      uint32_t some = __ballot_sync(0xffffffffu, mine_taken);
+      while (some) {                         // two words at a time: their chains of shuffles overlap
+        const int l0 = __ffs(some) - 1;
         some &= some - 1;
-        const uint32_t v = word_sh[x];
-        const int to = rank_sh[x] + __popc(v & ((1u << lane) - 1u));
-        const bool taken = ((v >> lane) & 1u) && to < want;
-        if (taken) a.list[to] = (base + x) * 32 + lane;
-        const uint32_t gone = __ballot_sync(0xffffffffu, taken);
-        if (lane == 0) c.free_mask[base + x] = v & ~gone;
+        const int l1 = some ? __ffs(some) - 1 : l0;
+        some &= some - 1;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int l = k == 0 ? l0 : l1;
+          const uint32_t word = __shfl_sync(0xffffffffu, v, l);
+          const int at_bit = __shfl_sync(0xffffffffu, to, l) + __popc(word & ((1u << lane) - 1u));
+          const int x = (i * 32 + l) * (PLAN_THREADS / 32) + (tid >> 5);
+          if (((word >> lane) & 1u) && at_bit < want) a.list[at_bit] = (base + x) * 32 + lane;
+        }
+      }
+      if (mine_taken) {                      // the word without the pages taken: its lowest ones
+        uint32_t rest = v;
+        if (to + __popc(v) <= want) rest = 0;
+        else for (int k = to; k < want; ++k) rest &= rest - 1;
+        c.free_mask[base + mine_x] = rest;
       }
     }
     found += all;
@@ -274,8 +291,10 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const PagedVie
       }
     }
     if (MODE == PLAN_COPY) {                 // the owner of each page, a warp per row
-      for (int i = 0; i < 32; ++i) {
-        const int need = __shfl_sync(0xffffffffu, r < c.R ? w.need : 0, i), o = __shfl_sync(0xffffffffu, off, i);
+      const int mine = r < c.R ? w.need : 0;
+      for (uint32_t some = __ballot_sync(0xffffffffu, mine > 0); some; some &= some - 1) {
+        const int i = __ffs(some) - 1;
+        const int need = __shfl_sync(0xffffffffu, mine, i), o = __shfl_sync(0xffffffffu, off, i);
         for (int k = lane; k < need; k += 32) a.owner[o + k] = base + (tid & ~31) + i;
       }
     }
@@ -421,23 +440,25 @@ __global__ void __launch_bounds__(256) pages_copy_kernel(const PagedView c, cons
 // up to some m has landed, the slots up to m can be written without touching a token that is still
 // to be read, and the loads of later tokens may be under way at any time.  So chunks of tokens stream
 // through a ring in shared memory (cp.async), written in order, one barrier per chunk: loads of
-// CP_STAGES - 1 chunks are in flight while one is stored.  Where a token lies takes two dependent reads
-// (index, table); they run two chunks ahead of the copies, in registers.  The columns of a token
+// STAGES - 1 chunks are in flight while one is stored.  Where a token lies takes two dependent reads
+// (index, table); they are made for eight chunks at a time, one group ahead of the copies.  The columns of a token
 // (16-byte vectors of K and of V) do not depend on each other, so a cluster of CTAs shares a row by
 // columns.  At the end the cluster gives the row its new pages.
-constexpr int CP_THREADS = 256;
-constexpr int CP_TOK = 128;                // tokens per chunk: a thread of each half of the CTA looks one up
-constexpr int CP_STAGES = 4;
+constexpr int CP_THREADS = 512;
+constexpr int CP_TOK = 128;                // tokens per chunk
+constexpr int CP_GROUP = 8;                // chunks whose tokens are looked up together
 
 template <int VPS>   // 16-byte vectors of a token per CTA
 struct Cp {
+  static constexpr int STAGES = VPS == 16 ? 3 : 4;
   static constexpr int STAGE = CP_TOK * VPS * 16;
-  static constexpr int SLOTS = CP_STAGES + 2;              // chunks whose places are kept
-  static constexpr int OFF_FROM = CP_STAGES * STAGE;       // int64 [SLOTS][CP_TOK] source and target offsets
-  static constexpr int OFF_TO = OFF_FROM + SLOTS * CP_TOK * 8;
-  static constexpr int OFF_INDEX = OFF_TO + SLOTS * CP_TOK * 8;  // int32 [SLOTS][CP_TOK] source tokens
-  static constexpr int OFF_SIDE = OFF_INDEX + SLOTS * CP_TOK * 4;   // [CP_STAGES][CP_TOK] 4 bytes
-  static constexpr int SMEM = OFF_SIDE + CP_STAGES * CP_TOK * 4;
+  static constexpr int PLACES = 2 * CP_GROUP * CP_TOK;     // tokens whose places are kept: two groups
+  static constexpr int LOOKS = CP_GROUP * CP_TOK / CP_THREADS;
+  static constexpr int OFF_PLACE = STAGES * STAGE;      // [PLACES] source and target offsets
+  static constexpr int OFF_INDEX = OFF_PLACE + PLACES * 16;     // int32 [PLACES] source tokens
+  static constexpr int OFF_SIDE = OFF_INDEX + PLACES * 4;  // [STAGES][CP_TOK] 4 bytes
+  static constexpr int SMEM = OFF_SIDE + STAGES * CP_TOK * 4;
+  static_assert(STAGES <= CP_GROUP - 2, "a group's places are overwritten once its last chunk is stored");
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
@@ -467,98 +488,100 @@ __global__ void __launch_bounds__(CP_THREADS) compact_pages_kernel(const PagedVi
   // scores move with the first CTA's columns, positions with the last one's
   char* side = rank == 0 ? (char*)c.score : rank == nranks - 1 ? (char*)c.pos : nullptr;
   if (side) side += (size_t)r * c.cap * 4;
-  int64_t* from = reinterpret_cast<int64_t*>(smem + C::OFF_FROM);
-  int64_t* to = reinterpret_cast<int64_t*>(smem + C::OFF_TO);
+  longlong2* places = reinterpret_cast<longlong2*>(smem + C::OFF_PLACE);   // x: source, y: target; -1: stays
   int32_t* index_sh = reinterpret_cast<int32_t*>(smem + C::OFF_INDEX);
   uint32_t* side_sh = reinterpret_cast<uint32_t*>(smem + C::OFF_SIDE);
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem);
   const uint32_t side_ring = ring + C::OFF_SIDE;
   const int chunks = (cnt + CP_TOK - 1) / CP_TOK;
-  const int tok = tid & (CP_TOK - 1);
-  const bool finds = tid < CP_TOK;           // this thread finds a token's source (the others: its target)
   bool bad = false;
 
-  // Two reads behind each other, an iteration apart: what first() loads, second() looks at, and what
-  // second() loads, place() writes down.  Nothing is waited for in the iteration that asks for it.
-  int key = 0, before = 0, last_key = 0;     // source: idx[m], idx[m - 1], idx at the end of the page; target: dmap
-  int page = -1, key2 = 0;
-  const auto first = [&](int chunk) {
-    const int m = chunk * CP_TOK + tok;
-    if (m >= cnt) return;
-    if (finds) {
-      key = idx[m];
-      before = m > 0 ? idx[m - 1] : -1;
-      last_key = idx[min(((m >> c.shift) + 1) << c.shift, cnt) - 1];
-    } else {
-      key = dmap[m >> c.shift];
+  // A group's look-ups: what ask() loads, find() looks at some chunks later; what find() loads, place()
+  // writes down some chunks after that.  Nothing is waited for where it is asked for.
+  int key[C::LOOKS], before[C::LOOKS], last_key[C::LOOKS], target[C::LOOKS], page[C::LOOKS];
+  const auto ask = [&](int group) {
+#pragma unroll
+    for (int x = 0; x < C::LOOKS; ++x) {
+      const int m = group * CP_GROUP * CP_TOK + x * CP_THREADS + tid;
+      key[x] = before[x] = last_key[x] = target[x] = -1;
+      if (m >= cnt) continue;
+      key[x] = idx[m];
+      if (m > 0) before[x] = idx[m - 1];
+      last_key[x] = idx[min(((m >> c.shift) + 1) << c.shift, cnt) - 1];
+      target[x] = dmap[m >> c.shift];
     }
   };
-  const auto second = [&](int chunk) {
-    const int m = chunk * CP_TOK + tok;
-    page = -1;
-    if (m >= cnt) return;
-    key2 = key;
-    if (finds) {
+  const auto find = [&](int group) {
+#pragma unroll
+    for (int x = 0; x < C::LOOKS; ++x) {
+      const int m = group * CP_GROUP * CP_TOK + x * CP_THREADS + tid;
       // a page whose last kept token stays was planned as unchanged (it may be shared): none may move
       const int last = min(((m >> c.shift) + 1) << c.shift, cnt) - 1;
-      if (key >= m && key < n && key > before && (key == m || last_key != last)) page = table[key >> c.shift];
-    } else {
-      page = key <= -2 ? w.list[off - 2 - key] : key;
+      page[x] = -1;
+      if (m < cnt && key[x] >= m && key[x] < n && key[x] > before[x] && (key[x] == m || last_key[x] != last))
+        page[x] = table[key[x] >> c.shift];
+      if (target[x] <= -2) target[x] = w.list[off - 2 - target[x]];
     }
   };
-  const auto place = [&](int chunk) {
-    const int m = chunk * CP_TOK + tok;
-    if (m >= cnt) page = -1;
-    else if (!page_ok(page, c)) bad = true;
-    const int at = (chunk % C::SLOTS) * CP_TOK + tok, o = finds ? key2 & (c.ps - 1) : m & (c.ps - 1);
-    (finds ? from : to)[at] = page_ok(page, c) ? page * pgs + o * ts : -1;
-    if (finds) index_sh[at] = key2;
+  const auto place = [&](int group) {
+#pragma unroll
+    for (int x = 0; x < C::LOOKS; ++x) {
+      const int m = group * CP_GROUP * CP_TOK + x * CP_THREADS + tid, at = m & (C::PLACES - 1);
+      longlong2 z = make_longlong2(-1, -1);
+      if (m < cnt) {
+        if (page_ok(page[x], c) && page_ok(target[x], c)) {
+          z.x = page[x] * pgs + (key[x] & (c.ps - 1)) * ts;
+          z.y = target[x] * pgs + (m & (c.ps - 1)) * ts;
+          if (z.x == z.y) z.x = z.y = -1;
+        } else {
+          bad = true;
+        }
+      }
+      places[at] = z;
+      index_sh[at] = key[x];
+    }
   };
 
-  first(0);
-  second(0);
-  first(1);
+  ask(0);
+  find(0);
   place(0);
-  second(1);
-  first(2);
   __syncthreads();
-  for (int i = 0; i < chunks + CP_STAGES - 1; ++i) {
-    if (i + 1 < chunks) place(i + 1);
-    second(i + 2);
-    first(i + 3);
+  for (int i = 0; i < chunks + C::STAGES - 1; ++i) {
+    const int group = i / CP_GROUP + 1;
+    if (i % CP_GROUP == 0) ask(group);
+    if (i % CP_GROUP == CP_GROUP / 2 - 1) find(group);
+    if (i % CP_GROUP == CP_GROUP - 2) place(group);
     if (i < chunks) {
-      const int64_t* f = from + (i % C::SLOTS) * CP_TOK;
-      const int64_t* t = to + (i % C::SLOTS) * CP_TOK;
-      const uint32_t dst = ring + (i % CP_STAGES) * C::STAGE;
+      const int t0 = (i * CP_TOK) & (C::PLACES - 1);
+      const uint32_t dst = ring + (i % C::STAGES) * C::STAGE;
 #pragma unroll
       for (int e = tid; e < CP_TOK * VPS; e += CP_THREADS) {
-        const int64_t a = f[e / VPS], b = t[e / VPS];
-        if (a >= 0 && b >= 0 && a != b) cp_async16(dst + e * 16, base + a + (e % VPS) * 16);
+        const long long from = places[t0 + e / VPS].x;
+        if (from >= 0) cp_async16(dst + e * 16, base + from + (e % VPS) * 16);
       }
-      if (side && finds) {
-        const int m = i * CP_TOK + tok, j = index_sh[(i % C::SLOTS) * CP_TOK + tok];
-        if (f[tok] >= 0 && t[tok] >= 0 && j != m)
-          cp_async4(side_ring + ((i % CP_STAGES) * CP_TOK + tok) * 4, side + (size_t)j * 4);
+      if (side && tid < CP_TOK) {
+        const int j = index_sh[t0 + tid];
+        if (places[t0 + tid].x >= 0 && j != i * CP_TOK + tid)
+          cp_async4(side_ring + ((i % C::STAGES) * CP_TOK + tid) * 4, side + (size_t)j * 4);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
-    asm volatile("cp.async.wait_group %0;" ::"n"(CP_STAGES - 1) : "memory");
+    asm volatile("cp.async.wait_group %0;" ::"n"(C::STAGES - 1) : "memory");
     __syncthreads();                         // everybody's loads of the chunk below have landed
-    const int d = i - (CP_STAGES - 1);
+    const int d = i - (C::STAGES - 1);
     if (d >= 0) {
-      const int64_t* f = from + (d % C::SLOTS) * CP_TOK;
-      const int64_t* t = to + (d % C::SLOTS) * CP_TOK;
-      const uint8_t* src_sh = smem + (d % CP_STAGES) * C::STAGE;
+      const int t0 = (d * CP_TOK) & (C::PLACES - 1);
+      const uint8_t* src_sh = smem + (d % C::STAGES) * C::STAGE;
 #pragma unroll
       for (int e = tid; e < CP_TOK * VPS; e += CP_THREADS) {
-        const int64_t a = f[e / VPS], b = t[e / VPS];
-        if (a >= 0 && b >= 0 && a != b)
-          *reinterpret_cast<uint4*>(base + b + (e % VPS) * 16) = *reinterpret_cast<const uint4*>(src_sh + e * 16);
+        const long long to = places[t0 + e / VPS].y;
+        if (to >= 0)
+          *reinterpret_cast<uint4*>(base + to + (e % VPS) * 16) = *reinterpret_cast<const uint4*>(src_sh + e * 16);
       }
-      if (side && finds) {
-        const int m = d * CP_TOK + tok;
-        if (f[tok] >= 0 && t[tok] >= 0 && index_sh[(d % C::SLOTS) * CP_TOK + tok] != m)
-          *reinterpret_cast<uint32_t*>(side + (size_t)m * 4) = side_sh[(d % CP_STAGES) * CP_TOK + tok];
+      if (side && tid < CP_TOK) {
+        const int m = d * CP_TOK + tid;
+        if (places[t0 + tid].y >= 0 && index_sh[t0 + tid] != m)
+          *reinterpret_cast<uint32_t*>(side + (size_t)m * 4) = side_sh[(d % C::STAGES) * CP_TOK + tid];
       }
     }
   }
@@ -746,9 +769,9 @@ cudaError_t launch_paged_append(const PagedView& c, const PagedNew& n, void* ws,
     return launch_with_pdl(kernel, grid, dim3(256), 0, st, c, n, a, elt, by_new, by_heads, tokens);
   };
   switch (vpr) {
-    case 8: return wide ? go(append_copy_kernel<8, 4>) : go(append_copy_kernel<8, 1>);
-    case 16: return wide ? go(append_copy_kernel<16, 4>) : go(append_copy_kernel<16, 1>);
-    default: return wide ? go(append_copy_kernel<32, 4>) : go(append_copy_kernel<32, 1>);
+    case 8: return wide ? go(append_copy_kernel<8, 2>) : go(append_copy_kernel<8, 1>);
+    case 16: return wide ? go(append_copy_kernel<16, 2>) : go(append_copy_kernel<16, 1>);
+    default: return wide ? go(append_copy_kernel<32, 2>) : go(append_copy_kernel<32, 1>);
   }
 }
 
@@ -800,8 +823,12 @@ cudaError_t launch_paged_compact(const PagedView& c, const int32_t* idx, const i
   e = launch_plan<PLAN_COMPACT>(c, a, st);
   if (e != cudaSuccess) return e;
   const int elt = c.dtype == KVP_F32 ? 4 : 2, vpr = c.D * elt / 16;
-  // 128 bytes of a token per CTA
-  return launch_compact_pages<8>(c, a, elt, vpr / 8, st);
+  // Bytes of a token per CTA: 256 use DRAM best (120000 -> 16384 tokens of 56 rows 166 us, with 128
+  // bytes 200 us), if the rows are enough for some 100 CTAs; fewer rows are cut finer (8 rows 30000 ->
+  // 4096: 41 us with 256 bytes, 30 us with 128).
+  if (vpr >= 16 && (long long)c.R * (vpr / 8) >= 96) return launch_compact_pages<16>(c, a, elt, vpr / 16, st);
+  if (vpr == 32 || (long long)c.R * (vpr / 4) >= 48) return launch_compact_pages<8>(c, a, elt, vpr / 8, st);
+  return launch_compact_pages<4>(c, a, elt, vpr / 4, st);    // a cluster holds 8 CTAs: 4 for K, 4 for V
 }
 
 cudaError_t launch_paged_free(const PagedView& c, const int32_t* keep, int* status, cudaStream_t st) {

@@ -8,14 +8,15 @@ What only the device can see (a length or page out of range, no free page left) 
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
 
-from ._lib import _DTYPE, KVP_F32, _check, _dtype, _need, load
+from ._lib import _DTYPE, _check, _dtype, _need, load
 
-_NOTHING = contextlib.nullcontext()
+# a call costs the host a few microseconds; making a Stream object would be a third of them
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 class _Desc(ctypes.Structure):
@@ -75,6 +76,7 @@ class PagedCache:
                            None if score is None else score.data_ptr(), None if pos is None else pos.data_ptr(),
                            _dtype(k_pool), head_dim, page_size, n_pages, n_rows, max_pages)
         self._ref = ctypes.byref(self._desc)
+        self._index = self.device.index
         self._sizes = {}
 
     @classmethod
@@ -100,30 +102,29 @@ class PagedCache:
                           self.free_mask, cut(self.score), cut(self.pos))
 
     def _workspace(self, fn, *args):
-        """A workspace for one call (from the caching allocator: calls that overlap have their own)."""
+        """A workspace for one call (from the caching allocator: calls that overlap have their own):
+        (tensor, pointer, bytes)."""
         key = (fn, args)
         n = self._sizes.get(key)
         if n is None:
             n = self._sizes[key] = int(getattr(load(), fn + "_workspace_size")(self._ref, *args))
-        return torch.empty(n, dtype=torch.uint8, device=self.device) if n else None
+        if n == 0:
+            return None, None, 0
+        ws = torch.empty(n, dtype=torch.uint8, device=self.device)
+        return ws, ws.data_ptr(), n
 
     def _need(self, t, name, dtype, shape):
         _need(t, name, dtype, shape)
         if t.device != self.device:
             raise ValueError(f"{name} must be on {self.device}, got {t.device}")
 
+    def _elsewhere(self, stream):
+        """Whether the call has to be made under another device or stream than the current ones."""
+        return stream is not None or torch.cuda.current_device() != self._index
 
-def _on(cache, stream):
-    """The cache's device and the stream to launch on, made current: temporaries then belong to it."""
-    if stream is not None:
-        return torch.cuda.stream(stream)
-    if torch.cuda.current_device() != cache.device.index:
-        return torch.cuda.device(cache.device)
-    return _NOTHING
-
-
-def _raw_stream(cache):
-    return torch.cuda.current_stream(cache.device).cuda_stream
+    def _there(self, stream):
+        """Makes them current, so that the call's temporaries belong to the stream that uses them."""
+        return torch.cuda.stream(stream) if stream is not None else torch.cuda.device(self.device)
 
 
 def _cache(c):
@@ -134,88 +135,97 @@ def _cache(c):
 
 def kvp_paged_init(cache, stream=None):
     """Empty the cache: no row holds a page."""
-    with _on(_cache(cache), stream):
-        _check("kvp_paged_init", load().kvp_paged_init(cache._ref, _raw_stream(cache)))
+    if _cache(cache)._elsewhere(stream):
+        with cache._there(stream):
+            return kvp_paged_init(cache)
+    _check("kvp_paged_init", load().kvp_paged_init(cache._ref, _raw_stream(cache._index)))
 
 
 def _new_tokens(cache, t, name, like=None):
-    """[R, n_new, D] or [B, h_kv, n_new, D] with a contiguous last axis: (4-d view, strides or None)."""
+    """[R, n_new, D] or [B, h_kv, n_new, D] with a contiguous last axis: (h_kv, n_new, strides or None)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != cache.device:
         raise ValueError(f"{name} must be on {cache.device}, got {t.device}")
-    if t.dim() == 3:
-        t = t.unsqueeze(0)
-    if t.dim() != 4 or t.shape[0] * t.shape[1] != cache.n_rows or t.shape[3] != cache.head_dim:
-        raise ValueError(f"{name} must be [{cache.n_rows}, n_new, {cache.head_dim}] or [batch, h_kv, n_new, "
-                         f"{cache.head_dim}] with batch * h_kv = {cache.n_rows}, got {tuple(t.shape)}")
     if t.dtype != cache.dtype:
         raise ValueError(f"{name} must be {cache.dtype}, got {t.dtype}")
-    if like is not None and t.shape != like.shape:
-        raise ValueError(f"{name} must have shape {tuple(like.shape)}, got {tuple(t.shape)}")
+    shape = t.shape
+    if len(shape) == 3 and shape[0] == cache.n_rows and shape[2] == cache.head_dim:
+        h_kv, n_new = shape[0], shape[1]
+    elif len(shape) == 4 and shape[0] * shape[1] == cache.n_rows and shape[3] == cache.head_dim:
+        h_kv, n_new = shape[1], shape[2]
+    else:
+        raise ValueError(f"{name} must be [{cache.n_rows}, n_new, {cache.head_dim}] or [batch, h_kv, n_new, "
+                         f"{cache.head_dim}] with batch * h_kv = {cache.n_rows}, got {tuple(shape)}")
+    if like is not None and shape != like.shape:
+        raise ValueError(f"{name} must have shape {tuple(like.shape)}, got {tuple(shape)}")
     if t.is_contiguous():
-        return t, None
-    if t.stride(3) != 1:
+        return h_kv, n_new, None
+    strides = t.stride()
+    if strides[-1] != 1:
         raise ValueError(f"{name}: the head_dim axis must be contiguous")
-    return t, (ctypes.c_int64 * 3)(t.stride(0), t.stride(1), t.stride(2))
+    return h_kv, n_new, (ctypes.c_int64 * 3)(strides[0] if len(shape) == 4 else 0, strides[-3], strides[-2])
 
 
 def kvp_paged_append(cache, new_k, new_v, counts=None, new_pos=None, stream=None):
     """Append ``counts`` (int32 [R]; None: all) of the new tokens to every row: new_k, new_v
     [R, n_new, D] or [batch, h_kv, n_new, D] (strided views are read in place).  new_pos int32 [R]:
     the source position of each row's first new token, for a cache with ``pos``."""
-    k, ks = _new_tokens(_cache(cache), new_k, "new_k")
-    v, vs = _new_tokens(cache, new_v, "new_v", k)
+    if _cache(cache)._elsewhere(stream):
+        with cache._there(stream):
+            return kvp_paged_append(cache, new_k, new_v, counts, new_pos)
+    h_kv, n_new, ks = _new_tokens(cache, new_k, "new_k")
+    vs = _new_tokens(cache, new_v, "new_v", new_k)[2]
     if counts is not None:
         cache._need(counts, "counts", torch.int32, (cache.n_rows,))
     if new_pos is not None:
         cache._need(new_pos, "new_pos", torch.int32, (cache.n_rows,))
-    n_new = k.shape[2]
-    with _on(cache, stream):
-        ws = cache._workspace("kvp_paged_append", n_new)
-        rc = load().kvp_paged_append(cache._ref, k.data_ptr(), v.data_ptr(), ks, vs, k.shape[1], n_new,
-                                     None if counts is None else counts.data_ptr(),
-                                     None if new_pos is None else new_pos.data_ptr(),
-                                     None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
-                                     _raw_stream(cache))
+    ws, ws_ptr, ws_bytes = cache._workspace("kvp_paged_append", n_new)
+    rc = load().kvp_paged_append(cache._ref, new_k.data_ptr(), new_v.data_ptr(), ks, vs, h_kv, n_new,
+                                 None if counts is None else counts.data_ptr(),
+                                 None if new_pos is None else new_pos.data_ptr(), ws_ptr, ws_bytes,
+                                 _raw_stream(cache._index))
     _check("kvp_paged_append", rc)
 
 
 def kvp_paged_fork(cache, src, copy=False, stream=None):
     """Give every row r with src[r] >= 0 (int32 [R]) the tokens of row src[r]: on the same pages, or
     (copy) on fresh ones."""
-    _cache(cache)._need(src, "src", torch.int32, (cache.n_rows,))
+    if _cache(cache)._elsewhere(stream):
+        with cache._there(stream):
+            return kvp_paged_fork(cache, src, copy)
+    cache._need(src, "src", torch.int32, (cache.n_rows,))
     copy = int(bool(copy))
-    with _on(cache, stream):
-        ws = cache._workspace("kvp_paged_fork", copy)
-        rc = load().kvp_paged_fork(cache._ref, src.data_ptr(), copy, None if ws is None else ws.data_ptr(),
-                                   0 if ws is None else ws.numel(), _raw_stream(cache))
-    _check("kvp_paged_fork", rc)
+    ws, ws_ptr, ws_bytes = cache._workspace("kvp_paged_fork", copy)
+    _check("kvp_paged_fork", load().kvp_paged_fork(cache._ref, src.data_ptr(), copy, ws_ptr, ws_bytes,
+                                                   _raw_stream(cache._index)))
 
 
 def kvp_paged_compact(cache, idx, count, stream=None):
     """Keep, in place, the tokens idx [R, b_max] (int32, ascending) of every row, count [R] of them
     (negative: leave the row), and release the pages that empties."""
-    _cache(cache)._need(idx, "idx", torch.int32, None)
+    if _cache(cache)._elsewhere(stream):
+        with cache._there(stream):
+            return kvp_paged_compact(cache, idx, count)
+    cache._need(idx, "idx", torch.int32, None)
     if idx.dim() != 2 or idx.shape[0] != cache.n_rows:
         raise ValueError(f"idx must be [{cache.n_rows}, b_max], got {tuple(idx.shape)}")
     cache._need(count, "count", torch.int32, (cache.n_rows,))
     b_max = idx.shape[1]
-    with _on(cache, stream):
-        ws = cache._workspace("kvp_paged_compact", b_max)
-        rc = load().kvp_paged_compact(cache._ref, idx.data_ptr(), count.data_ptr(), b_max,
-                                      None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
-                                      _raw_stream(cache))
-    _check("kvp_paged_compact", rc)
+    ws, ws_ptr, ws_bytes = cache._workspace("kvp_paged_compact", b_max)
+    _check("kvp_paged_compact", load().kvp_paged_compact(cache._ref, idx.data_ptr(), count.data_ptr(), b_max, ws_ptr,
+                                                         ws_bytes, _raw_stream(cache._index)))
 
 
 def kvp_paged_free(cache, keep=None, stream=None):
     """Cut every row r to keep[r] tokens (int32 [R]; negative: leave the row; None: empty all rows)."""
+    if _cache(cache)._elsewhere(stream):
+        with cache._there(stream):
+            return kvp_paged_free(cache, keep)
     if keep is not None:
-        _cache(cache)._need(keep, "keep", torch.int32, (cache.n_rows,))
-    with _on(_cache(cache), stream):
-        rc = load().kvp_paged_free(cache._ref, None if keep is None else keep.data_ptr(), _raw_stream(cache))
-    _check("kvp_paged_free", rc)
+        cache._need(keep, "keep", torch.int32, (cache.n_rows,))
+    _check("kvp_paged_free", load().kvp_paged_free(cache._ref, None if keep is None else keep.data_ptr(),
+                                                   _raw_stream(cache._index)))
 
 
 def kvp_paged_decode_attn(q, cache, sm_scale=None, out=None, out_dtype=None, lse=None, return_lse=False,
@@ -224,41 +234,47 @@ def kvp_paged_decode_attn(q, cache, sm_scale=None, out=None, out_dtype=None, lse
     r = l * h_kv + h -> out [L, H_q, D] float32 (or ``out_dtype`` = the cache's dtype); with
     ``return_lse`` (out, lse float32 [L, H_q]).  ``add_scores`` adds every token's probability,
     summed over its group, to ``cache.score``."""
+    if _cache(cache)._elsewhere(stream):
+        with cache._there(stream):
+            return kvp_paged_decode_attn(q, cache, sm_scale, out, out_dtype, lse, return_lse, add_scores, workspace)
     if not isinstance(q, torch.Tensor):
         raise TypeError("q must be a torch.Tensor")
-    if q.device != _cache(cache).device:
+    if q.device != cache.device:
         raise ValueError(f"q must be on {cache.device}, got {q.device}")
-    if q.dim() != 3 or q.dtype != cache.dtype or q.shape[2] != cache.head_dim:
-        raise ValueError(f"q must be {cache.dtype} [n_layers, h_q, {cache.head_dim}], got {q.dtype} {tuple(q.shape)}")
-    L, Hq, D = q.shape
+    D = cache.head_dim
+    if q.dim() != 3 or q.dtype != cache.dtype or q.shape[2] != D:
+        raise ValueError(f"q must be {cache.dtype} [n_layers, h_q, {D}], got {q.dtype} {tuple(q.shape)}")
+    L, Hq, _ = q.shape
     if L < 1 or cache.n_rows % L:
         raise ValueError("the cache's rows must be n_layers * h_kv")
-    if not q.is_contiguous() and (q.stride(2) != 1 or (q.stride(1) != D and Hq > 1)):
-        raise ValueError("q: the head and head_dim axes must be contiguous")
-    q_stride = q.stride(0) if L > 1 else 0
-    if q_stride == 0 and L > 1:
-        raise ValueError("q: the layer axis must not be broadcast")
-    if sm_scale is None:
-        sm_scale = D ** -0.5
-    with _on(cache, stream):
-        if out is None:
-            out = torch.empty(L, Hq, D, dtype=torch.float32 if out_dtype is None else out_dtype, device=cache.device)
-        else:
-            cache._need(out, "out", out_dtype, (L, Hq, D))
-        if out.dtype not in _DTYPE:
-            raise ValueError(f"unsupported out dtype {out.dtype}")
-        if lse is not None:
-            cache._need(lse, "lse", torch.float32, (L, Hq))
-        elif return_lse:
-            lse = torch.empty(L, Hq, dtype=torch.float32, device=cache.device)
-        if workspace is None:
-            workspace = cache._workspace("kvp_paged_decode_attn", Hq, cache.n_rows // L, int(bool(add_scores)))
-        else:
-            cache._need(workspace, "workspace", torch.uint8, None)
-        rc = load().kvp_paged_decode_attn(q.data_ptr(), q_stride, cache._ref, Hq, cache.n_rows // L, float(sm_scale),
-                                          out.data_ptr(), KVP_F32 if out.dtype == torch.float32 else _DTYPE[out.dtype],
-                                          None if lse is None else lse.data_ptr(), int(bool(add_scores)),
-                                          None if workspace is None else workspace.data_ptr(),
-                                          0 if workspace is None else workspace.numel(), _raw_stream(cache))
+    q_stride = 0                                   # dense
+    if not q.is_contiguous():
+        if q.stride(2) != 1 or (q.stride(1) != D and Hq > 1):
+            raise ValueError("q: the head and head_dim axes must be contiguous")
+        if L > 1:
+            q_stride = q.stride(0)
+            if q_stride == 0:
+                raise ValueError("q: the layer axis must not be broadcast")
+    h_kv = cache.n_rows // L
+    add_scores = int(bool(add_scores))
+    if out is None:
+        out = torch.empty((L, Hq, D), dtype=out_dtype or torch.float32, device=cache.device)
+    else:
+        cache._need(out, "out", out_dtype, (L, Hq, D))
+    if out.dtype not in _DTYPE:
+        raise ValueError(f"unsupported out dtype {out.dtype}")
+    if lse is not None:
+        cache._need(lse, "lse", torch.float32, (L, Hq))
+    elif return_lse:
+        lse = torch.empty((L, Hq), dtype=torch.float32, device=cache.device)
+    if workspace is None:
+        workspace, ws_ptr, ws_bytes = cache._workspace("kvp_paged_decode_attn", Hq, h_kv, add_scores)
+    else:
+        cache._need(workspace, "workspace", torch.uint8, None)
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel()
+    rc = load().kvp_paged_decode_attn(q.data_ptr(), q_stride, cache._ref, Hq, h_kv,
+                                      D ** -0.5 if sm_scale is None else float(sm_scale), out.data_ptr(),
+                                      _DTYPE[out.dtype], None if lse is None else lse.data_ptr(), add_scores, ws_ptr,
+                                      ws_bytes, _raw_stream(cache._index))
     _check("kvp_paged_decode_attn", rc)
     return (out, lse) if return_lse else out

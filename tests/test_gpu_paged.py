@@ -206,7 +206,7 @@ def test_many_rows_and_pages(kvp):
     assert (c.free_mask.cpu().numpy() == paged.free_mask({"refs": own})).all()
 
 
-@pytest.mark.parametrize("dtype,D,R", [("f16", 128, 5), ("f32", 128, 3), ("f32", 64, 40), ("bf16", 64, 9)])
+@pytest.mark.parametrize("dtype,D,R", [("f16", 128, 5), ("f32", 128, 3), ("f32", 64, 40), ("bf16", 64, 9), ("f16", 128, 30), ("bf16", 128, 8)])
 def test_compact_long_rows(kvp, dtype, D, R):
     """Rows of many chunks, kept in long runs, single tokens and none; half of them share pages with others."""
     rng = np.random.default_rng(D + R)
