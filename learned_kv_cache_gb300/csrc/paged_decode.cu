@@ -18,25 +18,76 @@ using paged::Params;
 using paged::Range;
 using paged::TILE;
 
-constexpr int PD_WARPS = 4;
+// The kernel of fp32 caches (the tensor cores have no fp32 products).  4 G D FMAs per 8 D bytes: bound
+// by HBM up to some four query heads, by the FMA pipe's issue slots above, so what surrounds the FMAs is
+// kept small.  A group of LPK lanes reads KB keys at a time, 16 bytes of each per lane.  Summing the
+// KB * GP partial dot products over the lanes one by one would take log2(LPK) shuffles each; halving
+// exchanges (a lane passes on the half of its values that its partner keeps) take one each, and leave
+// every lane with the logit of one (key, head), so that the softmax is computed once and not LPK times.
+// The weights come back to all lanes through shared memory.
+template <int D, int GP>
+struct Pf {
+  static constexpr int LPK = D / 4;                        // lanes per key
+  static constexpr int SUBS = 32 / LPK;                    // groups of lanes in a warp, each with its own keys
+  static constexpr int KB = GP <= 4 ? 8 : 32 / GP;         // keys at a time: never across a page (16 slots)
+  static constexpr int V = KB * GP;                        // logits of a group at a time
+  static constexpr int WARPS = GP <= 4 ? 8 : 4;
+  static constexpr int THREADS = 32 * WARPS;
+  static constexpr int STATES = WARPS * SUBS;
+  static constexpr int HAVE = V > LPK ? V / LPK : 1;       // logits a lane ends up with
+  static constexpr int SAME = LPK > V ? LPK / V : 1;       // lanes that end up with the same one
+};
 
-// Each warp takes every fourth step of keys; a key's row is read by a group of lanes with 16-byte
-// loads, the partial dot products are summed across the group.
-template <typename T, int D, int GP>
-__global__ void __launch_bounds__(PD_WARPS * 32) paged_decode_kernel(const T* __restrict__ q, const Params p) {
-  constexpr int EV = 16 / sizeof(T), LPK = D / EV, KPW = 32 / LPK, UN = 4;
+// Sums v[0, V) over the LPK lanes of a group; lane l is left with the sums of values
+// [l * HAVE / SAME, ...) in v[0, HAVE).
+template <int V, int LPK>
+__device__ __forceinline__ void sum_scatter(float (&v)[V]) {
+  const int lane = threadIdx.x & 31;
+  int n = V;
+#pragma unroll
+  for (int s = LPK / 2; s > 0; s >>= 1) {
+    if (n > 1) {
+      n >>= 1;
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        if (i < n) {
+          const float keep = (lane & s) ? v[i + n] : v[i], pass = (lane & s) ? v[i] : v[i + n];
+          v[i] = keep + __shfl_xor_sync(0xffffffffu, pass, s);
+        }
+      }
+    } else {
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], s);
+    }
+  }
+}
+
+__device__ __forceinline__ float4 stream_float4(const float* p) {
+  const uint4 u = ld_stream16(p);
+  return make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
+}
+
+template <int D, int GP>
+__global__ void __launch_bounds__(Pf<D, GP>::THREADS, GP <= 8 ? 2 : 1)
+    paged_decode_f32_kernel(const float* __restrict__ q, const Params p) {
+  using C = Pf<D, GP>;
   __shared__ int scan_sh[41];
-  __shared__ float st_m[PD_WARPS][GP], st_l[PD_WARPS][GP];
-  __shared__ float st_o[PD_WARPS][GP][D];
+  __shared__ float st_m[C::STATES][GP], st_l[C::STATES][GP];
+  __shared__ __align__(16) float st_o[C::STATES][GP][D];
+  __shared__ __align__(16) float weight_sh[C::STATES][C::V];
+  __shared__ float factor_sh[C::STATES][GP];
   wait_prior_grid();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, sub = lane / LPK, dl = lane % LPK;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, dl = lane % C::LPK;
+  const int state = warp * C::SUBS + lane / C::LPK;
+  const int first_value = dl * C::HAVE / C::SAME;          // of this lane's logits
+  const int key_of = first_value / GP, head_of = first_value % GP;
+  const bool counts = dl % C::SAME == 0;                   // one of the lanes that have the same logit
   const int cta = blockIdx.x;
   const Range g = paged::find_range(p, cta, scan_sh);
-  paged::empty_rows<T, D>(p, cta);
+  paged::empty_rows<float, D>(p, cta);
   if (cta >= g.active) return;
   const PagedView& c = p.c;
-  const T* kp = (const T*)c.k + dl * EV;
-  const T* vp = (const T*)c.v + dl * EV;
+  const float* kp = (const float*)c.k + dl * 4;
+  const float* vp = (const float*)c.v + dl * 4;
 
   int r = g.row, u = g.tile;
   for (int x = g.begin; x < g.end;) {
@@ -49,119 +100,145 @@ __global__ void __launch_bounds__(PD_WARPS * 32) paged_decode_kernel(const T* __
     const int u1 = min(nt, u + (g.end - x));
     const int lo = u * TILE, hi = min(n, u1 * TILE);
     const int l = r / p.Hkv, hk = r % p.Hkv;
-    float qf[GP][EV], mx[GP], sm[GP], o[GP][EV];
+    float4 qf[GP], o[GP];
+    float mx[C::HAVE], sum[C::HAVE], lost[C::HAVE];        // of this lane's heads; lost: what sum rounds off
 #pragma unroll
     for (int h = 0; h < GP; ++h) {
-      mx[h] = -INFINITY;
-      sm[h] = 0.f;
-      uint4 w = make_uint4(0, 0, 0, 0);
-      if (h < p.G) w = *reinterpret_cast<const uint4*>(q + l * p.q_stride + (size_t)(hk * p.G + h) * D + dl * EV);
-      Vec16<T>::unpack(w, qf[h]);
+      qf[h] = o[h] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (h < p.G) qf[h] = *reinterpret_cast<const float4*>(q + l * p.q_stride + (size_t)(hk * p.G + h) * D + dl * 4);
+    }
 #pragma unroll
-      for (int t = 0; t < EV; ++t) o[h][t] = 0.f;
+    for (int i = 0; i < C::HAVE; ++i) {
+      mx[i] = -INFINITY;
+      sum[i] = lost[i] = 0.f;
     }
     const int32_t* table = c.table + (size_t)r * c.max_pages;
-    for (int m0 = lo; m0 < hi; m0 += PD_WARPS * KPW * UN) {
-      uint4 ku[UN], vu[UN];
-      bool ok[UN];
+    constexpr int STEP = C::STATES * C::KB;
+    int m = lo + state * C::KB;
+    int page = m < hi ? table[m >> c.shift] : 0;
+    for (int m0 = lo; m0 < hi; m0 += STEP, m += STEP) {
+      const int next = m + STEP < hi ? table[(m + STEP) >> c.shift] : 0;
+      const bool good = page >= 0 && page < c.n_pages;
+      if (m < hi && !good) raise_status(p.status, KVP_ERR_DEVICE_CHECK);
+      const int64_t at = page * c.page_stride + (m & (c.ps - 1)) * c.token_stride;
+      float4 k[C::KB], v[C::KB];
 #pragma unroll
-      for (int s = 0; s < UN; ++s) {
-        const int m = m0 + (s * PD_WARPS + warp) * KPW + sub;
-        ok[s] = m < hi;
-        ku[s] = vu[s] = make_uint4(0, 0, 0, 0);
-        if (ok[s]) {
-          const int pg = table[m >> c.shift];
-          ok[s] = pg >= 0 && pg < c.n_pages;
-          if (ok[s]) {
-            const int64_t at = pg * c.page_stride + (m & (c.ps - 1)) * c.token_stride;
-            ku[s] = ld_stream16(kp + at);
-            vu[s] = ld_stream16(vp + at);
-          } else {
-            raise_status(p.status, KVP_ERR_DEVICE_CHECK);
-          }
-        }
+      for (int i = 0; i < C::KB; ++i) {
+        const bool live = good && m + i < hi;
+        k[i] = v[i] = make_float4(0.f, 0.f, 0.f, 0.f);     // slots behind the row's end are not read
+        if (live) k[i] = stream_float4(kp + at + i * c.token_stride);
       }
 #pragma unroll
-      for (int s = 0; s < UN; ++s) {
-        const int m = m0 + (s * PD_WARPS + warp) * KPW + sub;
-        float kf[EV], vf[EV];
-        Vec16<T>::unpack(ku[s], kf);
-        Vec16<T>::unpack(vu[s], vf);
+      for (int i = 0; i < C::KB; ++i)
+        if (good && m + i < hi) v[i] = stream_float4(vp + at + i * c.token_stride);
+      page = next;
+      float s[C::V];
+#pragma unroll
+      for (int i = 0; i < C::KB; ++i)
+#pragma unroll
+        for (int h = 0; h < GP; ++h)
+          s[i * GP + h] = fmaf(qf[h].x, k[i].x, fmaf(qf[h].y, k[i].y, fmaf(qf[h].z, k[i].z, qf[h].w * k[i].w)));
+      sum_scatter<C::V, C::LPK>(s);
+      // this lane's logits, the new maxima of their heads (over the group's keys), the weights
+      float w[C::HAVE], top[C::HAVE];
+      bool grew = false;
+#pragma unroll
+      for (int i = 0; i < C::HAVE; ++i) {
+        w[i] = good && m + key_of < hi ? fmaf(s[i], p.c2, s[i] * p.c2_low) : -INFINITY;
+        if (p.logits && counts && good && m + key_of < hi && head_of + i < p.G)
+          p.logits[((size_t)r * c.cap + m + key_of) * p.gpad + head_of + i] = w[i];
+        top[i] = w[i];
+      }
+#pragma unroll
+      for (int b = C::SAME * GP / C::HAVE; b < C::LPK; b <<= 1)
+#pragma unroll
+        for (int i = 0; i < C::HAVE; ++i) top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], b));
+#pragma unroll
+      for (int i = 0; i < C::HAVE; ++i) {
+        top[i] = fmaxf(top[i], mx[i]);
+        grew |= top[i] > mx[i];
+      }
+      if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+        for (int i = 0; i < C::HAVE; ++i) {
+          const float f = paged::weight(mx[i], top[i]);
+          sum[i] *= f;
+          lost[i] *= f;
+          mx[i] = top[i];
+          if (counts && key_of == 0) factor_sh[state][head_of + i] = f;
+        }
+        __syncwarp();
 #pragma unroll
         for (int h = 0; h < GP; ++h) {
-          if (h >= p.G) break;
-          float a = 0.f;
-#pragma unroll
-          for (int t = 0; t < EV; ++t) a = fmaf(qf[h][t], kf[t], a);
-#pragma unroll
-          for (int off = LPK / 2; off > 0; off >>= 1) a += __shfl_xor_sync(0xffffffffu, a, off);
-          a = paged::base2(p, a);
-          if (!ok[s]) continue;
-          if (p.logits && dl == 0) p.logits[((size_t)r * c.cap + m) * GP + h] = a;
-          if (a > mx[h]) {
-            const float f = fast_exp2(mx[h] - a);
-            sm[h] *= f;
-#pragma unroll
-            for (int t = 0; t < EV; ++t) o[h][t] *= f;
-            mx[h] = a;
-          }
-          const float w = a == -INFINITY ? 0.f : fast_exp2(a - mx[h]);
-          sm[h] += w;
-#pragma unroll
-          for (int t = 0; t < EV; ++t) o[h][t] = fmaf(w, vf[t], o[h][t]);
+          const float f = factor_sh[state][h];
+          o[h].x *= f;
+          o[h].y *= f;
+          o[h].z *= f;
+          o[h].w *= f;
         }
       }
-    }
-    // the lane groups of a warp, then the warps
 #pragma unroll
-    for (int h = 0; h < GP; ++h) {
-      if (h >= p.G) break;
-      float M = mx[h];
-#pragma unroll
-      for (int off = LPK; off < 32; off <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-      const float f = paged::weight(mx[h], M);
-      float s = sm[h] * f;
-#pragma unroll
-      for (int off = LPK; off < 32; off <<= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-      if (lane == 0) {
-        st_m[warp][h] = M;
-        st_l[warp][h] = s;
+      for (int i = 0; i < C::HAVE; ++i) {
+        w[i] = w[i] == -INFINITY ? 0.f : fast_exp2(w[i] - mx[i]);
+        const float to = sum[i] + w[i];
+        lost[i] += w[i] - (to - sum[i]);
+        sum[i] = to;
+        if (counts) weight_sh[state][first_value + i] = w[i];
       }
+      __syncwarp();
 #pragma unroll
-      for (int t = 0; t < EV; ++t) {
-        float y = o[h][t] * f;
+      for (int i = 0; i < C::KB; ++i)
 #pragma unroll
-        for (int off = LPK; off < 32; off <<= 1) y += __shfl_xor_sync(0xffffffffu, y, off);
-        if (sub == 0) st_o[warp][h][dl * EV + t] = y;
+        for (int h = 0; h < GP; ++h) {
+          const float f = weight_sh[state][i * GP + h];
+          o[h].x = fmaf(f, v[i].x, o[h].x);
+          o[h].y = fmaf(f, v[i].y, o[h].y);
+          o[h].z = fmaf(f, v[i].z, o[h].z);
+          o[h].w = fmaf(f, v[i].w, o[h].w);
+        }
+      __syncwarp();                          // the weights are read
+    }
+    // the sums of the lanes that share a head, then the states of the CTA
+#pragma unroll
+    for (int i = 0; i < C::HAVE; ++i) {
+      float t = sum[i] + lost[i];
+#pragma unroll
+      for (int b = C::SAME * GP / C::HAVE; b < C::LPK; b <<= 1) t += __shfl_xor_sync(0xffffffffu, t, b);
+      if (counts && key_of == 0) {
+        st_m[state][head_of + i] = mx[i];
+        st_l[state][head_of + i] = t;
       }
     }
+#pragma unroll
+    for (int h = 0; h < GP; ++h)
+      if (h < p.G) *reinterpret_cast<float4*>(&st_o[state][h][dl * 4]) = o[h];
     __syncthreads();
     const bool whole = u == 0 && u1 == nt;
     float* part = p.part + ((size_t)cta * 2 + (u > 0 ? 0 : 1)) * p.pstride;
-    for (int e = tid; e < p.G * D; e += PD_WARPS * 32) {
+    for (int e = tid; e < p.G * D; e += C::THREADS) {
       const int h = e / D, d = e % D;
       float M = -INFINITY, L = 0.f, O = 0.f;
 #pragma unroll
-      for (int w = 0; w < PD_WARPS; ++w) M = fmaxf(M, st_m[w][h]);
+      for (int w = 0; w < C::STATES; ++w) M = fmaxf(M, st_m[w][h]);
 #pragma unroll
-      for (int w = 0; w < PD_WARPS; ++w) {
+      for (int w = 0; w < C::STATES; ++w) {
         const float f = paged::weight(st_m[w][h], M);
         L = fmaf(st_l[w][h], f, L);
         O = fmaf(st_o[w][h][d], f, O);
       }
       if (whole) {
         const size_t head = (size_t)l * p.Hq + hk * p.G + h;
-        paged::store_out<T>(p, head * D + d, L == 0.f ? 0.f : O / L);
+        reinterpret_cast<float*>(p.out)[head * D + d] = L == 0.f ? 0.f : O / L;
         if (d == 0) {
           const float l2 = L == 0.f ? -INFINITY : M + log2f(L);
           if (p.lse) p.lse[head] = l2 * KVP_LN2;
-          if (p.lse2) p.lse2[(size_t)r * GP + h] = l2;
+          if (p.lse2) p.lse2[(size_t)r * p.gpad + h] = l2;
         }
       } else {
-        part[2 * GP + e] = O;
+        part[2 * p.gpad + e] = O;
         if (d == 0) {
           part[h] = M;
-          part[GP + h] = L;
+          part[p.gpad + h] = L;
         }
       }
     }
@@ -170,6 +247,19 @@ __global__ void __launch_bounds__(PD_WARPS * 32) paged_decode_kernel(const T* __
     ++r;
     u = 0;
   }
+}
+
+template <int D>
+cudaError_t run_f32(const Params& p, const void* q, cudaStream_t st) {
+  const auto go = [&](auto kernel, int threads) {
+    count_launches(1);
+    return launch_with_pdl(kernel, dim3((unsigned)p.ctas), dim3((unsigned)threads), 0, st, (const float*)q, p);
+  };
+  if (p.G == 1) return go(paged_decode_f32_kernel<D, 1>, Pf<D, 1>::THREADS);
+  if (p.G == 2) return go(paged_decode_f32_kernel<D, 2>, Pf<D, 2>::THREADS);
+  if (p.G <= 4) return go(paged_decode_f32_kernel<D, 4>, Pf<D, 4>::THREADS);
+  if (p.G <= 8) return go(paged_decode_f32_kernel<D, 8>, Pf<D, 8>::THREADS);
+  return go(paged_decode_f32_kernel<D, 16>, Pf<D, 16>::THREADS);
 }
 
 // Merges the partials of the rows that several CTAs share, and adds the tokens' probabilities to the
@@ -345,6 +435,7 @@ size_t layout(const PagedView& c, int G, int add_scores, Params* p, void* ws) {
     return x;
   };
   p->ctas = ctas;
+  p->gpad = GP;
   p->pstride = 2 * GP + GP * c.D;
   p->part = (float*)take((size_t)ctas * 2 * p->pstride * 4);
   p->range = (Range*)take((size_t)ctas * sizeof(Range));
@@ -356,13 +447,8 @@ size_t layout(const PagedView& c, int G, int add_scores, Params* p, void* ws) {
 template <typename T, int D, int GP>
 cudaError_t run(const Params& p, const PagedDecodeArgs& a, cudaStream_t st) {
   cudaError_t e;
-  if constexpr (sizeof(T) == 2) {
-    e = launch_paged_decode_mma(p, a.q, st);
-  } else {
-    count_launches(1);
-    e = launch_with_pdl(paged_decode_kernel<T, D, GP>, dim3((unsigned)p.ctas), dim3(PD_WARPS * 32), 0, st,
-                        (const T*)a.q, p);
-  }
+  if constexpr (sizeof(T) == 2) e = launch_paged_decode_mma(p, a.q, st);
+  else e = run_f32<D>(p, a.q, st);
   if (e != cudaSuccess) return e;
   // a row of one tile is never shared, and without scores nothing is left to do
   if (!a.add_scores && p.c.cap <= TILE) return cudaSuccess;

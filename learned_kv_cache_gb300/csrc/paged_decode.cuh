@@ -34,6 +34,7 @@ struct Range {
 struct Params {
   PagedView c;
   int G, Hq, Hkv;
+  int gpad;              // G padded to 8 or 16: the GP of the layouts below
   int64_t q_stride;
   float c2, c2_low;      // scale * log2 e, and what the float leaves of it
   int ctas;              // launched
@@ -52,9 +53,14 @@ __device__ __forceinline__ int row_len(const Params& p, int r) {
   const int n = p.c.lens[r];
   return n < 0 ? 0 : (n > p.c.cap ? p.c.cap : n);
 }
-// Base-2 logit of a dot product, with one rounding: a long row's weights differ by powers of e, and an
-// error of the factor common to all logits grows with their difference.
-__device__ __forceinline__ float base2(const Params& p, float s) { return fmaf(s, p.c2, s * p.c2_low); }
+// Base-2 logit of the dot product a + b, and in `low` what is left of it (a two-term sum and product:
+// what a + b and the product with c2 round off, and c2's own remainder).
+__device__ __forceinline__ float base2(const Params& p, float a, float b, float& low) {
+  const float s = a + b, t = s - a, left = (a - (s - t)) + (b - t);
+  const float x = s * p.c2;
+  low = fmaf(s, p.c2, -x) + fmaf(s, p.c2_low, left * p.c2);
+  return x;
+}
 __device__ __forceinline__ int tiles_of(int n) { return (n + TILE - 1) / TILE; }
 
 __device__ __forceinline__ int cta_begin(int c, int total, int active) {

@@ -20,7 +20,8 @@
 //    2^-14 an f16 part loses bits, and beside a sink token that is where all the others' weights lie.
 //  * The tensor cores' running sum drops bits at every step, always towards zero; over the hundreds of
 //    tiles of a long row that would show, and in the logits of a sink token too.  Each step of 16 is
-//    summed on its own and added in fp32.
+//    summed on its own and added in fp32; a logit keeps what its last sum and its scaling round away
+//    (half a step of a sink's logit of 20 is 1e-6 of its weight).
 //  * Slots behind a row's end may hold anything.  Their logits are replaced by -inf, and their V is
 //    cleared in the fragments of the row's last tile: 0 * NaN would be NaN.
 #include <type_traits>
@@ -210,7 +211,7 @@ __global__ void __launch_bounds__(PM_THREADS, 2)
   constexpr int SPLIT = std::is_same<T, __half>::value ? 2 : 3;   // 16-bit parts of a weight
   constexpr float ABOVE = std::is_same<T, __half>::value ? 14.f : 0.f;   // log2 of the weights' scale
   uint32_t qb[C::NT][C::KSTEPS][2];
-  float m2[C::NT][2], ls[C::NT][2], o[C::NT][C::KSTEPS][4];
+  float m2[C::NT][2], ls[C::NT][2], lost[C::NT][2], o[C::NT][C::KSTEPS][4];   // lost: what ls rounds off
   int li = 0, turn = 0;
 
   // Row r, tiles [u0, u1) of its nt: merge the warps' states; the whole row's result, or a partial.
@@ -225,7 +226,7 @@ __global__ void __launch_bounds__(PM_THREADS, 2)
     const size_t head0 = (size_t)(r / p.Hkv) * p.Hq + (size_t)(r % p.Hkv) * p.G;
 #pragma unroll
     for (int x = 0; x < C::NT; ++x) {
-      float l0 = ls[x][0], l1 = ls[x][1];
+      float l0 = ls[x][0] + lost[x][0], l1 = ls[x][1] + lost[x][1];
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1) {
         l0 += __shfl_xor_sync(0xffffffffu, l0, off);
@@ -300,7 +301,7 @@ __global__ void __launch_bounds__(PM_THREADS, 2)
 #pragma unroll
     for (int y = 0; y < C::NT; ++y) {
       m2[y][0] = m2[y][1] = -INFINITY;
-      ls[y][0] = ls[y][1] = 0.f;
+      ls[y][0] = ls[y][1] = lost[y][0] = lost[y][1] = 0.f;
 #pragma unroll
       for (int db = 0; db < C::KSTEPS; ++db) o[y][db][0] = o[y][db][1] = o[y][db][2] = o[y][db][3] = 0.f;
     }
@@ -327,28 +328,42 @@ __global__ void __launch_bounds__(PM_THREADS, 2)
       const bool v0 = key0 < n, v1 = key0 + 8 < n;
       const int j = lane >> 3;
       if (u * TILE + kw < n) {
-        float sc[C::NT][4];
+        // the steps of 16 in a tree, its last sum with what it rounds away
+        float half[2][C::NT][4], sc[C::NT][4], low[C::NT][4];
 #pragma unroll
-        for (int y = 0; y < C::NT; ++y) sc[y][0] = sc[y][1] = sc[y][2] = sc[y][3] = 0.f;
+        for (int z = 0; z < 2; ++z)
 #pragma unroll
-        for (int ks = 0; ks < C::KSTEPS; ++ks) {
-          uint32_t a[4];
-          ldsm_x4(swz(kt, kw + (j & 1) * 8 + (lane & 7), 16 * ks + (j >> 1) * 8), a);
+          for (int k2 = 0; k2 < C::KSTEPS / 4; ++k2) {
+            float pair[C::NT][2][4];
 #pragma unroll
-          for (int y = 0; y < C::NT; ++y) {
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
-            mma16816<T>(sum, a, qb[y][ks][0], qb[y][ks][1]);
+            for (int k = 0; k < 2; ++k) {
+              const int ks = z * (C::KSTEPS / 2) + 2 * k2 + k;
+              uint32_t a[4];
+              ldsm_x4(swz(kt, kw + (j & 1) * 8 + (lane & 7), 16 * ks + (j >> 1) * 8), a);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sc[y][i] += sum[i];
+              for (int y = 0; y < C::NT; ++y) {
+                pair[y][k][0] = pair[y][k][1] = pair[y][k][2] = pair[y][k][3] = 0.f;
+                mma16816<T>(pair[y][k], a, qb[y][ks][0], qb[y][ks][1]);
+              }
+            }
+#pragma unroll
+            for (int y = 0; y < C::NT; ++y)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float x = pair[y][0][i] + pair[y][1][i];
+                half[z][y][i] = k2 == 0 ? x : half[z][y][i] + x;
+              }
           }
-        }
         uint32_t b[C::NT][SPLIT][2];
         bool grew = false;
         float nm[C::NT][2];
 #pragma unroll
         for (int y = 0; y < C::NT; ++y) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sc[y][i] = (i < 2 ? v0 : v1) ? paged::base2(p, sc[y][i]) : -INFINITY;
+          for (int i = 0; i < 4; ++i) {
+            sc[y][i] = paged::base2(p, half[0][y][i], half[1][y][i], low[y][i]);
+            if (!(i < 2 ? v0 : v1)) sc[y][i] = -INFINITY;
+          }
           if (p.logits) {
             float* lg = p.logits + ((size_t)r * p.c.cap + key0) * GP + 8 * y + 2 * t;
             if (v0) *reinterpret_cast<float2*>(lg) = make_float2(sc[y][0], sc[y][1]);
@@ -370,6 +385,8 @@ __global__ void __launch_bounds__(PM_THREADS, 2)
             // nothing but NaN so far (sum NaN, maximum -inf): 0 * NaN keeps it
             ls[y][0] *= f0;
             ls[y][1] *= f1;
+            lost[y][0] *= f0;
+            lost[y][1] *= f1;
 #pragma unroll
             for (int db = 0; db < C::KSTEPS; ++db) {
               o[y][db][0] *= f0;
@@ -385,9 +402,13 @@ __global__ void __launch_bounds__(PM_THREADS, 2)
         for (int y = 0; y < C::NT; ++y) {
           float w[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) w[i] = sc[y][i] == -INFINITY ? 0.f : fast_exp2(sc[y][i] - m2[y][i & 1]);
-          ls[y][0] += w[0] + w[2];
-          ls[y][1] += w[1] + w[3];
+          for (int i = 0; i < 4; ++i) w[i] = sc[y][i] == -INFINITY ? 0.f : fast_exp2((sc[y][i] - m2[y][i & 1]) + low[y][i]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float add = w[i] + w[i + 2], sum = ls[y][i] + add;
+            lost[y][i] += add - (sum - ls[y][i]);
+            ls[y][i] = sum;
+          }
           // P^T as B fragments: movmatrix turns the [key][head] layout of the first product's result
           // into the [head][key] layout that the second one reads
 #pragma unroll
