@@ -70,7 +70,7 @@ template <int D, int GP>
 __global__ void __launch_bounds__(Pf<D, GP>::THREADS, GP <= 8 ? 2 : 1)
     paged_decode_f32_kernel(const float* __restrict__ q, const Params p) {
   using C = Pf<D, GP>;
-  __shared__ int scan_sh[41];
+  __shared__ int scan_sh[36 + C::THREADS / 2];
   __shared__ float st_m[C::STATES][GP], st_l[C::STATES][GP];
   __shared__ __align__(16) float st_o[C::STATES][GP][D];
   __shared__ __align__(16) float weight_sh[C::STATES][C::V];
@@ -420,7 +420,7 @@ int decode_ctas() {
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return 2 * sms;
+  return sms < 256 ? 2 * sms : 512;
 }
 
 int padded_group(int G) { return G <= 8 ? 8 : 16; }

@@ -60,7 +60,7 @@ struct Pm {
   static constexpr int OFF_BAR = OFF_INV + 2 * GP * 4;
   static constexpr int OFF_FLAG = OFF_BAR + 16 * STAGES;
   static constexpr int OFF_SCAN = OFF_FLAG + 16;
-  static constexpr int SMEM = OFF_SCAN + 48 * 4 + 1024;    // + alignment slack
+  static constexpr int SMEM = OFF_SCAN + (36 + PM_THREADS / 2) * 4 + 1024;   // + alignment slack
   static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two CTAs per SM");
 };
 

@@ -334,6 +334,7 @@ __device__ __forceinline__ uint32_t div_by(uint32_t x, const FastDiv& d) {
 template <int VPR, int UN>
 __global__ void __launch_bounds__(256) append_copy_kernel(const PagedView c, const PagedNew a, const PlanArgs w,
                                                           int elt, FastDiv by_new, FastDiv by_heads, long long tokens) {
+  if (UN == 1) allow_next_grid();            // few blocks: the step's next kernel may take its places beside them
   wait_prior_grid();
   const int64_t ts = c.token_stride * elt, pgs = c.page_stride * elt;
   char* pk = (char*)c.k;
