@@ -622,3 +622,100 @@ def test_python_refusals(kvp):
         kvp.PagedCache(c.k_pool, c.v_pool, c.table, c.lens, c.refs, c.free_mask[:0])
     with pytest.raises(TypeError):
         kvp.kvp_paged_init(None)
+
+
+def test_offsets_past_32_bits(kvp):
+    """Pools of more than 2^31 elements and per-slot arrays of more than 2^31 entries, used at their far ends."""
+    D, ps, n_pages = 128, 128, 140000                           # 2.3e9 elements a pool
+    c = kvp.PagedCache.empty(8, 6, n_pages, ps, D, torch.float16)
+    refs = np.ones(n_pages, np.int32)
+    refs[-40:] = 0
+    c.refs.copy_(torch.from_numpy(refs))
+    words = np.zeros((n_pages + 31) // 32, np.uint32)
+    for p in range(n_pages - 40, n_pages):
+        words[p // 32] |= np.uint32(1 << (p % 32))
+    c.free_mask.copy_(torch.from_numpy(words.view(np.int32)))
+    new = torch.randn(2, 8, 600, D, device="cuda").half()
+    lens = [600, 300, 1, 129, 0, 0, 0, 0]
+    kvp.kvp_paged_append(c, new[0], new[1], counts=i32(lens))
+    kvp.kvp_paged_fork(c, i32([-1, -1, -1, -1, 0, -1, -1, -1]), copy=True)
+    kvp.kvp_paged_fork(c, i32([-1, -1, -1, -1, -1, 1, -1, -1]))
+    idx = np.tile(np.arange(0, 1200, 2), (8, 1))
+    kvp.kvp_paged_compact(c, i32(idx), i32([-1, 150, -1, -1, 300, -1, -1, -1]))
+    kvp.kvp_check_device_status()
+    assert int(c.table[0, 0]) == n_pages - 40
+    rows = rows_of(c)
+    for x in range(2):
+        assert torch.equal(rows[x][0], new[x, 0].cpu()) and torch.equal(rows[x][5], new[x, 1, :300].cpu())
+        assert torch.equal(rows[x][1], new[x, 1, :300:2].cpu()) and torch.equal(rows[x][4], new[x, 0, ::2].cpu())
+    check_decode(kvp, c, torch.randn(2, 16, D, device="cuda").half())
+    del c, new
+
+    c = kvp.PagedCache.empty(3, 1 << 20, 64, 1024, 64, torch.bfloat16, positions=True)   # 3 * 2^30 slots
+    new = torch.randn(3, 1500, 64, device="cuda").to(torch.bfloat16)
+    kvp.kvp_paged_append(c, new, new, counts=i32([1500, 0, 1500]), new_pos=i32([7, 0, 10 ** 6]))
+    kvp.kvp_paged_compact(c, i32(np.tile(np.arange(500, 1500), (3, 1))), i32([-1, -1, 1000]))
+    kvp.kvp_paged_fork(c, i32([-1, 2, -1]))
+    kvp.kvp_check_device_status()
+    assert c.pos[0, :1500].tolist() == list(range(7, 1507))
+    for r in (1, 2):
+        assert c.pos[r, :1000].tolist() == list(range(10 ** 6 + 500, 10 ** 6 + 1500))
+        assert torch.equal(rows_of(c)[0][r], new[2, 500:].cpu())
+    check_decode(kvp, c, torch.randn(1, 3, 64, device="cuda").to(torch.bfloat16))
+
+
+def test_captured_evictions(kvp):
+    """Two graphs on one cache (append + decode, compact + free), each with its own temporaries, replayed in turn."""
+    R, D, ps, cap = 4, 64, 16, 64
+    c = kvp.PagedCache.empty(R, 8, 40, ps, D, torch.float16, scores=True, positions=True)
+    new = torch.zeros(2, R, 1, D, device="cuda").half()
+    q = torch.zeros(2, 4, D, device="cuda").half()
+    at = torch.zeros(R, dtype=torch.int32, device="cuda")
+    out = torch.zeros(2, 4, D, device="cuda")
+    budgets = torch.full((R,), 40, dtype=torch.int32, device="cuda")
+
+    def step():
+        kvp.kvp_paged_append(c, new[0], new[1], new_pos=at)
+        kvp.kvp_paged_decode_attn(q, c, out=out, add_scores=True)
+
+    def evict():
+        idx, count = kvp.kvp_select_topk(c.score, budgets, 2, 8, 40, T=cap)
+        kvp.kvp_paged_compact(c, idx, count)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        for _ in range(cap):
+            step()
+        evict()
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    kvp.kvp_check_device_status()
+    graphs = []
+    for fn in (step, evict):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            fn()
+        graphs.append(g)
+    kvp.kvp_paged_free(c)
+    c.score.zero_()
+    seen = [[] for _ in range(R)]                               # (position, key) of the tokens a row holds
+    for t in range(200):
+        new.normal_()
+        q.normal_()
+        at.fill_(t)
+        graphs[0].replay()
+        for r in range(R):
+            seen[r].append((t, new[0, r, 0].cpu()))
+        if len(seen[0]) == cap:
+            torch.cuda.synchronize()
+            kept, _ = oracle.select_topk(c.score[:, :cap].cpu().numpy(), [40] * R, 2, 8, b_max=40)
+            graphs[1].replay()
+            seen = [[x[j] for j in kept[r]] for r, x in enumerate(seen)]
+            torch.cuda.synchronize()
+            kvp.kvp_check_device_status()
+            for r in range(R):
+                assert c.pos[r, :40].tolist() == [p for p, _ in seen[r]]
+                assert torch.equal(rows_of(c)[0][r], torch.stack([k for _, k in seen[r]]))
+            assert int(c.refs.sum()) == R * 3
+    assert c.lens.tolist() == [len(seen[0])] * R
