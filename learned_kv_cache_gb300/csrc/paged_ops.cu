@@ -53,6 +53,13 @@ __device__ __forceinline__ int32_t* table_row(const PagedView& c, int r) { retur
 
 __device__ __forceinline__ bool page_ok(int p, const PagedView& c) { return p >= 0 && p < c.n_pages; }
 
+// Word x of the free mask; nothing behind the last page.
+__device__ __forceinline__ uint32_t mask_word(const PagedView& c, int x) {
+  const int left = c.n_pages - 32 * x;
+  if (left <= 0) return 0u;
+  return c.free_mask[x] & (left >= 32 ? 0xffffffffu : (1u << left) - 1u);
+}
+
 // One reference less; the page is free when it was the last.
 __device__ __forceinline__ void release_page(const PagedView& c, int p, int* status) {
   if (!page_ok(p, c)) {
@@ -169,6 +176,8 @@ __global__ void __launch_bounds__(NEED_THREADS) compact_need_kernel(const PagedV
 }
 
 // The plan.  A thread has a row (several in turn above 1024 rows) and PLAN_WORDS words of the mask.
+// Bound by latency: lengths, table, counts of the tail pages 2.0 us; the mask and the list 1.3 us for
+// 256 pages, 2.0 us for 5600; the rows' books 0.9 us.
 template <int MODE>
 __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const PagedView c, const PlanArgs a) {
   __shared__ int scan_sh[33];
@@ -183,7 +192,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const PagedVie
   // the first words are on their way while the rows are looked at
   uint32_t mask[PLAN_WORDS];
 #pragma unroll
-  for (int k = 0; k < PLAN_WORDS; ++k) mask[k] = PLAN_WORDS * tid + k < words ? c.free_mask[PLAN_WORDS * tid + k] : 0u;
+  for (int k = 0; k < PLAN_WORDS; ++k) mask[k] = mask_word(c, PLAN_WORDS * tid + k);
   if (tid == 0) used_sh = 0;
 
   RowPlan w{-1, 0, -1, 0};
@@ -211,7 +220,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const PagedVie
 #pragma unroll
     for (int k = 0; k < PLAN_WORDS; ++k) {
       const int x = base + PLAN_WORDS * tid + k;
-      if (base > 0) mask[k] = x < words ? c.free_mask[x] : 0u;
+      if (base > 0) mask[k] = mask_word(c, x);
       mine += __popc(mask[k]);
     }
     int all;
@@ -329,64 +338,42 @@ __device__ __forceinline__ uint32_t div_by(uint32_t x, const FastDiv& d) {
 }
 
 // New tokens to their slots, and the books of the pages taken for them: a page's entry and count are
-// written by the thread of the first new token in it.  UN tokens per thread are in flight: four where
-// there is more than one pass of work for the GPU, one where there is less (a decode step).
-template <int VPR, int UN>
+// written by the thread of the first new token in it.  Bound by HBM: a thread has one vector of K and
+// one of V under way, and the occupancy does the rest (56 rows x 4096..8192 tokens: 72 us, with two
+// tokens per thread 72 us, with four 94 us).
+template <int VPR>
 __global__ void __launch_bounds__(256) append_copy_kernel(const PagedView c, const PagedNew a, const PlanArgs w,
-                                                          int elt, FastDiv by_new, FastDiv by_heads, long long tokens) {
-  if (UN == 1) allow_next_grid();            // few blocks: the step's next kernel may take its places beside them
+                                                          int elt, FastDiv by_new, FastDiv by_heads, long long tokens,
+                                                          int few) {
+  if (few) allow_next_grid();                // a decode step's: the next kernel may take its places beside them
   wait_prior_grid();
   const int64_t ts = c.token_stride * elt, pgs = c.page_stride * elt;
   char* pk = (char*)c.k;
   char* pv = (char*)c.v;
   constexpr int TOK = 256 / VPR;             // tokens per CTA and pass
   const int v = threadIdx.x % VPR;
-  const long long step = (long long)gridDim.x * TOK * UN;
-  for (long long x0 = (long long)blockIdx.x * TOK * UN + threadIdx.x / VPR; x0 < tokens; x0 += step) {
-    uint4 k[UN], y[UN];
-    int row[UN], slot[UN], page[UN], new_page[UN];
-#pragma unroll
-    for (int u = 0; u < UN; ++u) {
-      const long long x = x0 + u * TOK;
-      row[u] = -1;
-      if (x >= tokens) continue;
-      const int r = (int)div_by((uint32_t)x, by_new), i = (int)((uint32_t)x - (uint32_t)r * by_new.by);
-      if (i >= (a.counts ? __ldg(a.counts + r) : a.n_new)) continue;
-      const int b = (int)div_by((uint32_t)r, by_heads), h = r - b * a.h_kv;
-      k[u] = ld_stream16((const char*)a.k + (b * a.ks[0] + h * a.ks[1] + i * a.ks[2]) * elt + v * 16);
-      y[u] = ld_stream16((const char*)a.v + (b * a.vs[0] + h * a.vs[1] + i * a.vs[2]) * elt + v * 16);
-      row[u] = r;
-      slot[u] = i;
-    }
-#pragma unroll
-    for (int u = 0; u < UN; ++u) {
-      page[u] = -1;
-      new_page[u] = 0;
-      const int r = row[u];
-      if (r < 0) continue;
-      const int start = __ldg(w.start + r), tail = __ldg(w.tail + r), off = __ldg(w.off + r);
-      if (start < 0) continue;
-      const int i = slot[u], t = start + i, j = t >> c.shift;
-      const int first = tail >= 0 ? start >> c.shift : pages_of(start, c);
-      page[u] = j >= first ? __ldg(w.list + off + j - first) : table_row(c, r)[j];
-      new_page[u] = j >= first && (i == 0 || (t & (c.ps - 1)) == 0);
-      slot[u] = t;
-      if (v == 0 && c.pos) c.pos[(size_t)r * c.cap + t] = a.pos ? __ldg(a.pos + r) + i : t;
-    }
-#pragma unroll
-    for (int u = 0; u < UN; ++u) {
-      if (!page_ok(page[u], c)) continue;
-      const int r = row[u], t = slot[u], p = page[u];
-      const int64_t to = p * pgs + (t & (c.ps - 1)) * ts + v * 16;
-      *reinterpret_cast<uint4*>(pk + to) = k[u];
-      *reinterpret_cast<uint4*>(pv + to) = y[u];
-      if (v == 0) {
-        if (new_page[u]) {
-          table_row(c, r)[t >> c.shift] = p;
-          c.refs[p] = 1;
-        }
-        if (c.score) c.score[(size_t)r * c.cap + t] = 0.f;
+  for (long long x = (long long)blockIdx.x * TOK + threadIdx.x / VPR; x < tokens; x += (long long)gridDim.x * TOK) {
+    const int r = (int)div_by((uint32_t)x, by_new), i = (int)((uint32_t)x - (uint32_t)r * by_new.by);
+    if (i >= (a.counts ? __ldg(a.counts + r) : a.n_new)) continue;
+    const int b = (int)div_by((uint32_t)r, by_heads), h = r - b * a.h_kv;
+    const uint4 k = ld_stream16((const char*)a.k + (b * a.ks[0] + h * a.ks[1] + i * a.ks[2]) * elt + v * 16);
+    const uint4 y = ld_stream16((const char*)a.v + (b * a.vs[0] + h * a.vs[1] + i * a.vs[2]) * elt + v * 16);
+    const int start = __ldg(w.start + r), tail = __ldg(w.tail + r), off = __ldg(w.off + r);
+    if (start < 0) continue;
+    const int t = start + i, j = t >> c.shift, o = t & (c.ps - 1);
+    const int first = tail >= 0 ? start >> c.shift : pages_of(start, c);
+    const int p = j >= first ? __ldg(w.list + off + j - first) : table_row(c, r)[j];
+    if (!page_ok(p, c)) continue;            // the plan has raised the status
+    const int64_t to = p * pgs + o * ts + v * 16;
+    *reinterpret_cast<uint4*>(pk + to) = k;
+    *reinterpret_cast<uint4*>(pv + to) = y;
+    if (v == 0) {
+      if (j >= first && (i == 0 || o == 0)) {
+        table_row(c, r)[j] = p;
+        c.refs[p] = 1;
       }
+      if (c.score) c.score[(size_t)r * c.cap + t] = 0.f;
+      if (c.pos) c.pos[(size_t)r * c.cap + t] = a.pos ? __ldg(a.pos + r) + i : t;
     }
   }
   // tokens of shared tail pages, to the pages that replace them: a CTA per row
@@ -404,7 +391,8 @@ __global__ void __launch_bounds__(256) append_copy_kernel(const PagedView c, con
   }
 }
 
-// Whole pages of the rows that are copied, one page per CTA at a time.
+// Whole pages of the rows that are copied, one page per CTA at a time: the list of the pages taken is
+// the list of the work, whatever the rows' lengths.
 template <int VPR>
 __global__ void __launch_bounds__(256) pages_copy_kernel(const PagedView c, const PlanArgs w, int elt) {
   wait_prior_grid();
@@ -442,9 +430,11 @@ __global__ void __launch_bounds__(256) pages_copy_kernel(const PagedView c, cons
 // to be read, and the loads of later tokens may be under way at any time.  So chunks of tokens stream
 // through a ring in shared memory (cp.async), written in order, one barrier per chunk: loads of
 // STAGES - 1 chunks are in flight while one is stored.  Where a token lies takes two dependent reads
-// (index, table); they are made for eight chunks at a time, one group ahead of the copies.  The columns of a token
-// (16-byte vectors of K and of V) do not depend on each other, so a cluster of CTAs shares a row by
-// columns.  At the end the cluster gives the row its new pages.
+// (index, table); they are made for eight chunks at a time, one group ahead of the copies.  The columns
+// of a token (16-byte vectors of K and of V) do not depend on each other, so a cluster of CTAs shares a
+// row by columns.  At the end the cluster gives the row its new pages.  120000 -> 16384 tokens of 56
+// rows run at 5.8 TB/s (bound by HBM: half reads in pieces of 256 bytes, half writes), -> 4096 at 4.4
+// TB/s: of those 55 us the three launches and the first look-ups take 12.
 constexpr int CP_THREADS = 512;
 constexpr int CP_TOK = 128;                // tokens per chunk
 constexpr int CP_GROUP = 8;                // chunks whose tokens are looked up together
@@ -605,7 +595,7 @@ __global__ void __launch_bounds__(CP_THREADS) compact_pages_kernel(const PagedVi
 
 // ------------------------------------------------------------------ sharing and releasing
 
-// Row r takes the pages of row src[r]; one CTA per row.
+// Row r takes the pages of row src[r]; one CTA per row.  Bound by latency (56 forks of 1024 pages 3.9 us).
 __global__ void __launch_bounds__(256) fork_kernel(const PagedView c, const int32_t* __restrict__ src, int* status) {
   wait_prior_grid();
   const int r = blockIdx.x, s = src[r];
@@ -630,7 +620,7 @@ __global__ void __launch_bounds__(256) fork_kernel(const PagedView c, const int3
   if (threadIdx.x == 0) c.lens[r] = n;
 }
 
-// Row r keeps its first keep[r] tokens; one CTA per row.
+// Row r keeps its first keep[r] tokens; one CTA per row.  Bound by latency (28 rows of 1875 pages 4.7 us).
 __global__ void __launch_bounds__(512) free_kernel(const PagedView c, const int32_t* __restrict__ keep, int* status) {
   wait_prior_grid();
   const int r = blockIdx.x;
@@ -763,17 +753,13 @@ cudaError_t launch_paged_append(const PagedView& c, const PagedNew& n, void* ws,
   const long long tokens = (long long)n.n_new * c.R;
   const FastDiv by_new = fast_div((uint32_t)n.n_new), by_heads = fast_div((uint32_t)n.h_kv);
   // a block per row at least, for the shared tails
-  const bool wide = tokens * vpr > 8LL * 256 * sm_count();
   const dim3 grid(blocks_for(tokens * vpr > 256LL * c.R ? tokens * vpr : 256LL * c.R, 8));
-  count_launches(1);
+  const int few = tokens * vpr <= 8LL * 256 * sm_count();
   const auto go = [&](auto kernel) {
-    return launch_with_pdl(kernel, grid, dim3(256), 0, st, c, n, a, elt, by_new, by_heads, tokens);
+    count_launches(1);
+    return launch_with_pdl(kernel, grid, dim3(256), 0, st, c, n, a, elt, by_new, by_heads, tokens, few);
   };
-  switch (vpr) {
-    case 8: return wide ? go(append_copy_kernel<8, 2>) : go(append_copy_kernel<8, 1>);
-    case 16: return wide ? go(append_copy_kernel<16, 2>) : go(append_copy_kernel<16, 1>);
-    default: return wide ? go(append_copy_kernel<32, 2>) : go(append_copy_kernel<32, 1>);
-  }
+  return vpr == 8 ? go(append_copy_kernel<8>) : vpr == 16 ? go(append_copy_kernel<16>) : go(append_copy_kernel<32>);
 }
 
 size_t paged_fork_workspace(const PagedView& c, int copy) {

@@ -577,6 +577,16 @@ def test_what_only_the_device_sees(kvp):
         assert torch.equal(t, b)
 
 
+def test_bits_behind_the_last_page_are_no_pages(kvp):
+    c = kvp.PagedCache.empty(1, 3, 2, 16, 64, torch.float16)
+    c.free_mask.fill_(-1)
+    z = torch.ones(1, 40, 64, device="cuda").half()
+    raises_status(kvp, lambda: kvp.kvp_paged_append(c, z, z))                # three pages of two
+    kvp.kvp_paged_append(c, z[:, :32], z[:, :32])
+    kvp.kvp_check_device_status()
+    assert c.lens.tolist() == [32] and c.table[0, :2].tolist() == [0, 1]
+
+
 def test_unordered_indices_do_not_reach_shared_pages(kvp):
     """Indices that are not ascending raise the status; another row on the same pages keeps its tokens."""
     c = kvp.PagedCache.empty(2, 4, 12, 16, 64, torch.float16)
