@@ -178,14 +178,13 @@ __global__ void __launch_bounds__(NEED_THREADS) compact_need_kernel(const PagedV
 // The plan.  A thread has a row (several in turn above 1024 rows) and PLAN_WORDS words of the mask.
 // Bound by latency: lengths, table, counts of the tail pages 2.0 us; the mask and the list 1.3 us for
 // 256 pages, 2.0 us for 5600; the rows' books 0.9 us.
-template <int MODE>
-__global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const PagedView c, const PlanArgs a) {
+template <int MODE, int PLAN_THREADS>
+__device__ __forceinline__ void make_plan(const PagedView& c, const PlanArgs& a) {
   __shared__ int scan_sh[33];
   __shared__ int used_sh;
   // a word of padding per 32: below, the lanes of a warp read words 32 apart
   __shared__ uint32_t word_sh[PLAN_WORDS * PLAN_THREADS * 33 / 32];
   __shared__ int rank_sh[PLAN_WORDS * PLAN_THREADS * 33 / 32];
-  wait_prior_grid();
   const int tid = threadIdx.x, lane = tid & 31;
   const int words = (c.n_pages + 31) >> 5;
   const bool one = c.R <= PLAN_THREADS;      // every row stays in its thread's registers
@@ -312,9 +311,15 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const PagedVie
   if (lane == 0 && used > 0) atomicMax(&used_sh, used);
   __syncthreads();
   used = used_sh;
-  if (tid == 0) *a.used = used;
+  if (MODE == PLAN_COPY && tid == 0) *a.used = used;
   // pages that were found for a row that was left alone go back
   for (int i = used + tid; i < found; i += PLAN_THREADS) atomicOr(c.free_mask + (a.list[i] >> 5), 1u << (a.list[i] & 31));
+}
+
+template <int MODE>
+__global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const PagedView c, const PlanArgs a) {
+  wait_prior_grid();
+  make_plan<MODE, PLAN_THREADS>(c, a);
 }
 
 // ------------------------------------------------------------------ moving tokens
@@ -340,29 +345,27 @@ __device__ __forceinline__ uint32_t div_by(uint32_t x, const FastDiv& d) {
 // New tokens to their slots, and the books of the pages taken for them: a page's entry and count are
 // written by the thread of the first new token in it.  Bound by HBM: a thread has one vector of K and
 // one of V under way, and the occupancy does the rest (56 rows x 4096..8192 tokens: 72 us, with two
-// tokens per thread 72 us, with four 94 us).
+// tokens per thread 72 us, with four 94 us).  Starts, tails, offsets and the list come from the plan.
 template <int VPR>
-__global__ void __launch_bounds__(256) append_copy_kernel(const PagedView c, const PagedNew a, const PlanArgs w,
-                                                          int elt, FastDiv by_new, FastDiv by_heads, long long tokens,
-                                                          int few) {
-  if (few) allow_next_grid();                // a decode step's: the next kernel may take its places beside them
-  wait_prior_grid();
+__device__ __forceinline__ void append_tokens(const PagedView& c, const PagedNew& a, const int32_t* starts,
+                                              const int32_t* tails, const int32_t* offs, const int32_t* list, int elt,
+                                              const FastDiv& by_new, const FastDiv& by_heads, long long tokens,
+                                              long long thread, long long threads) {
   const int64_t ts = c.token_stride * elt, pgs = c.page_stride * elt;
   char* pk = (char*)c.k;
   char* pv = (char*)c.v;
-  constexpr int TOK = 256 / VPR;             // tokens per CTA and pass
-  const int v = threadIdx.x % VPR;
-  for (long long x = (long long)blockIdx.x * TOK + threadIdx.x / VPR; x < tokens; x += (long long)gridDim.x * TOK) {
+  const int v = (int)(thread % VPR);
+  for (long long x = thread / VPR; x < tokens; x += threads / VPR) {
     const int r = (int)div_by((uint32_t)x, by_new), i = (int)((uint32_t)x - (uint32_t)r * by_new.by);
     if (i >= (a.counts ? __ldg(a.counts + r) : a.n_new)) continue;
     const int b = (int)div_by((uint32_t)r, by_heads), h = r - b * a.h_kv;
     const uint4 k = ld_stream16((const char*)a.k + (b * a.ks[0] + h * a.ks[1] + i * a.ks[2]) * elt + v * 16);
     const uint4 y = ld_stream16((const char*)a.v + (b * a.vs[0] + h * a.vs[1] + i * a.vs[2]) * elt + v * 16);
-    const int start = __ldg(w.start + r), tail = __ldg(w.tail + r), off = __ldg(w.off + r);
+    const int start = starts[r], tail = tails[r], off = offs[r];
     if (start < 0) continue;
     const int t = start + i, j = t >> c.shift, o = t & (c.ps - 1);
     const int first = tail >= 0 ? start >> c.shift : pages_of(start, c);
-    const int p = j >= first ? __ldg(w.list + off + j - first) : table_row(c, r)[j];
+    const int p = j >= first ? list[off + j - first] : table_row(c, r)[j];
     if (!page_ok(p, c)) continue;            // the plan has raised the status
     const int64_t to = p * pgs + o * ts + v * 16;
     *reinterpret_cast<uint4*>(pk + to) = k;
@@ -376,19 +379,75 @@ __global__ void __launch_bounds__(256) append_copy_kernel(const PagedView c, con
       if (c.pos) c.pos[(size_t)r * c.cap + t] = a.pos ? __ldg(a.pos + r) + i : t;
     }
   }
-  // tokens of shared tail pages, to the pages that replace them: a CTA per row
-  for (int r = blockIdx.x; r < c.R; r += gridDim.x) {
-    const int from = w.tail[r], start = w.start[r];
-    if (start < 0 || from < 0) continue;
-    const int p = w.list[w.off[r]], n = (start & (c.ps - 1)) * VPR;
-    for (int e = threadIdx.x; e < n; e += 256) {
-      const int64_t at = (e / VPR) * ts + (e % VPR) * 16;
-      const uint4 x = *reinterpret_cast<const uint4*>(pk + from * pgs + at);
-      const uint4 z = *reinterpret_cast<const uint4*>(pv + from * pgs + at);
-      *reinterpret_cast<uint4*>(pk + p * pgs + at) = x;
-      *reinterpret_cast<uint4*>(pv + p * pgs + at) = z;
-    }
+}
+
+// The tokens of row r's shared tail page, to the page that replaces it; `group` threads share the row,
+// UN vectors of each in flight.
+template <int VPR, int UN>
+__device__ __forceinline__ void copy_tail(const PagedView& c, int from, int to, int tokens, int elt, int thread, int group) {
+  const int64_t ts = c.token_stride * elt, pgs = c.page_stride * elt;
+  char* pool[2] = {(char*)c.k, (char*)c.v};
+#pragma unroll UN
+  for (int e = thread; e < tokens * VPR; e += group) {
+    const int64_t at = (e / VPR) * ts + (e % VPR) * 16;
+    const uint4 x = ld_stream16(pool[0] + from * pgs + at), y = ld_stream16(pool[1] + from * pgs + at);
+    *reinterpret_cast<uint4*>(pool[0] + to * pgs + at) = x;
+    *reinterpret_cast<uint4*>(pool[1] + to * pgs + at) = y;
   }
+}
+
+template <int VPR>
+__global__ void __launch_bounds__(256) append_copy_kernel(const PagedView c, const PagedNew a, const PlanArgs w,
+                                                          int elt, FastDiv by_new, FastDiv by_heads, long long tokens) {
+  wait_prior_grid();
+  append_tokens<VPR>(c, a, w.start, w.tail, w.off, w.list, elt, by_new, by_heads, tokens,
+                     (long long)blockIdx.x * 256 + threadIdx.x, (long long)gridDim.x * 256);
+  for (int r = blockIdx.x; r < c.R; r += gridDim.x) {      // a CTA per row
+    const int from = w.tail[r], start = w.start[r];
+    if (start >= 0 && from >= 0)
+      copy_tail<VPR, 1>(c, from, w.list[w.off[r]], start & (c.ps - 1), elt, threadIdx.x, 256);
+  }
+}
+
+// A decode step's append in one launch and without a workspace: one cluster, whose first CTA makes the
+// plan in its shared memory; the others read it there.  The plan is what a step takes long for, and a
+// second launch and a workspace cost the host as much again: 56 rows x 1 token + decode + free 15.4 ->
+// 14.7 us of GPU time, a call from Python 13.2 -> 6.2 us of host time (256 rows that all have a shared
+// tail to copy: 8.5 -> 12.1 us of GPU time).
+constexpr int AS_ROWS = 512;               // their numbers and the list are in static shared memory
+constexpr int AS_PAGES = 1024;
+constexpr int AS_CTAS = 16;                // the largest cluster: the copies have that many SMs
+constexpr int AS_THREADS = 512;
+
+template <int VPR>
+__global__ void __launch_bounds__(AS_THREADS) append_step_kernel(const PagedView c, const PagedNew a, PlanArgs w,
+                                                                  int elt, FastDiv by_new, FastDiv by_heads,
+                                                                  int tokens) {
+  __shared__ int32_t start_sh[AS_ROWS], off_sh[AS_ROWS], tail_sh[AS_ROWS], list_sh[AS_PAGES];
+  allow_next_grid();                         // the step's next kernel may take its places beside this one
+  wait_prior_grid();
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = (int)cluster.block_rank();
+  if (rank == 0) {
+    w.start = start_sh;
+    w.off = off_sh;
+    w.tail = tail_sh;
+    w.list = list_sh;
+    make_plan<PLAN_APPEND, AS_THREADS>(c, w);
+  }
+  cluster.sync();
+  const int32_t* starts = cluster.map_shared_rank(start_sh, 0);
+  const int32_t* offs = cluster.map_shared_rank(off_sh, 0);
+  const int32_t* tails = cluster.map_shared_rank(tail_sh, 0);
+  const int32_t* list = cluster.map_shared_rank(list_sh, 0);
+  const int thread = rank * AS_THREADS + threadIdx.x, threads = AS_CTAS * AS_THREADS;
+  append_tokens<VPR>(c, a, starts, tails, offs, list, elt, by_new, by_heads, tokens, thread, threads);
+  for (int r = thread >> 5; r < c.R; r += threads >> 5) {  // a warp per row
+    const int from = tails[r], start = starts[r];
+    if (start >= 0 && from >= 0)
+      copy_tail<VPR, 4>(c, from, list[offs[r]], start & (c.ps - 1), elt, threadIdx.x & 31, 32);
+  }
+  cluster.sync();                            // the plan has been read
 }
 
 // Whole pages of the rows that are copied, one page per CTA at a time: the list of the pages taken is
@@ -736,28 +795,76 @@ cudaError_t launch_paged_init(const PagedView& c, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+cudaLaunchConfig_t step_config(cudaLaunchAttribute (&attr)[2], cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(AS_CTAS);
+  cfg.blockDim = dim3(AS_THREADS);
+  cfg.stream = st;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = AS_CTAS;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1] = pdl_attribute();
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cfg;
+}
+
+// Clusters of 16 CTAs need 16 SMs that lie together, which a partitioned GPU may not have.
+bool step_clusters_fit() {
+  static const bool fit = [] {
+    cudaLaunchAttribute attr[2];
+    const cudaLaunchConfig_t cfg = step_config(attr, nullptr);
+    int n = 0;
+    const bool ok = cudaFuncSetAttribute(append_step_kernel<16>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
+                        cudaSuccess &&
+                    cudaOccupancyMaxActiveClusters(&n, append_step_kernel<16>, &cfg) == cudaSuccess && n > 0;
+    if (!ok) cudaGetLastError();             // not an error of the caller's
+    return ok;
+  }();
+  return fit;
+}
+
+// Whether an append is a step: few rows and tokens.
+bool append_is_step(const PagedView& c, int n_new) {
+  const int vpr = c.D * (c.dtype == KVP_F32 ? 4 : 2) / 16;
+  return c.R <= AS_ROWS && append_list_cap(c, n_new) <= AS_PAGES &&
+         (long long)n_new * c.R * vpr <= 4LL * AS_CTAS * AS_THREADS && step_clusters_fit();
+}
+
 size_t paged_append_workspace(const PagedView& c, int n_new) {
   PlanArgs a{};
-  return plan_layout(c, &a, nullptr, append_list_cap(c, n_new), false, true, 0);
+  return append_is_step(c, n_new) ? 0 : plan_layout(c, &a, nullptr, append_list_cap(c, n_new), false, true, 0);
 }
 
 cudaError_t launch_paged_append(const PagedView& c, const PagedNew& n, void* ws, int* status, cudaStream_t st) {
   PlanArgs a{};
-  plan_layout(c, &a, ws, append_list_cap(c, n.n_new), false, true, 0);
   a.counts = n.counts;
   a.n_new = n.n_new;
   a.status = status;
-  cudaError_t e = launch_plan<PLAN_APPEND>(c, a, st);
-  if (e != cudaSuccess) return e;
   const int elt = c.dtype == KVP_F32 ? 4 : 2, vpr = c.D * elt / 16;
   const long long tokens = (long long)n.n_new * c.R;
   const FastDiv by_new = fast_div((uint32_t)n.n_new), by_heads = fast_div((uint32_t)n.h_kv);
+  if (append_is_step(c, n.n_new)) {
+    const auto step = [&](auto kernel) {
+      cudaLaunchAttribute attr[2];
+      const cudaLaunchConfig_t cfg = step_config(attr, st);
+      cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (e != cudaSuccess) return e;
+      count_launches(1);
+      e = cudaLaunchKernelEx(&cfg, kernel, c, n, a, elt, by_new, by_heads, (int)tokens);
+      return e != cudaSuccess ? e : cudaGetLastError();
+    };
+    return vpr == 8 ? step(append_step_kernel<8>) : vpr == 16 ? step(append_step_kernel<16>) : step(append_step_kernel<32>);
+  }
+  plan_layout(c, &a, ws, append_list_cap(c, n.n_new), false, true, 0);
+  cudaError_t e = launch_plan<PLAN_APPEND>(c, a, st);
+  if (e != cudaSuccess) return e;
   // a block per row at least, for the shared tails
   const dim3 grid(blocks_for(tokens * vpr > 256LL * c.R ? tokens * vpr : 256LL * c.R, 8));
-  const int few = tokens * vpr <= 8LL * 256 * sm_count();
   const auto go = [&](auto kernel) {
     count_launches(1);
-    return launch_with_pdl(kernel, grid, dim3(256), 0, st, c, n, a, elt, by_new, by_heads, tokens, few);
+    return launch_with_pdl(kernel, grid, dim3(256), 0, st, c, n, a, elt, by_new, by_heads, tokens);
   };
   return vpr == 8 ? go(append_copy_kernel<8>) : vpr == 16 ? go(append_copy_kernel<16>) : go(append_copy_kernel<32>);
 }

@@ -418,6 +418,46 @@ def test_strided_pools_and_queries(kvp):
     check_decode(kvp, c, q)
 
 
+@pytest.mark.parametrize("dtype,D,R,n_new,ps", [("f16", 128, 512, 1, 16), ("f32", 64, 200, 5, 16), ("bf16", 64, 1, 60, 32),
+                                                ("f32", 128, 300, 2, 64), ("bf16", 128, 513, 1, 16)])
+def test_appends_of_a_step(kvp, dtype, D, R, n_new, ps):
+    """Small appends (one launch, no workspace) and the first that are not: pages from all over the mask, every
+    second row with a tail that it shares."""
+    rng = np.random.default_rng(R)
+    np_dt = np.int32 if dtype == "f32" else np.int16
+    n_pages = 70000
+    o = paged.empty_cache(2 * R, 6, n_pages, ps, D, np_dt, scores=True, positions=True) if R < 300 else None
+    if o is None:
+        R //= 2
+        o = paged.empty_cache(2 * R, 6, n_pages, ps, D, np_dt, scores=True, positions=True)
+    c = to_gpu(kvp, o, DT[dtype])
+    first = rng.integers(0, 1 << 14, (2, 2 * R, 40, D)).astype(np_dt)
+    cnt = [int(x) if r < R else 0 for r, x in enumerate(rng.integers(0, 41, 2 * R))]
+    paged.append(o, first[0], first[1], cnt)
+    kvp.kvp_paged_append(c, *(torch.from_numpy(x).view(DT[dtype]).cuda() for x in first), counts=i32(cnt))
+    src = [-1] * R + [r if r % 2 else -1 for r in range(R)]
+    paged.fork(o, src)
+    kvp.kvp_paged_fork(c, i32(src))
+    for step in range(3):
+        new = rng.integers(0, 1 << 14, (2, 2 * R, n_new, D)).astype(np_dt)
+        cnt = rng.integers(0, min(n_new, 6 * ps // 4) + 1, 2 * R)
+        cnt = np.minimum(cnt, 6 * ps - o["lens"])
+        assert paged.append(o, new[0], new[1], cnt) == []
+        kvp.kvp_paged_append(c, *(torch.from_numpy(x).view(DT[dtype]).cuda() for x in new), counts=i32(cnt))
+        kvp.kvp_check_device_status()
+        torch.cuda.synchronize()
+        assert c.lens.tolist() == o["lens"].tolist() and c.refs.tolist() == o["refs"].tolist()
+        assert (c.table.cpu().numpy() == o["table"]).all()
+        assert (c.free_mask.cpu().numpy() == paged.free_mask(o)).all()
+        used = np.nonzero(o["refs"])[0]
+        for name, pool in (("k", c.k_pool), ("v", c.v_pool)):
+            got = pool[torch.from_numpy(used).cuda()].cpu().view(BITS[c.dtype]).numpy()
+            assert (got == o[name][used]).all()
+        for r in range(2 * R):
+            n = int(o["lens"][r])
+            assert (c.pos[r, :n].cpu().numpy() == o["pos"][r, :n]).all()
+
+
 def test_layers_share_one_pool(kvp):
     """rows(): the calls on one layer's rows leave the other layers' alone."""
     c = kvp.PagedCache.empty(12, 4, 40, 16, 64, torch.float16)
