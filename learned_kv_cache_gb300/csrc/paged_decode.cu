@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(Pf<D, GP>::THREADS, GP <= 8 ? 2 : 1)
   const bool counts = dl % C::SAME == 0;                   // one of the lanes that have the same logit
   const int cta = blockIdx.x;
   const Range g = paged::find_range(p, cta, scan_sh);
-  paged::empty_rows<float, D>(p, cta);
+  paged::empty_rows<float, D>(p, cta, C::THREADS);
   if (cta >= g.active) return;
   const PagedView& c = p.c;
   const float* kp = (const float*)c.k + dl * 4;

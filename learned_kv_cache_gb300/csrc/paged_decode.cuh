@@ -173,11 +173,11 @@ __device__ __forceinline__ void store_out4(const Params& p, size_t i, float4 x) 
 }
 
 // Rows without tokens have no tile: the CTAs share them out by index, a lane looks at a row and a warp
-// clears its outputs.
+// clears its outputs.  `threads` of the CTA take part.
 template <typename T, int D>
-__device__ __forceinline__ void empty_rows(const Params& p, int cta) {
+__device__ __forceinline__ void empty_rows(const Params& p, int cta, int threads) {
   const int lane = threadIdx.x & 31;
-  for (int i = threadIdx.x - lane; (long long)i * p.ctas + cta < p.c.R; i += blockDim.x) {
+  for (int i = threadIdx.x - lane; (long long)i * p.ctas + cta < p.c.R; i += threads) {
     const long long x = (long long)(i + lane) * p.ctas + cta;
     const int n = x < p.c.R ? p.c.lens[x] : 1;
     if (n < 0 || n > p.c.cap) raise_status(p.status, KVP_ERR_DEVICE_CHECK);
