@@ -553,8 +553,9 @@ int kvp_paged_free(const kvp_paged_cache* cache, const int32_t* keep, kvp_stream
  * The work is split by the rows' lengths on the device, so one captured call
  * serves a cache that grows and shrinks.  Slots behind a row's last token may
  * hold anything; the outputs must not overlap q.  workspace:
- * kvp_paged_decode_attn_workspace_size() bytes, 256-byte aligned (a few MB; with
- * add_scores 32 or 64 bytes per slot of the table besides, for the logits). */
+ * kvp_paged_decode_attn_workspace_size() bytes, 256-byte aligned (a few MB, none
+ * for tables of few tokens a row; with add_scores 32 or 64 bytes per slot of the
+ * table besides, for the logits). */
 size_t kvp_paged_decode_attn_workspace_size(const kvp_paged_cache* cache, int h_q, int h_kv,
                                             int add_scores);
 int kvp_paged_decode_attn(const void* q, int64_t q_stride, const kvp_paged_cache* cache, int h_q,

@@ -14,6 +14,7 @@
 namespace kvp {
 namespace {
 
+using paged::MAX_CTAS;
 using paged::Params;
 using paged::Range;
 using paged::TILE;
@@ -414,13 +415,113 @@ __global__ void __launch_bounds__(JOIN_THREADS) paged_join_kernel(const Params p
   }
 }
 
+// The same of few rows, which have many parts each, when no scores are asked for: a block joins JOIN_LANES
+// quads of outputs of one head.  It finds the row's parts from the lengths, so that there is a block per
+// result and not per CTA of the decode kernel, and reads all its states and outputs in one go.
+constexpr int JOIN_LANES = 8;
+// Parts a row can have for that.  GPU time of a call with the other kernel / this one, rows of 8192 tokens,
+// D 128: 1 row of 8 query heads on a KV head 11.9 / 8.6 us, 8 rows 15.2 / 12.2, 16 rows 15.6 / 15.7, 24 rows
+// 19.7 / 21.4; 16 heads 18.4 / 10.6, 24.5 / 17.3, 25.6 / 24.3, 32.4 / 33.4; 1 row of 131072 tokens 25.5 / 14.7.
+constexpr int FEW_PARTS = 16;
+
+template <typename T, int D, int GP>
+__global__ void __launch_bounds__(JOIN_THREADS) paged_join_few_kernel(const Params p) {
+  constexpr int GROUPS = JOIN_THREADS / JOIN_LANES, WARPS = JOIN_THREADS / 32;
+  constexpr int K = MAX_CTAS / GROUPS, KS = MAX_CTAS / JOIN_THREADS;
+  __shared__ float weights[MAX_CTAS], red[2][WARPS];
+  __shared__ float4 sum_sh[WARPS * JOIN_LANES];
+  wait_prior_grid();
+  allow_next_grid();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int r = blockIdx.x / p.G, h = blockIdx.x % p.G;
+  int before = 0, mine = 0, total = 0;
+  for (int x = lane; x < p.c.R; x += 32) {
+    const int t = paged::tiles_of(paged::row_len(p, x));
+    total += t;
+    if (x < r) before += t;
+    if (x == r) mine = t;
+  }
+  total = __reduce_add_sync(0xffffffffu, total);
+  before = __reduce_add_sync(0xffffffffu, before);
+  mine = __reduce_add_sync(0xffffffffu, mine);
+  if (mine == 0) return;
+  const int active = paged::active_ctas(p, total);
+  const int lo = paged::cta_of(before, total, active), n = paged::cta_of(before + mine - 1, total, active) - lo + 1;
+  if (n == 1) return;                        // finished where it was read
+  const auto at = [&](int i) { return p.part + ((size_t)(lo + i) * 2 + (i == 0 ? 1 : 0)) * p.pstride; };
+  const int e = 4 * (blockIdx.y * JOIN_LANES + tid % JOIN_LANES), grp = tid / JOIN_LANES;
+  float m[KS], l[KS];
+  float4 x[K];
+#pragma unroll
+  for (int k = 0; k < KS; ++k) {
+    const int i = tid + k * JOIN_THREADS;
+    m[k] = i < n ? at(i)[h] : -INFINITY;
+    l[k] = i < n ? at(i)[GP + h] : 0.f;
+  }
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (grp + k * GROUPS < n) x[k] = *reinterpret_cast<const float4*>(at(grp + k * GROUPS) + 2 * GP + h * D + e);
+  }
+  float M = m[0];
+#pragma unroll
+  for (int k = 1; k < KS; ++k) M = fmaxf(M, m[k]);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  if (lane == 0) red[0][warp] = M;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) M = fmaxf(M, red[0][w]);
+  float L = 0.f;
+#pragma unroll
+  for (int k = 0; k < KS; ++k) {
+    const float f = paged::weight(m[k], M);
+    weights[tid + k * JOIN_THREADS] = f;
+    L = fmaf(l[k], f, L);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+  if (lane == 0) red[1][warp] = L;
+  __syncthreads();
+  L = red[1][0];
+#pragma unroll
+  for (int w = 1; w < WARPS; ++w) L += red[1][w];
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  const auto add = [&](const float4& a, float f) {
+    o.x = fmaf(a.x, f, o.x);
+    o.y = fmaf(a.y, f, o.y);
+    o.z = fmaf(a.z, f, o.z);
+    o.w = fmaf(a.w, f, o.w);
+  };
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+    if (grp + k * GROUPS < n) add(x[k], weights[grp + k * GROUPS] * inv);
+  // the groups' sums: those of a warp by shuffles, then the warps'
+#pragma unroll
+  for (int off = JOIN_LANES; off < 32; off <<= 1) {
+    o.x += __shfl_xor_sync(0xffffffffu, o.x, off);
+    o.y += __shfl_xor_sync(0xffffffffu, o.y, off);
+    o.z += __shfl_xor_sync(0xffffffffu, o.z, off);
+    o.w += __shfl_xor_sync(0xffffffffu, o.w, off);
+  }
+  if (lane < JOIN_LANES) sum_sh[warp * JOIN_LANES + lane] = o;
+  __syncthreads();
+  if (tid >= JOIN_LANES) return;
+#pragma unroll
+  for (int w = 1; w < WARPS; ++w) add(sum_sh[w * JOIN_LANES + tid], 1.f);
+  const size_t head = (size_t)(r / p.Hkv) * p.Hq + (size_t)(r % p.Hkv) * p.G + h;
+  paged::store_out4<T>(p, head * D + e, o);
+  if (p.lse && e == 0) p.lse[head] = L == 0.f ? -INFINITY : (M + log2f(L)) * KVP_LN2;
+}
+
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 int decode_ctas() {
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return sms < 256 ? 2 * sms : 512;
+  return 2 * sms < paged::MAX_CTAS ? 2 * sms : paged::MAX_CTAS;
 }
 
 int padded_group(int G) { return G <= 8 ? 8 : 16; }
@@ -435,6 +536,12 @@ size_t layout(const PagedView& c, int G, int add_scores, Params* p, void* ws) {
     return x;
   };
   p->ctas = ctas;
+  p->whole = !add_scores && (c.cap + TILE - 1) / TILE <= paged::whole_tiles(c.dtype) &&
+             c.R <= paged::WHOLE_ROWS * ctas;
+  if (p->whole) {
+    if (p->ctas > c.R) p->ctas = c.R;
+    return 0;
+  }
   p->gpad = GP;
   p->pstride = 2 * GP + GP * c.D;
   p->part = (float*)take((size_t)ctas * 2 * p->pstride * 4);
@@ -450,8 +557,12 @@ cudaError_t run(const Params& p, const PagedDecodeArgs& a, cudaStream_t st) {
   if constexpr (sizeof(T) == 2) e = launch_paged_decode_mma(p, a.q, st);
   else e = run_f32<D>(p, a.q, st);
   if (e != cudaSuccess) return e;
-  // a row of one tile is never shared, and without scores nothing is left to do
-  if (!a.add_scores && p.c.cap <= TILE) return cudaSuccess;
+  if (p.whole) return cudaSuccess;           // every row has been finished where it was read
+  if (!a.add_scores && (long long)FEW_PARTS * p.c.R < p.ctas) {
+    count_launches(1);
+    return launch_with_pdl(paged_join_few_kernel<T, D, GP>, dim3((unsigned)(p.c.R * p.G), D / (4 * JOIN_LANES)),
+                           dim3(JOIN_THREADS), 0, st, p);
+  }
   // Blocks per CTA of the decode kernel.  Rows of which there are many have few parts each (one block
   // joins 1024 outputs of up to 8 parts in one go); of a few long rows the outputs are dealt out
   // further, and so are the scores of long ranges.

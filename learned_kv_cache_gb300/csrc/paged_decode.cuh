@@ -6,7 +6,7 @@
 // device the split: the tiles of TILE keys of all rows form one sequence, and CTA c of the P active
 // ones takes [c * total / P, (c + 1) * total / P) of it.  A row that lies inside one CTA's range is
 // finished there; of a longer one every CTA leaves a partial (maximum, sum, output) that the join
-// kernel merges in CTA order, so results do not depend on timing.
+// kernel merges in CTA order, so results do not depend on timing.  Short rows are not cut (whole_tiles).
 #pragma once
 
 #include <type_traits>
@@ -18,10 +18,23 @@ namespace kvp {
 namespace paged {
 
 constexpr int TILE = 64;                 // keys per tile
+constexpr int MAX_CTAS = 512;            // (two per SM)
 // Tiles per CTA below which fewer CTAs are active.  GPU time of a call at 4 / 2 / 1 (f16, 12 query
-// heads on 2 KV heads, 28 layers): 64 tokens a row 12.3 / 9.0 / 7.4 us, 512 tokens 10.9 / 10.4 / 11.6 us
-// (more parts to join), longer rows the same.
+// heads on 2 KV heads, 28 layers, in tables wide enough to be cut): 64 tokens a row 12.3 / 9.0 / 7.4 us,
+// 512 tokens 10.9 / 10.4 / 11.6 us (more parts to join), longer rows the same.
 constexpr int MIN_TILES = 2;
+
+// Rows whose table holds no more tiles than this are not cut: a CTA takes whole rows, an equal number each,
+// so that nothing is left to join and nobody has to know the lengths of all rows (scores need the join
+// kernel's second look at the logits, so there rows are always cut).  GPU time of a call without / with
+// the rule, 6 query heads on a KV head, D 128:
+//   bf16, 56 rows: 64 tokens 8.0 / 4.9 us, 256 9.3 / 6.8, 512 9.7 / 8.9; 900 rows: 64 12.0 / 9.7, 512 46.9 / 40.1
+//   fp32, 56 rows: 64 tokens 12.4 / 6.4 us, 128 10.6 / 9.2, 256 13.7 / 15.1; 900 rows: 64 24.8 / 23.1
+// A CTA of the fp32 kernel takes three times as long over a tile, and so gains less by the wait it saves.
+constexpr int whole_tiles(int dtype) { return dtype == KVP_F32 ? 3 : 9; }
+// Rows per CTA up to which that holds.  More rows gain 8 % by it (16384 of ~64 tokens 152 / 140 us), but where
+// the long ones lie side by side an equal number of rows is no equal share.
+constexpr int WHOLE_ROWS = 4;
 
 // Range of one CTA in the tile sequence, kept for the join kernel.
 struct Range {
@@ -38,6 +51,7 @@ struct Params {
   int64_t q_stride;
   float c2, c2_low;      // scale * log2 e, and what the float leaves of it
   int ctas;              // launched
+  int whole;             // 1: rows are not cut (part and range are not used)
   float* part;           // [ctas][2][pstride]: m[GP], l[GP], o[GP][D]; slot 0: the row began in an
   int pstride;           //   earlier CTA, slot 1: it goes on in the next one
   Range* range;          // [ctas]
@@ -64,13 +78,17 @@ __device__ __forceinline__ int tiles_of(int n) { return (n + TILE - 1) / TILE; }
 // 32-bit divisions where the products fit (a 64-bit one is a subroutine of some hundred cycles, and
 // nothing is copied yet while a CTA looks for its range).
 __device__ __forceinline__ int cta_begin(int c, int total, int active) {
-  if (total < (1 << 22)) return (int)((uint32_t)c * (uint32_t)total / (uint32_t)active);   // c, active <= 512
+  if (total < (1 << 22)) return (int)((uint32_t)c * (uint32_t)total / (uint32_t)active);   // c, active <= MAX_CTAS
   return (int)((long long)c * total / active);
 }
 // CTA that owns tile x.
 __device__ __forceinline__ int cta_of(int x, int total, int active) {
   if (total < (1 << 22)) return (int)((((uint32_t)x + 1) * (uint32_t)active - 1) / (uint32_t)total);
   return (int)((((long long)x + 1) * active - 1) / total);
+}
+
+__device__ __forceinline__ int active_ctas(const Params& p, int total) {
+  return min((total + MIN_TILES - 1) / MIN_TILES, p.ctas);
 }
 
 // This CTA's range.  Every thread of the block calls it; `sh` holds 36 + blockDim.x / 2 ints.  Each thread
@@ -80,6 +98,15 @@ __device__ __forceinline__ int cta_of(int x, int total, int active) {
 // the whole call; for few rows it would be one barrier and 0.3 us more).
 __device__ __forceinline__ Range find_range(const Params& p, int cta, int* sh) {
   const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31;
+  if (p.whole) {                             // an equal number of rows each
+    Range g{};
+    const int end = (int)((long long)(cta + 1) * p.c.R / p.ctas);
+    g.row = (int)((long long)cta * p.c.R / p.ctas);
+    for (int r = g.row; r < end; ++r) g.end += tiles_of(row_len(p, r));
+    g.active = g.end > 0 ? p.ctas : 0;
+    __syncthreads();                         // as on the other way, for the caller's shared memory
+    return g;
+  }
   const bool one = p.c.R <= nt;
   const int per = one ? 1 : ((p.c.R + nt - 1) / nt + 3) & ~3, r0 = min(tid * per, p.c.R), r1 = min(r0 + per, p.c.R);
   int mine = 0;
@@ -100,8 +127,7 @@ __device__ __forceinline__ Range find_range(const Params& p, int cta, int* sh) {
   }
   int total;
   const int before = block_exclusive_scan(mine, sh, &total);
-  int active = (total + MIN_TILES - 1) / MIN_TILES;
-  if (active > p.ctas) active = p.ctas;
+  const int active = active_ctas(p, total);
   Range g{};
   g.total = total;
   g.active = active;

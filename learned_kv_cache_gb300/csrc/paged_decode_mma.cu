@@ -24,7 +24,7 @@
 //    (half a step of a sink's logit of 20 is 1e-6 of its weight).
 //  * Measured: 56 rows x 120000 tokens of 128 f16 values 490 us (7.0 TB/s), x 4096 26 us with the join (6
 //    us to the first tiles: lengths, page ids, K and V are three dependent reads; 3 us of join), 8 rows x
-//    131072 bf16 87 us (6.2 TB/s).
+//    131072 bf16 84 us (6.4 TB/s).
 //  * Slots behind a row's end may hold anything.  Their logits are replaced by -inf, and their V is
 //    cleared in the fragments of the row's last tile: 0 * NaN would be NaN.
 #include <type_traits>

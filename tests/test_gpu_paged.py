@@ -366,6 +366,43 @@ def test_decode_splits(kvp, dtype, lens):
     check_decode(kvp, c, q, sm_scale=0.31)
 
 
+def capped(c, pages):
+    """The same rows with a table cut to `pages` columns."""
+    t = c.table[:, :pages].contiguous()
+    return type(c)(c.k_pool, c.v_pool, t, c.lens, c.refs, c.free_mask, None, None)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("D,G,lens", [
+    (128, 1, [20000]), (64, 4, [5003, 0, 9001, 64]), (128, 16, [700, 129]), (64, 16, [4100]),
+    (128, 5, [0, 0, 33000, 1, 0, 65]), (128, 8, [1500 + 64 * i for i in range(18)]), (64, 3, [900 + i for i in range(19)]),
+])
+def test_decode_of_few_rows(kvp, dtype, D, G, lens):
+    """Rows that many CTAs share, without scores: from one part to as many as there are CTAs."""
+    c = filled(kvp, lens, 64, D, dtype, seed=len(lens) + G)
+    q = torch.randn(1, len(lens) * G, D, generator=torch.Generator().manual_seed(G)).to(DT[dtype]).cuda()
+    check_decode(kvp, c, q)
+    if dtype != "f32":
+        check_decode(kvp, c, q, out_dtype=DT[dtype])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("D,G,ps,cap,R", [(128, 6, 64, 192, 1), (64, 2, 16, 192, 56), (128, 1, 64, 576, 303), (128, 4, 32, 192, 304),
+                                          (64, 16, 64, 576, 305), (128, 8, 16, 80, 1216), (64, 1, 64, 64, 1217),
+                                          (128, 12, 128, 512, 700)])
+def test_decode_of_short_rows(kvp, dtype, D, G, ps, cap, R):
+    """Tables so narrow that rows are not cut (and, of fp32, some that are): one row or several per CTA,
+    empty rows first, last and in runs, full ones."""
+    gen = torch.Generator().manual_seed(R)
+    lens = torch.randint(0, cap + 1, (R,), generator=gen)
+    lens[torch.rand(R, generator=gen) < 0.3] = 0
+    lens[R // 3:R // 3 + 9] = 0
+    lens[R // 2], lens[-1] = cap, 0 if R > 1 else cap
+    c = capped(filled(kvp, lens.tolist(), ps, D, dtype, seed=R), cap // ps)
+    q = torch.randn(1, R * G, D, generator=gen).to(DT[dtype]).cuda()
+    check_decode(kvp, c, q)
+
+
 def test_decode_extreme_values(kvp):
     """One-hot softmax at large logits, equal keys (the mean of the values), stale infinities."""
     c = filled(kvp, [200, 90, 64, 1], 32, 128, "bf16", seed=3, stale=float("inf"), key_scale=30.0)
