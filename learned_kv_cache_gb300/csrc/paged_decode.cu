@@ -234,6 +234,7 @@ __global__ void __launch_bounds__(Pf<D, GP>::THREADS, GP <= 8 ? 2 : 1)
           const float l2 = L == 0.f ? -INFINITY : M + log2f(L);
           if (p.lse) p.lse[head] = l2 * KVP_LN2;
           if (p.lse2) p.lse2[(size_t)r * p.gpad + h] = l2;
+          factor_sh[0][h] = l2;              // (the factors are not in use here)
         }
       } else {
         part[2 * p.gpad + e] = O;
@@ -244,6 +245,11 @@ __global__ void __launch_bounds__(Pf<D, GP>::THREADS, GP <= 8 ? 2 : 1)
       }
     }
     __syncthreads();
+    if (p.whole && p.logits) {
+      constexpr int PAD = GP <= 8 ? 8 : 16;
+      paged::add_row_scores<PAD>(p, r, tid, n, C::THREADS, factor_sh[0]);
+      __syncthreads();
+    }
     x += u1 - u;
     ++r;
     u = 0;
@@ -320,7 +326,6 @@ __global__ void __launch_bounds__(JOIN_THREADS) paged_join_kernel(const Params p
   const int cta = blockIdx.x, y = blockIdx.y, ny = gridDim.y, tid = threadIdx.x;
   const Range g = p.range[cta];
   if (cta >= g.active) return;
-  const PagedView& c = p.c;
   if (g.tile > 0 && g.lo == cta - 1) {
     const int lo = g.lo, hi = g.hi;
     const size_t head0 = (size_t)(g.row / p.Hkv) * p.Hq + (size_t)(g.row % p.Hkv) * p.G;
@@ -390,25 +395,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) paged_join_kernel(const Params p
       join_states<GP>(p, paged::cta_of(x - u, g.total, g.active), paged::cta_of(x - u + nt - 1, g.total, g.active),
                       lse_sh, nullptr);
     }
-    float lse[GP];
-#pragma unroll
-    for (int h = 0; h < GP; ++h) lse[h] = h < p.G ? lse_sh[h] : 0.f;
-    const int hi = min(n, u1 * TILE);
-    for (int m = u * TILE + y * JOIN_THREADS + tid; m < hi; m += ny * JOIN_THREADS) {
-      const float4* lg = reinterpret_cast<const float4*>(p.logits + ((size_t)r * c.cap + m) * GP);
-      float* score = c.score + (size_t)r * c.cap + m;
-      const float before = *score;
-      float s = 0.f;
-#pragma unroll
-      for (int k = 0; k < GP / 4; ++k) {
-        const float4 w = lg[k];
-        const float z[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (4 * k + i < p.G && z[i] != -INFINITY) s += fast_exp2(z[i] - lse[4 * k + i]);
-      }
-      *score = before + s;
-    }
+    paged::add_row_scores<GP>(p, r, u * TILE + y * JOIN_THREADS + tid, min(n, u1 * TILE), ny * JOIN_THREADS, lse_sh);
     x += u1 - u;
     ++r;
     u = 0;
@@ -536,18 +523,18 @@ size_t layout(const PagedView& c, int G, int add_scores, Params* p, void* ws) {
     return x;
   };
   p->ctas = ctas;
-  p->whole = !add_scores && (c.cap + TILE - 1) / TILE <= paged::whole_tiles(c.dtype) &&
+  p->gpad = GP;
+  p->logits = add_scores ? (float*)take((size_t)c.R * c.cap * GP * 4) : nullptr;
+  p->whole = (c.cap + TILE - 1) / TILE <= paged::whole_tiles(c.dtype) &&
              c.R <= paged::WHOLE_ROWS * ctas;
   if (p->whole) {
     if (p->ctas > c.R) p->ctas = c.R;
-    return 0;
+    return at;
   }
-  p->gpad = GP;
   p->pstride = 2 * GP + GP * c.D;
   p->part = (float*)take((size_t)ctas * 2 * p->pstride * 4);
   p->range = (Range*)take((size_t)ctas * sizeof(Range));
   p->lse2 = add_scores ? (float*)take((size_t)c.R * GP * 4) : nullptr;
-  p->logits = add_scores ? (float*)take((size_t)c.R * c.cap * GP * 4) : nullptr;
   return at;
 }
 
@@ -557,7 +544,7 @@ cudaError_t run(const Params& p, const PagedDecodeArgs& a, cudaStream_t st) {
   if constexpr (sizeof(T) == 2) e = launch_paged_decode_mma(p, a.q, st);
   else e = run_f32<D>(p, a.q, st);
   if (e != cudaSuccess) return e;
-  if (p.whole) return cudaSuccess;           // every row has been finished where it was read
+  if (p.whole) return cudaSuccess;           // every row has been finished, and scored, where it was read
   if (!a.add_scores && (long long)FEW_PARTS * p.c.R < p.ctas) {
     count_launches(1);
     return launch_with_pdl(paged_join_few_kernel<T, D, GP>, dim3((unsigned)(p.c.R * p.G), D / (4 * JOIN_LANES)),

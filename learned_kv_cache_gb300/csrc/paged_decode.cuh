@@ -25,11 +25,11 @@ constexpr int MAX_CTAS = 512;            // (two per SM)
 constexpr int MIN_TILES = 2;
 
 // Rows whose table holds no more tiles than this are not cut: a CTA takes whole rows, an equal number each,
-// so that nothing is left to join and nobody has to know the lengths of all rows (scores need the join
-// kernel's second look at the logits, so there rows are always cut).  GPU time of a call without / with
-// the rule, 6 query heads on a KV head, D 128:
+// so that nothing is left to join or to score, and nobody has to know the lengths of all rows.  GPU time
+// of a call without / with the rule, 6 query heads on a KV head, D 128:
 //   bf16, 56 rows: 64 tokens 8.0 / 4.9 us, 256 9.3 / 6.8, 512 9.7 / 8.9; 900 rows: 64 12.0 / 9.7, 512 46.9 / 40.1
 //   fp32, 56 rows: 64 tokens 12.4 / 6.4 us, 128 10.6 / 9.2, 256 13.7 / 15.1; 900 rows: 64 24.8 / 23.1
+//   with scores: bf16, 56 rows: 64 tokens 9.5 / 5.3 us, 512 11.2 / 10.6; 300 rows: 512 20.9 / 13.7
 // A CTA of the fp32 kernel takes three times as long over a tile, and so gains less by the wait it saves.
 constexpr int whole_tiles(int dtype) { return dtype == KVP_F32 ? 3 : 9; }
 // Rows per CTA up to which that holds.  More rows gain 8 % by it (16384 of ~64 tokens 152 / 140 us), but where
@@ -195,6 +195,30 @@ __device__ __forceinline__ void store_out4(const Params& p, size_t i, float4 x) 
     const __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
     *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) + i) =
         make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  }
+}
+
+// Adds the probabilities of tokens [m0, hi) of row r, `step` apart, to their scores; lse: base 2, of the
+// group's heads.
+template <int GP>
+__device__ __forceinline__ void add_row_scores(const Params& p, int r, int m0, int hi, int step, const float* lse_sh) {
+  float lse[GP];
+#pragma unroll
+  for (int h = 0; h < GP; ++h) lse[h] = h < p.G ? lse_sh[h] : 0.f;
+  for (int m = m0; m < hi; m += step) {
+    const float4* lg = reinterpret_cast<const float4*>(p.logits + ((size_t)r * p.c.cap + m) * GP);
+    float* score = p.c.score + (size_t)r * p.c.cap + m;
+    const float before = *score;
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < GP / 4; ++k) {
+      const float4 w = lg[k];
+      const float z[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (4 * k + i < p.G && z[i] != -INFINITY) s += fast_exp2(z[i] - lse[4 * k + i]);
+    }
+    *score = before + s;
   }
 }
 

@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(PM_THREADS, 2)
   int li = 0, turn = 0;
 
   // Row r, tiles [u0, u1) of its nt: merge the warps' states; the whole row's result, or a partial.
-  const auto finish = [&](int r, int u0, int u1, int nt) {
+  const auto finish = [&](int r, int n, int u0, int u1, int nt) {
     float* sm_m = reinterpret_cast<float*>(smem + C::OFF_ML) + turn * 2 * PM_CWARPS * GP;
     float* sm_l = sm_m + PM_CWARPS * GP;
     float* sm_o = reinterpret_cast<float*>(smem + C::OFF_O);
@@ -254,6 +254,7 @@ __global__ void __launch_bounds__(PM_THREADS, 2)
         const float l2 = L == 0.f ? -INFINITY : M + log2f(L);
         if (p.lse) p.lse[head0 + h] = l2 * KVP_LN2;
         if (p.lse2) p.lse2[(size_t)r * GP + h] = l2;
+        sm_l[h] = l2;            // only this thread reads the head's sums
       } else {
         part[h] = M;
         part[GP + h] = L;
@@ -295,6 +296,7 @@ __global__ void __launch_bounds__(PM_THREADS, 2)
       if (whole) paged::store_out4<T>(p, head0 * D + e, z);
       else *reinterpret_cast<float4*>(part + 2 * GP + e) = z;
     }
+    if (p.whole && p.logits) paged::add_row_scores<GP>(p, r, threadIdx.x, n, PM_CWARPS * 32, sm_l);
   };
 
   int r = g.row, u0 = g.tile, n = paged::row_len(p, r);
@@ -455,7 +457,7 @@ __global__ void __launch_bounds__(PM_THREADS, 2)
       if (lane == 0) ptx::mbar_arrive(bar_empty + 8 * s);
     }
     if (x + (u1 - u0) >= g.end) allow_next_grid();   // the join kernel's CTAs may take their places
-    if (u1 > u0) finish(r, u0, u1, nt);
+    if (u1 > u0) finish(r, n, u0, u1, nt);
     x += u1 - u0;
     ++r;
     u0 = 0;

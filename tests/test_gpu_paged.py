@@ -369,7 +369,8 @@ def test_decode_splits(kvp, dtype, lens):
 def capped(c, pages):
     """The same rows with a table cut to `pages` columns."""
     t = c.table[:, :pages].contiguous()
-    return type(c)(c.k_pool, c.v_pool, t, c.lens, c.refs, c.free_mask, None, None)
+    score = None if c.score is None else c.score[:, :pages * c.page_size].contiguous()
+    return type(c)(c.k_pool, c.v_pool, t, c.lens, c.refs, c.free_mask, score, None)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
@@ -398,9 +399,9 @@ def test_decode_of_short_rows(kvp, dtype, D, G, ps, cap, R):
     lens[torch.rand(R, generator=gen) < 0.3] = 0
     lens[R // 3:R // 3 + 9] = 0
     lens[R // 2], lens[-1] = cap, 0 if R > 1 else cap
-    c = capped(filled(kvp, lens.tolist(), ps, D, dtype, seed=R), cap // ps)
     q = torch.randn(1, R * G, D, generator=gen).to(DT[dtype]).cuda()
-    check_decode(kvp, c, q)
+    for scores in (False, True):
+        check_decode(kvp, capped(filled(kvp, lens.tolist(), ps, D, dtype, seed=R, scores=scores), cap // ps), q)
 
 
 def test_decode_extreme_values(kvp):
