@@ -20,12 +20,18 @@ using paged::Range;
 using paged::TILE;
 
 // The kernel of fp32 caches (the tensor cores have no fp32 products).  4 G D FMAs per 8 D bytes: bound
-// by HBM up to some four query heads, by the FMA pipe's issue slots above, so what surrounds the FMAs is
-// kept small.  A group of LPK lanes reads KB keys at a time, 16 bytes of each per lane.  Summing the
+// by HBM up to some four query heads; above, by what the two warps per scheduler that 2 D GP registers of
+// queries and outputs leave room for can issue, so what surrounds the FMAs is kept small.  A group of
+// LPK lanes reads KB keys at a time, 16 bytes of each per lane.  Summing the
 // KB * GP partial dot products over the lanes one by one would take log2(LPK) shuffles each; halving
 // exchanges (a lane passes on the half of its values that its partner keeps) take one each, and leave
 // every lane with the logit of one (key, head), so that the softmax is computed once and not LPK times.
 // The weights come back to all lanes through shared memory.
+// Few warps have few loads in flight: from five heads on, K and V come through a ring in shared memory,
+// in which a lane reads what it has copied itself.  64 rows x 8192 tokens, D 128, with the loads where
+// they are used / one step ahead in registers / the ring / and the weighted sums two at a time: 8 heads
+// 138 / 135 / 109 / 104 us, 16 heads 252 / 237 / 190 / 187 us (4 heads 84 us, 6.4 TB/s).  Six warps per
+// CTA, with three stages: 113 us.
 template <int D, int GP>
 struct Pf {
   static constexpr int LPK = D / 4;                        // lanes per key
@@ -35,9 +41,9 @@ struct Pf {
   static constexpr int WARPS = GP <= 4 ? 8 : 4;
   static constexpr int THREADS = 32 * WARPS;
   static constexpr int STATES = WARPS * SUBS;
-  // K and V of the next keys are asked for as soon as these ones' registers are free, where few warps fit:
-  // 64 rows x 8192 tokens, D 128, 16 heads 252 -> 237 us, 8 heads 138 -> 135; 4 heads spill, 85 -> 98 us.
-  static constexpr bool AHEAD = GP >= 8;
+  static constexpr int STAGES = GP <= 4 ? 1 : 16 / KB;     // steps of a warp under way
+  static constexpr int STAGE_BYTES = 2 * KB * 512;         // K, then V
+  static constexpr int SMEM = STAGES > 1 ? WARPS * STAGES * STAGE_BYTES : 0;
   static constexpr int HAVE = V > LPK ? V / LPK : 1;       // logits a lane ends up with
   static constexpr int SAME = LPK > V ? LPK / V : 1;       // lanes that end up with the same one
 };
@@ -70,6 +76,23 @@ __device__ __forceinline__ float4 stream_float4(const float* p) {
   return make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
 }
 
+// Two products and sums in one instruction, each rounded as by fmaf.  (The dot products gain nothing by
+// it: their halves still have to be added.)
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)), "l"(*reinterpret_cast<uint64_t*>(&c)));
+  return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(__cvta_generic_to_global(src)),
+               "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 template <int D, int GP>
 __global__ void __launch_bounds__(Pf<D, GP>::THREADS, GP <= 8 ? 2 : 1)
     paged_decode_f32_kernel(const float* __restrict__ q, const Params p) {
@@ -79,6 +102,7 @@ __global__ void __launch_bounds__(Pf<D, GP>::THREADS, GP <= 8 ? 2 : 1)
   __shared__ __align__(16) float st_o[C::STATES][GP][D];
   __shared__ __align__(16) float weight_sh[C::STATES][C::V];
   __shared__ float factor_sh[C::STATES][GP];
+  extern __shared__ __align__(16) uint8_t ring_raw[];      // per warp: STAGES of K and V
   wait_prior_grid();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, dl = lane % C::LPK;
   const int state = warp * C::SUBS + lane / C::LPK;
@@ -86,6 +110,8 @@ __global__ void __launch_bounds__(Pf<D, GP>::THREADS, GP <= 8 ? 2 : 1)
   const int key_of = first_value / GP, head_of = first_value % GP;
   const bool counts = dl % C::SAME == 0;                   // one of the lanes that have the same logit
   const int cta = blockIdx.x;
+  // a lane reads what it has copied itself, so that nobody has to be waited for
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(ring_raw) + warp * C::STAGES * C::STAGE_BYTES + lane * 16;
   const Range g = paged::find_range(p, cta, scan_sh);
   paged::empty_rows<float, D>(p, cta, C::THREADS);
   if (cta >= g.active) return;
@@ -120,28 +146,69 @@ __global__ void __launch_bounds__(Pf<D, GP>::THREADS, GP <= 8 ? 2 : 1)
     constexpr int STEP = C::STATES * C::KB;
     int m = lo + state * C::KB;
     const auto page_of = [&](int t) { return t < hi ? table[t >> c.shift] : 0; };
-    const auto fetch = [&](float4 (&x)[C::KB], const float* pool, int t, int page) {
+    const auto page_good = [&](int t, int page) {
       const bool good = page >= 0 && page < c.n_pages;
+      if (t < hi && !good) raise_status(p.status, KVP_ERR_DEVICE_CHECK);
+      return good;
+    };
+    // slots behind the row's end are not read, but cleared
+    const auto fetch = [&](float4 (&x)[C::KB], const float* pool, int t, int page, bool good) {
       const float* at = pool + page * c.page_stride + (t & (c.ps - 1)) * c.token_stride;
 #pragma unroll
       for (int i = 0; i < C::KB; ++i) {
-        x[i] = make_float4(0.f, 0.f, 0.f, 0.f);            // slots behind the row's end are not read
+        x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (good && t + i < hi) x[i] = stream_float4(at + i * c.token_stride);
       }
     };
-    int page = page_of(m), next = page_of(m + STEP);
-    float4 k[C::KB], v[C::KB];
-    if (C::AHEAD) {
-      fetch(k, kp, m, page);
-      fetch(v, vp, m, page);
+    uint32_t goods = 0;                      // a bit per stage
+    const auto issue = [&](int t, int page, int stage) {
+      const bool good = page_good(t, page);
+      goods = good ? goods | 1u << stage : goods & ~(1u << stage);
+      const int64_t at = page * c.page_stride + (t & (c.ps - 1)) * c.token_stride;
+#pragma unroll
+      for (int i = 0; i < C::KB; ++i) {
+        const bool live = good && t + i < hi;
+        const uint32_t to = ring + stage * C::STAGE_BYTES + i * 512;
+        cp_async16_zfill(to, live ? kp + at + i * c.token_stride : kp, live);
+        cp_async16_zfill(to + C::KB * 512, live ? vp + at + i * c.token_stride : vp, live);
+      }
+    };
+    const auto staged = [&](int stage, int i) {
+      return *reinterpret_cast<const float4*>(ring_raw + warp * C::STAGES * C::STAGE_BYTES + stage * C::STAGE_BYTES +
+                                              i * 512 + lane * 16);
+    };
+    int page = page_of(m), stage = 0;
+    if constexpr (C::STAGES > 1) {
+      int pages[C::STAGES];
+#pragma unroll
+      for (int i = 0; i < C::STAGES; ++i) pages[i] = page_of(m + i * STEP);
+#pragma unroll
+      for (int i = 0; i < C::STAGES - 1; ++i) {
+        if (lo + i * STEP < hi) issue(m + i * STEP, pages[i], i);
+        cp_async_commit();
+      }
+      page = pages[C::STAGES - 1];
     }
     for (int m0 = lo; m0 < hi; m0 += STEP, m += STEP) {
-      const bool good = page >= 0 && page < c.n_pages;
-      if (m < hi && !good) raise_status(p.status, KVP_ERR_DEVICE_CHECK);
-      const int after = page_of(m + 2 * STEP);
-      if (!C::AHEAD) {
-        fetch(k, kp, m, page);
-        fetch(v, vp, m, page);
+      float4 k[C::KB], v[C::KB];
+      bool good;
+      if constexpr (C::STAGES > 1) {
+        // the stage before this one has been read: its place is the next one's
+        const int next = page_of(m + C::STAGES * STEP);
+        if (m0 + (C::STAGES - 1) * STEP < hi)
+          issue(m + (C::STAGES - 1) * STEP, page, stage == 0 ? C::STAGES - 1 : stage - 1);
+        cp_async_commit();
+        page = next;
+        cp_async_wait<C::STAGES - 1>();
+        good = goods >> stage & 1;
+#pragma unroll
+        for (int i = 0; i < C::KB; ++i) k[i] = staged(stage, i);
+      } else {
+        const int next = page_of(m + STEP);
+        good = page_good(m, page);
+        fetch(k, kp, m, page, good);
+        fetch(v, vp, m, page, good);
+        page = next;
       }
       float s[C::V];
 #pragma unroll
@@ -149,7 +216,6 @@ __global__ void __launch_bounds__(Pf<D, GP>::THREADS, GP <= 8 ? 2 : 1)
 #pragma unroll
         for (int h = 0; h < GP; ++h)
           s[i * GP + h] = fmaf(qf[h].x, k[i].x, fmaf(qf[h].y, k[i].y, fmaf(qf[h].z, k[i].z, qf[h].w * k[i].w)));
-      if (C::AHEAD) fetch(k, kp, m + STEP, next);
       sum_scatter<C::V, C::LPK>(s);
       // this lane's logits, the new maxima of their heads (over the group's keys), the weights
       float w[C::HAVE], top[C::HAVE];
@@ -197,20 +263,22 @@ __global__ void __launch_bounds__(Pf<D, GP>::THREADS, GP <= 8 ? 2 : 1)
         sum[i] = to;
         if (counts) weight_sh[state][first_value + i] = w[i];
       }
+      if constexpr (C::STAGES > 1) {
+#pragma unroll
+        for (int i = 0; i < C::KB; ++i) v[i] = staged(stage, C::KB + i);
+      }
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < C::KB; ++i)
 #pragma unroll
         for (int h = 0; h < GP; ++h) {
-          const float f = weight_sh[state][i * GP + h];
-          o[h].x = fmaf(f, v[i].x, o[h].x);
-          o[h].y = fmaf(f, v[i].y, o[h].y);
-          o[h].z = fmaf(f, v[i].z, o[h].z);
-          o[h].w = fmaf(f, v[i].w, o[h].w);
+          const float w1 = weight_sh[state][i * GP + h];
+          const float2 f = make_float2(w1, w1);
+          const float2 a = fma2(f, make_float2(v[i].x, v[i].y), make_float2(o[h].x, o[h].y));
+          const float2 b = fma2(f, make_float2(v[i].z, v[i].w), make_float2(o[h].z, o[h].w));
+          o[h] = make_float4(a.x, a.y, b.x, b.y);
         }
-      if (C::AHEAD) fetch(v, vp, m + STEP, next);
-      page = next;
-      next = after;
+      if constexpr (C::STAGES > 1) stage = stage + 1 == C::STAGES ? 0 : stage + 1;
       __syncwarp();                          // the weights are read
     }
     // the sums of the lanes that share a head, then the states of the CTA
@@ -272,15 +340,19 @@ __global__ void __launch_bounds__(Pf<D, GP>::THREADS, GP <= 8 ? 2 : 1)
 
 template <int D>
 cudaError_t run_f32(const Params& p, const void* q, cudaStream_t st) {
-  const auto go = [&](auto kernel, int threads) {
+  const auto go = [&](auto kernel, int threads, int smem) {
+    if (smem > 0) {
+      const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (e != cudaSuccess) return e;
+    }
     count_launches(1);
-    return launch_with_pdl(kernel, dim3((unsigned)p.ctas), dim3((unsigned)threads), 0, st, (const float*)q, p);
+    return launch_with_pdl(kernel, dim3((unsigned)p.ctas), dim3((unsigned)threads), (size_t)smem, st, (const float*)q, p);
   };
-  if (p.G == 1) return go(paged_decode_f32_kernel<D, 1>, Pf<D, 1>::THREADS);
-  if (p.G == 2) return go(paged_decode_f32_kernel<D, 2>, Pf<D, 2>::THREADS);
-  if (p.G <= 4) return go(paged_decode_f32_kernel<D, 4>, Pf<D, 4>::THREADS);
-  if (p.G <= 8) return go(paged_decode_f32_kernel<D, 8>, Pf<D, 8>::THREADS);
-  return go(paged_decode_f32_kernel<D, 16>, Pf<D, 16>::THREADS);
+  if (p.G == 1) return go(paged_decode_f32_kernel<D, 1>, Pf<D, 1>::THREADS, Pf<D, 1>::SMEM);
+  if (p.G == 2) return go(paged_decode_f32_kernel<D, 2>, Pf<D, 2>::THREADS, Pf<D, 2>::SMEM);
+  if (p.G <= 4) return go(paged_decode_f32_kernel<D, 4>, Pf<D, 4>::THREADS, Pf<D, 4>::SMEM);
+  if (p.G <= 8) return go(paged_decode_f32_kernel<D, 8>, Pf<D, 8>::THREADS, Pf<D, 8>::SMEM);
+  return go(paged_decode_f32_kernel<D, 16>, Pf<D, 16>::THREADS, Pf<D, 16>::SMEM);
 }
 
 // Merges the partials of the rows that several CTAs share, and adds the tokens' probabilities to the

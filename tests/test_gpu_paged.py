@@ -655,6 +655,20 @@ def test_what_only_the_device_sees(kvp):
         assert torch.equal(t, b)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("G", [1, 4, 8, 16])
+def test_pages_out_of_range_spoil_their_row_only(kvp, dtype, G):
+    c = filled(kvp, [400, 700, 90, 33], 16, 128, dtype, seed=G, spare=3)
+    q = torch.randn(1, 4 * G, 128, generator=torch.Generator().manual_seed(G)).to(DT[dtype]).cuda()
+    out = kvp.kvp_paged_decode_attn(q, c)
+    for page in (-1, c.n_pages, -2 ** 31, 2 ** 31 - 1):
+        c.table[1, 17] = page
+        got = []
+        raises_status(kvp, lambda: got.append(kvp.kvp_paged_decode_attn(q, c)))
+        keep = [h for h in range(4 * G) if h // G != 1]
+        assert torch.equal(got[0][0, keep], out[0, keep]) and got[0].isfinite().all()
+
+
 def test_bits_behind_the_last_page_are_no_pages(kvp):
     c = kvp.PagedCache.empty(1, 3, 2, 16, 64, torch.float16)
     c.free_mask.fill_(-1)
