@@ -30,7 +30,7 @@ class _Desc(ctypes.Structure):
 class PagedCache:
     """The buffers of a paged cache, checked once.
 
-    k_pool, v_pool [n_pages, page_size, head_dim] (views with a contiguous last axis and equal
+    k_pool, v_pool [n_pages, page_size, head_dim] (views with a contiguous last axis and equal, non-zero
     strides will do: ``kv[:, 0]`` and ``kv[:, 1]`` of one [n_pages, 2, page_size, head_dim] buffer);
     table int32 [n_rows, max_pages]; lens int32 [n_rows]; refs int32 [n_pages]; free_mask int32
     [ceil(n_pages / 32)]; score float32 and pos int32 [n_rows, max_pages * page_size], each optional.
@@ -46,6 +46,9 @@ class PagedCache:
                 raise ValueError(f"{name} must be a CUDA tensor [n_pages, page_size, head_dim]")
             if t.stride(2) != 1:
                 raise ValueError(f"{name}: the head_dim axis must be contiguous")
+            # 0 stands for the dense stride in the descriptor, so a broadcast axis would run past the pool
+            if (t.shape[0] > 1 and t.stride(0) == 0) or (t.shape[1] > 1 and t.stride(1) == 0):
+                raise ValueError(f"{name}: the page and token axes must not be broadcast")
         if v_pool.shape != k_pool.shape or v_pool.dtype != k_pool.dtype or v_pool.stride() != k_pool.stride():
             raise ValueError("k_pool and v_pool must have the same shape, dtype and strides")
         n_pages, page_size, head_dim = k_pool.shape
