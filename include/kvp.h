@@ -474,9 +474,13 @@ int kvp_decode_attn_noalloc(const void* q, const void* kc, const void* vc, int d
  * attention its token has received, its source position); they move with the
  * tokens.
  * Pages are taken in a fixed order: the i-th page that a call needs (rows in
- * order, a row's pages in order) is the i-th lowest free one.  A row whose pages
- * run past the free ones is left as it was and KVP_ERR_DEVICE_CHECK is raised, as
- * it is for a page id, length, count or index out of range.
+ * order, a row's pages in order) is the i-th lowest free one.
+ * A row that a call cannot serve is left as it was, and KVP_ERR_DEVICE_CHECK is
+ * raised: its pages run past the free ones, its length, count or source is out of
+ * range, or (kvp_paged_compact) an index is not one of its tokens or not above the
+ * one before it, or a page id is out of range.  The other calls raise it for a page
+ * id out of range too, and pass over that page; what such a row then holds or gives
+ * is undefined, the other rows are served.
  * page_size is a power of two in [16, 1024]; 16-byte aligned pools; strides are
  * multiples of 16 bytes below 2^40 bytes.  max_pages * page_size <= 2^30,
  * n_rows * max_pages < 2^31 and n_rows * max_pages * page_size <= 2^36.
@@ -529,7 +533,10 @@ int kvp_paged_fork(const kvp_paged_cache* cache, const int32_t* src, int copy, v
  * idx [n_rows, b_max] int32, ascending; count [n_rows] int32 in [0, min(b_max,
  * lens[r])], negative: leave the row (kvp_select_topk's outputs).  A page that
  * other rows hold too is replaced by a fresh one if its tokens change; pages the
- * row no longer needs are released. */
+ * row no longer needs are released.
+ * kvp_select_topk takes one length T for all rows.  For rows of different lengths
+ * give it scores that are NaN behind each row's end and +inf where a token is kept
+ * in any case, budgets of at most lens[r], and n_sink = n_recent = 0. */
 size_t kvp_paged_compact_workspace_size(const kvp_paged_cache* cache, int b_max);
 int kvp_paged_compact(const kvp_paged_cache* cache, const int32_t* idx, const int32_t* count,
                       int b_max, void* workspace, size_t workspace_bytes, kvp_stream_t stream);

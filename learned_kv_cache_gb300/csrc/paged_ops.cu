@@ -140,9 +140,11 @@ __device__ __forceinline__ RowPlan row_plan(const PagedView& c, const PlanArgs& 
   return w;
 }
 
-// Which of a row's kept pages have to be fresh ones: those whose tokens change and that somebody
-// else holds too.  One CTA per row.
-constexpr int NEED_THREADS = 128;
+// Looks a row over, and says which of its kept pages have to be fresh ones: those whose tokens change and
+// that somebody else holds too.  One CTA per row.  A row is not touched unless every index and every page
+// id in it is good: behind this kernel nobody asks again.  Bound by latency.
+constexpr int NEED_THREADS = 512;
+constexpr int NEED_LOADS = 8;              // of a thread, under way at a time
 
 __global__ void __launch_bounds__(NEED_THREADS) compact_need_kernel(const PagedView c, const PlanArgs a) {
   __shared__ int scan_sh[33];
@@ -150,18 +152,37 @@ __global__ void __launch_bounds__(NEED_THREADS) compact_need_kernel(const PagedV
   wait_prior_grid();
   const int r = blockIdx.x, tid = threadIdx.x;
   const int cnt = a.count[r], n = c.lens[r];
-  const bool ok = n >= 0 && n <= c.cap && cnt <= n && cnt <= a.b_max;
+  const int32_t* idx = a.idx + (size_t)r * a.b_max;
+  const int32_t* table = table_row(c, r);
+  bool ok = n >= 0 && n <= c.cap && cnt <= n && cnt <= a.b_max;
+  if (ok && cnt >= 0) {
+    bool good = true;
+    // ascending from 0 on and below the length: then idx[m] >= m, too
+    for (int m0 = tid; m0 < cnt; m0 += NEED_LOADS * NEED_THREADS) {
+      int key[NEED_LOADS], before[NEED_LOADS];
+#pragma unroll
+      for (int u = 0; u < NEED_LOADS; ++u) {
+        const int m = m0 + u * NEED_THREADS;
+        key[u] = m < cnt ? idx[m] : 0;
+        before[u] = m < cnt && m > 0 ? idx[m - 1] : -1;
+      }
+#pragma unroll
+      for (int u = 0; u < NEED_LOADS; ++u) good &= key[u] > before[u] && key[u] < n;
+    }
+    const int held = pages_of(n, c);
+#pragma unroll 4
+    for (int j = tid; j < held; j += NEED_THREADS) good &= page_ok(table[j], c);
+    ok = __syncthreads_and(good);
+  }
   int need = 0;
   const int pages = ok && cnt > 0 ? pages_of(cnt, c) : 0;
   for (int j0 = 0; j0 < pages; j0 += NEED_THREADS) {
     const int j = j0 + tid;
     int d = -1;
     if (j < pages) {
-      const int p = table_row(c, r)[j];
       const int last = min((j + 1) << c.shift, cnt) - 1;   // ascending indices: if it stays, so do all before it
-      const bool moved = a.idx[(size_t)r * a.b_max + last] != last;
-      if (page_ok(p, c)) d = moved && c.refs[p] > 1 ? -2 : p;
-      else raise_status(a.status, KVP_ERR_DEVICE_CHECK);
+      const int p = table[j];
+      d = idx[last] != last && c.refs[p] > 1 ? -2 : p;
     }
     int all;
     const int before = block_exclusive_scan(d == -2, scan_sh, &all);
@@ -544,32 +565,25 @@ __global__ void __launch_bounds__(CP_THREADS) compact_pages_kernel(const PagedVi
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem);
   const uint32_t side_ring = ring + C::OFF_SIDE;
   const int chunks = (cnt + CP_TOK - 1) / CP_TOK;
-  bool bad = false;
 
   // A group's look-ups: what ask() loads, find() looks at some chunks later; what find() loads, place()
   // writes down some chunks after that.  Nothing is waited for where it is asked for.
-  int key[C::LOOKS], before[C::LOOKS], last_key[C::LOOKS], target[C::LOOKS], page[C::LOOKS];
+  // Indices and page ids are good: compact_need_kernel has looked at all of them.
+  int key[C::LOOKS], target[C::LOOKS], page[C::LOOKS];
   const auto ask = [&](int group) {
 #pragma unroll
     for (int x = 0; x < C::LOOKS; ++x) {
       const int m = group * CP_GROUP * CP_TOK + x * CP_THREADS + tid;
-      key[x] = before[x] = last_key[x] = target[x] = -1;
+      key[x] = target[x] = -1;
       if (m >= cnt) continue;
       key[x] = idx[m];
-      if (m > 0) before[x] = idx[m - 1];
-      last_key[x] = idx[min(((m >> c.shift) + 1) << c.shift, cnt) - 1];
       target[x] = dmap[m >> c.shift];
     }
   };
-  const auto find = [&](int group) {
+  const auto find = [&] {
 #pragma unroll
     for (int x = 0; x < C::LOOKS; ++x) {
-      const int m = group * CP_GROUP * CP_TOK + x * CP_THREADS + tid;
-      // a page whose last kept token stays was planned as unchanged (it may be shared): none may move
-      const int last = min(((m >> c.shift) + 1) << c.shift, cnt) - 1;
-      page[x] = -1;
-      if (m < cnt && key[x] >= m && key[x] < n && key[x] > before[x] && (key[x] == m || last_key[x] != last))
-        page[x] = table[key[x] >> c.shift];
+      page[x] = key[x] >= 0 ? table[key[x] >> c.shift] : -1;
       if (target[x] <= -2) target[x] = w.list[off - 2 - target[x]];
     }
   };
@@ -578,14 +592,10 @@ __global__ void __launch_bounds__(CP_THREADS) compact_pages_kernel(const PagedVi
     for (int x = 0; x < C::LOOKS; ++x) {
       const int m = group * CP_GROUP * CP_TOK + x * CP_THREADS + tid, at = m & (C::PLACES - 1);
       longlong2 z = make_longlong2(-1, -1);
-      if (m < cnt) {
-        if (page_ok(page[x], c) && page_ok(target[x], c)) {
-          z.x = page[x] * pgs + (key[x] & (c.ps - 1)) * ts;
-          z.y = target[x] * pgs + (m & (c.ps - 1)) * ts;
-          if (z.x == z.y) z.x = z.y = -1;
-        } else {
-          bad = true;
-        }
+      if (page[x] >= 0) {
+        z.x = page[x] * pgs + (key[x] & (c.ps - 1)) * ts;
+        z.y = target[x] * pgs + (m & (c.ps - 1)) * ts;
+        if (z.x == z.y) z.x = z.y = -1;
       }
       places[at] = z;
       index_sh[at] = key[x];
@@ -593,13 +603,13 @@ __global__ void __launch_bounds__(CP_THREADS) compact_pages_kernel(const PagedVi
   };
 
   ask(0);
-  find(0);
+  find();
   place(0);
   __syncthreads();
   for (int i = 0; i < chunks + C::STAGES - 1; ++i) {
     const int group = i / CP_GROUP + 1;
     if (i % CP_GROUP == 0) ask(group);
-    if (i % CP_GROUP == CP_GROUP / 2 - 1) find(group);
+    if (i % CP_GROUP == CP_GROUP / 2 - 1) find();
     if (i % CP_GROUP == CP_GROUP - 2) place(group);
     if (i < chunks) {
       const int t0 = (i * CP_TOK) & (C::PLACES - 1);
@@ -635,7 +645,6 @@ __global__ void __launch_bounds__(CP_THREADS) compact_pages_kernel(const PagedVi
       }
     }
   }
-  if (bad) raise_status(w.status, KVP_ERR_DEVICE_CHECK);
   cluster.sync();                            // every CTA has read the row's table and length
   const int old_pages = pages_of(n, c), new_pages = pages_of(cnt, c);
   release_pages(c, rank * CP_THREADS + tid, old_pages, nranks * CP_THREADS, w.status, [&](int j) {

@@ -206,7 +206,17 @@ def kvp_paged_fork(cache, src, copy=False, stream=None):
 
 def kvp_paged_compact(cache, idx, count, stream=None):
     """Keep, in place, the tokens idx [R, b_max] (int32, ascending) of every row, count [R] of them
-    (negative: leave the row), and release the pages that empties."""
+    (negative: leave the row), and release the pages that empties.  A row whose indices are not all its
+    own, or do not ascend, stays as it is and raises the device status.
+
+    kvp_select_topk takes one length for all rows.  For rows of different lengths give it scores that are
+    NaN (ranked last) behind each row's end and +inf where a token is to be kept in any case::
+
+        col, n = torch.arange(T, device=cache.device), cache.lens[:, None]
+        score = torch.where((col < n_sink) | (col >= n - n_recent), math.inf, cache.score[:, :T])
+        score = torch.where(col < n, score, math.nan)
+        idx, count = kvp_select_topk(score, torch.minimum(budgets, cache.lens), 0, 0, b_max, T=T)
+    """
     if _cache(cache)._elsewhere(stream):
         with cache._there(stream):
             return kvp_paged_compact(cache, idx, count)
