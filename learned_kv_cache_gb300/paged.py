@@ -127,7 +127,11 @@ class PagedCache:
 
     def _there(self, stream):
         """Makes them current, so that the call's temporaries belong to the stream that uses them."""
-        return torch.cuda.stream(stream) if stream is not None else torch.cuda.device(self.device)
+        if stream is None:
+            return torch.cuda.device(self.device)
+        if stream.device != self.device:
+            raise ValueError(f"stream must be on {self.device}, got {stream.device}")
+        return torch.cuda.stream(stream)
 
 
 def _cache(c):

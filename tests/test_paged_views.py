@@ -1,10 +1,12 @@
 """What PagedCache refuses by looking at tensors alone (fake CUDA tensors: no GPU, no data)."""
+import types
 import warnings
 
 import pytest
 import torch
 from torch._subclasses.fake_tensor import FakeTensorMode
 
+from learned_kv_cache_gb300 import paged
 from learned_kv_cache_gb300.paged import PagedCache
 
 
@@ -47,3 +49,16 @@ def test_strided_pools_are_taken():
     assert (c._desc.page_stride, c._desc.token_stride) == (2048, 128)
     c = cache(pool(1, 16, 64).expand(1, 16, 64))
     assert (c._desc.page_stride, c._desc.token_stride) == (0, 64)
+
+
+def test_a_stream_of_another_device_is_refused():
+    """It used to be dropped: the call ran on the current stream of the cache's device."""
+    c = cache(pool(100, 16, 64))
+    other = types.SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=0)
+    z, q = pool(4, 1, 64), pool(2, 4, 64)
+    for call in (lambda: paged.kvp_paged_init(c, stream=other), lambda: paged.kvp_paged_append(c, z, z, stream=other),
+                 lambda: paged.kvp_paged_fork(c, ints(4), stream=other), lambda: paged.kvp_paged_free(c, stream=other),
+                 lambda: paged.kvp_paged_compact(c, ints(4, 1), ints(4), stream=other),
+                 lambda: paged.kvp_paged_decode_attn(q, c, stream=other)):
+        with pytest.raises(ValueError, match="stream must be on cuda:0, got cuda:1"):
+            call()
