@@ -482,7 +482,7 @@ int kvp_decode_attn_noalloc(const void* q, const void* kc, const void* vc, int d
  * id out of range too, and pass over that page; what such a row then holds or gives
  * is undefined, the other rows are served.
  * page_size is a power of two in [16, 1024]; 16-byte aligned pools; strides are
- * multiples of 16 bytes below 2^40 bytes.  max_pages * page_size <= 2^30,
+ * multiples of 16 bytes below 2^40 bytes.  n_rows <= 2^28, max_pages * page_size <= 2^30,
  * n_rows * max_pages < 2^31 and n_rows * max_pages * page_size <= 2^36.
  * Calls that change a cache must be ordered with every other call on it (one
  * stream, or events); decode calls without add_scores may overlap each other,

@@ -139,7 +139,8 @@ int paged_view(const kvp_paged_cache* c, kvp::PagedView* out) {
     return fail(KVP_ERR_INVALID_ARG, "n_pages=%d n_rows=%d max_pages=%d must be >= 1", c->n_pages, c->n_rows,
                 c->max_pages);
   const long long cap = (long long)c->max_pages * c->page_size;
-  if (cap > (1LL << 30) || cap * c->n_rows > (1LL << 36) || (long long)c->n_rows * c->max_pages > 0x7fffffffLL)
+  // 2^28 rows: up to 4 blocks a row in a launch, and sums of the rows' pages, stay below 2^31
+  if (c->n_rows > (1 << 28) || cap > (1LL << 30) || cap * c->n_rows > (1LL << 36) || (long long)c->n_rows * c->max_pages > 0x7fffffffLL)
     return fail(KVP_ERR_INVALID_ARG, "table too large: n_rows=%d max_pages=%d page_size=%d", c->n_rows,
                 c->max_pages, c->page_size);
   if (!c->k_pool || !c->v_pool || !c->table || !c->lens || !c->refs || !c->free_mask)

@@ -99,3 +99,11 @@ def test_workspaces_grow_with_the_work(lib):
     assert lib.kvp_paged_fork_workspace_size(c, 0) == 0 and lib.kvp_paged_fork_workspace_size(c, 1) > 0
     assert lib.kvp_paged_append_workspace_size(c, 0) == 0
     assert lib.kvp_paged_decode_attn_workspace_size(c, 34, 2, 0) == 0
+
+
+def test_more_rows_than_a_launch_counts_are_refused(lib):
+    """A compaction launches up to 4 blocks a row (8 of few), an append sums up to n_new / 16 + 2 pages a row: both in 32 bits."""
+    for n_rows in ((1 << 28) + 1, 1 << 29, 1 << 30, (1 << 31) - 1):
+        test_a_bad_cache_is_refused_by_every_call(lib, dict(n_rows=n_rows, max_pages=1, page_size=16), -1)
+    c = desc(n_rows=1 << 28, max_pages=1, page_size=16)
+    assert lib.kvp_paged_compact_workspace_size(c, 16) >= 4 << 28
