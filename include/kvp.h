@@ -553,7 +553,8 @@ int kvp_paged_free(const kvp_paged_cache* cache, const int32_t* keep, kvp_stream
  *
  * q [n_layers, h_q, head_dim] dtype, q_stride elements from layer to layer (0 =
  * dense; multiple of 16 bytes); sm_scale is a double (1 / sqrt(128) is no float, and
- * its rounding is the same for every logit of a row, so it does not average out); out [n_layers, h_q, head_dim] of out_dtype
+ * its rounding is the same for every logit of a row, so it does not average out),
+ * sm_scale * log2(e) finite in 32 bits; out [n_layers, h_q, head_dim] of out_dtype
  * (KVP_F32 or the cache's dtype); lse [n_layers, h_q] float32 or NULL.  An empty
  * row gives out 0 and lse -inf.  add_scores = 1 adds every token's probability,
  * summed over the group's query heads, to cache->score.  G = h_q / h_kv <= 16.

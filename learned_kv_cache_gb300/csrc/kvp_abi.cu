@@ -821,7 +821,8 @@ int kvp_paged_decode_attn(const void* q, int64_t q_stride, const kvp_paged_cache
   if (!aligned16(q) || !aligned16(out)) return fail(KVP_ERR_INVALID_ARG, "q/out not 16-byte aligned");
   if (out_dtype != KVP_F32 && out_dtype != v.dtype)
     return fail(KVP_ERR_UNSUPPORTED, "out_dtype %d is neither KVP_F32 nor the cache's dtype", out_dtype);
-  if (!std::isfinite(sm_scale)) return fail(KVP_ERR_INVALID_ARG, "sm_scale not finite");
+  if (!std::isfinite((float)(sm_scale * 1.4426950408889634)))
+    return fail(KVP_ERR_INVALID_ARG, "sm_scale=%g: sm_scale * log2(e) must be finite in 32 bits", sm_scale);
   if (add_scores != 0 && add_scores != 1) return fail(KVP_ERR_INVALID_ARG, "add_scores must be 0 or 1");
   if (add_scores && !v.score) return fail(KVP_ERR_INVALID_ARG, "add_scores given, but the cache has no score");
   KVP_TRY(check_workspace(workspace, workspace_bytes, kvp::paged_decode_workspace(v, h_q, h_kv, add_scores)));

@@ -107,3 +107,10 @@ def test_more_rows_than_a_launch_counts_are_refused(lib):
         test_a_bad_cache_is_refused_by_every_call(lib, dict(n_rows=n_rows, max_pages=1, page_size=16), -1)
     c = desc(n_rows=1 << 28, max_pages=1, page_size=16)
     assert lib.kvp_paged_compact_workspace_size(c, 16) >= 4 << 28
+
+
+@pytest.mark.parametrize("scale", [1e300, -1e300, 3e38, float("inf")])
+def test_a_scale_that_is_no_float_is_refused(lib, scale):
+    """The kernels multiply by sm_scale * log2(e) in 32 bits; an infinite one would make every row NaN."""
+    assert decode(lib, desc(), scale=scale) == -1
+    assert b"sm_scale" in lib.kvp_last_error()
