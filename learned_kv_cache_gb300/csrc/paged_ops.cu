@@ -13,6 +13,8 @@
 // References are counted with integer atomics, whose order changes nothing.
 #include <cooperative_groups.h>
 
+#include <atomic>
+
 #include "kvp_common.cuh"
 #include "kvp_launch.h"
 
@@ -819,19 +821,27 @@ cudaLaunchConfig_t step_config(cudaLaunchAttribute (&attr)[2], cudaStream_t st) 
   return cfg;
 }
 
-// Clusters of 16 CTAs need 16 SMs that lie together, which a partitioned GPU may not have.
+// Clusters of 16 CTAs need 16 SMs that lie together, which a partitioned GPU may not have.  Every device is
+// asked once.
 bool step_clusters_fit() {
-  static const bool fit = [] {
+  static std::atomic<signed char> known[64];               // 1: they fit, -1: they do not
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();                      // not an error of the caller's
+    return false;
+  }
+  if (dev < 0 || dev >= 64) return false;
+  if (known[dev] == 0) {
     cudaLaunchAttribute attr[2];
     const cudaLaunchConfig_t cfg = step_config(attr, nullptr);
     int n = 0;
     const bool ok = cudaFuncSetAttribute(append_step_kernel<16>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
                         cudaSuccess &&
                     cudaOccupancyMaxActiveClusters(&n, append_step_kernel<16>, &cfg) == cudaSuccess && n > 0;
-    if (!ok) cudaGetLastError();             // not an error of the caller's
-    return ok;
-  }();
-  return fit;
+    if (!ok) cudaGetLastError();
+    known[dev] = ok ? 1 : -1;
+  }
+  return known[dev] > 0;
 }
 
 // Whether an append is a step: few rows and tokens.

@@ -1,5 +1,8 @@
 """What the paged calls refuse before anything is launched (no GPU needed: no pointer is followed)."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 
@@ -114,3 +117,37 @@ def test_a_scale_that_is_no_float_is_refused(lib, scale):
     """The kernels multiply by sm_scale * log2(e) in 32 bits; an infinite one would make every row NaN."""
     assert decode(lib, desc(), scale=scale) == -1
     assert b"sm_scale" in lib.kvp_last_error()
+
+
+FAKE_RUNTIME = """
+typedef struct { int on; int fits[4]; } state;
+state fake;
+int cudaGetDevice(int* d) { *d = fake.on; return 0; }
+int cudaGetLastError(void) { return 0; }
+int cudaFuncSetAttribute(const void* f, int a, int v) { return 0; }
+int cudaOccupancyMaxActiveClusters(int* n, const void* f, const void* c) { *n = fake.fits[fake.on]; return 0; }
+"""
+
+FAKE_USE = """
+import ctypes, sys
+lib, fake = ctypes.CDLL(sys.argv[1]), ctypes.CDLL(sys.argv[2])
+state = (ctypes.c_int * 5).in_dll(fake, "fake")
+desc = ctypes.create_string_buffer(bytes.fromhex(sys.argv[3]))
+lib.kvp_paged_append_workspace_size.restype = ctypes.c_size_t
+state[1:] = [9, 0, 9, 0]
+for device in (0, 1, 2, 3, 1, 0):
+    state[0] = device
+    print(device, lib.kvp_paged_append_workspace_size(desc, 1) == 0)
+"""
+
+
+def test_every_device_is_asked_for_its_clusters(lib, tmp_path):
+    """A step's append runs in one cluster of 16 where the current device holds one, not where the first device asked did
+    (the CUDA runtime's answers come from a stand-in)."""
+    fake = tmp_path / "fake.so"
+    (tmp_path / "fake.c").write_text(FAKE_RUNTIME)
+    subprocess.run(["gcc", "-shared", "-fPIC", "-o", str(fake), str(tmp_path / "fake.c")], check=True)
+    d = bytes(_Desc(**GOOD)).hex()
+    out = subprocess.run([sys.executable, "-c", FAKE_USE, _lib.LIB_PATH, str(fake), d], check=True, capture_output=True, text=True,
+                         env={**os.environ, "LD_PRELOAD": str(fake)}).stdout.split()
+    assert out == "0 True 1 False 2 True 3 False 1 False 0 True".split()
