@@ -18,6 +18,7 @@
 //    bf16 would leave 2^-17 of every weight in an fp32 output.
 //  * f16 weights are kept 2^14 above the softmax's own (the reference is the maximum minus 14): below
 //    2^-14 an f16 part loses bits, and beside a sink token that is where all the others' weights lie.
+//    What the two parts leave of a weight is 2^-22 of it, and never more than 2^-39 of the row's largest.
 //  * The tensor cores' running sum drops bits at every step, always towards zero; over the hundreds of
 //    tiles of a long row that would show, and in the logits of a sink token too.  Each step of 16 is
 //    summed on its own and added in fp32; a logit keeps what its last sum and its scaling round away
