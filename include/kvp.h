@@ -560,7 +560,8 @@ int kvp_paged_free(const kvp_paged_cache* cache, const int32_t* keep, kvp_stream
  * summed over the group's query heads, to cache->score.  G = h_q / h_kv <= 16.
  * The work is split by the rows' lengths on the device, so one captured call
  * serves a cache that grows and shrinks.  Slots behind a row's last token may
- * hold anything; the outputs must not overlap q.  workspace:
+ * hold anything; an infinite V of a token that has weight makes its outputs infinite
+ * or NaN; the outputs must not overlap q.  workspace:
  * kvp_paged_decode_attn_workspace_size() bytes, 256-byte aligned (a few MB, none
  * for tables of few tokens a row; with add_scores 32 or 64 bytes per slot of the
  * table besides, for the logits). */

@@ -349,7 +349,9 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const PagedVie
 // 16-byte vectors throughout: VPR of them make one token's K (or V); consecutive threads take
 // consecutive vectors of a token.
 
-// Division by a number that the launch fixes: q = (x * mul) >> (32 + shift), exact for x < 2^31.
+// Division by a number that the launch fixes (a product with its rounded-up reciprocal: Granlund and
+// Montgomery, "Division by Invariant Integers using Multiplication"): q = (x * mul) >> (32 + shift).  mul
+// exceeds the reciprocal's 2^(32 + shift) by less than `by` <= 2^(shift + 1), so q is exact for x < 2^31.
 struct FastDiv {
   uint32_t mul, shift, by;
 };
@@ -435,8 +437,8 @@ __global__ void __launch_bounds__(256) append_copy_kernel(const PagedView c, con
 // A decode step's append in one launch and without a workspace: one cluster, whose first CTA makes the
 // plan in its shared memory; the others read it there.  The plan is what a step takes long for, and a
 // second launch and a workspace cost the host as much again: 56 rows x 1 token + decode + free 15.4 ->
-// 14.7 us of GPU time, a call from Python 13.2 -> 6.2 us of host time (256 rows that all have a shared
-// tail to copy: 8.5 -> 12.1 us of GPU time).
+// 14.7 us of GPU time, a call from Python 13.2 -> 6.2 us of host time.  Shared tails, which 16 SMs copy with
+// a warp per row, take longer than in the wide kernels (append_is_step).
 constexpr int AS_ROWS = 512;               // their numbers and the list are in static shared memory
 constexpr int AS_PAGES = 1024;
 constexpr int AS_CTAS = 16;                // the largest cluster: the copies have that many SMs
@@ -665,7 +667,9 @@ __global__ void __launch_bounds__(CP_THREADS) compact_pages_kernel(const PagedVi
 
 // ------------------------------------------------------------------ sharing and releasing
 
-// Row r takes the pages of row src[r]; one CTA per row.  Bound by latency (56 forks of 1024 pages 3.9 us).
+// Row r takes the pages of row src[r]; one CTA per row.  Bound by latency: 56 forks of 1024 pages 3.9 us.  With
+// scores and positions it is those that take long, 256 slots in turn: 56 forks of 1024 tokens 3.8 us, of 8192
+// 13 us, of 131072 170 us (their bytes, 117 MB, would be 18 us).
 __global__ void __launch_bounds__(256) fork_kernel(const PagedView c, const int32_t* __restrict__ src, int* status) {
   wait_prior_grid();
   const int r = blockIdx.x, s = src[r];
@@ -844,7 +848,12 @@ bool step_clusters_fit() {
   return known[dev] > 0;
 }
 
-// Whether an append is a step: few rows and tokens.
+// Whether an append is a step: few rows and tokens.  The rule goes by the host time of a call, and by the GPU
+// time of rows with tails of their own (8 / 64 / 256 rows: 4.7 / 5.3 / 6.4 us, plan and copies apart 6.2 / 6.8 /
+// 7.3).  It does not look at the tails that are shared: those are copied by 16 SMs here and by all of them
+// there, which shows from pages of 256 tokens on.  GPU time, rows in pairs on the same pages, half a page to
+// copy for each, in one launch / plan and copies apart: 256 rows, pages of 32 tokens 11.3 / 9.3 us, 256 29 /
+// 13, 1024 92 / 32; 8 rows, 32 7.5 / 7.0, 256 15.8 / 8.9, 1024 47 / 14.
 bool append_is_step(const PagedView& c, int n_new) {
   const int vpr = c.D * (c.dtype == KVP_F32 ? 4 : 2) / 16;
   return c.R <= AS_ROWS && append_list_cap(c, n_new) <= AS_PAGES &&
