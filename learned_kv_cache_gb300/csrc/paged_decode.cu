@@ -670,10 +670,10 @@ cudaError_t launch_paged_decode(const PagedView& c, const PagedDecodeArgs& a, vo
   const double c2 = a.scale * 1.4426950408889634;
   p.c2 = (float)c2;
   // The fp32 kernel's logit is s * c2 + s * c2_low, which for an infinite s has to be infinite too: c2_low
-  // gets c2's sign and is never 0.  (A test in the kernel costs 3 % with 4 query heads a group, 5 % with 16.)
+  // gets c2's sign and is 0 only with it.  (A test in the kernel costs 3 % with 4 query heads a group, 5 % with 16.)
   if (c.dtype == KVP_F32 && std::fabs((double)p.c2) > std::fabs(c2)) p.c2 = std::nextafter(p.c2, 0.f);
   p.c2_low = (float)(c2 - (double)p.c2);
-  if (c.dtype == KVP_F32 && p.c2_low == 0.f) p.c2_low = std::copysign(FLT_MIN, p.c2);
+  if (c.dtype == KVP_F32 && p.c2 != 0.f && p.c2_low == 0.f) p.c2_low = std::copysign(FLT_MIN, p.c2);
   p.out = a.out;
   p.out_f32 = a.out_f32;
   p.lse = a.lse;

@@ -204,3 +204,20 @@ def test_a_ragged_cache_is_evicted_again_and_again(kvp, dtype):  # noqa: F811
             kvp.kvp_paged_free(c.rows(R, 2 * R))
     kvp.kvp_paged_free(c)
     assert int(c.refs.sum()) == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("G", [1, 8])
+def test_a_scale_of_zero_gives_the_mean(kvp, dtype, G):  # noqa: F811
+    """Dot products up to 2^126, of either sign, weigh the same: out is off by the sums of 40 values and a division, 2^-23
+    each of the mean magnitude (and exp2(0) and the weights are exact)."""
+    c = filled(kvp, [40, 3], 16, 64, dtype, seed=G)
+    c.k_pool.copy_(torch.randn(c.k_pool.shape, generator=torch.Generator().manual_seed(1)) * 2.0 ** 120)
+    q = torch.randn(1, 2 * G, 64, generator=torch.Generator().manual_seed(2)).to(DT[dtype]).cuda()
+    out, lse = kvp.kvp_paged_decode_attn(q, c, sm_scale=0.0, return_lse=True)
+    kvp.kvp_check_device_status()
+    _, v = rows_of(c)
+    for r, n in enumerate((40, 3)):
+        got, want = out[0, r * G:(r + 1) * G].double().cpu(), v[r].double()
+        assert ((got - want.mean(0)).abs() <= 44 * 2.0 ** -23 * want.abs().mean(0)).all()
+        assert (lse[0, r * G:(r + 1) * G].double().cpu() - np.log(n)).abs().max() <= 2.0 ** -20
