@@ -144,7 +144,7 @@ __device__ __forceinline__ RowPlan row_plan(const PagedView& c, const PlanArgs& 
 
 // Looks a row over, and says which of its kept pages have to be fresh ones: those whose tokens change and
 // that somebody else holds too.  One CTA per row.  A row is not touched unless every index and every page
-// id in it is good: behind this kernel nobody asks again.  Bound by latency.
+// id in it is good.  Bound by latency.
 constexpr int NEED_THREADS = 512;
 constexpr int NEED_LOADS = 8;              // of a thread, under way at a time
 
@@ -572,7 +572,8 @@ __global__ void __launch_bounds__(CP_THREADS) compact_pages_kernel(const PagedVi
 
   // A group's look-ups: what ask() loads, find() looks at some chunks later; what find() loads, place()
   // writes down some chunks after that.  Nothing is waited for where it is asked for.
-  // Indices and page ids are good: compact_need_kernel has looked at all of them.
+  // Indices and page ids are good, compact_need_kernel has looked at all of them; the bounds here hold for
+  // indices that change under the call (in memory that it writes, say): nothing outside the pools is reached.
   int key[C::LOOKS], target[C::LOOKS], page[C::LOOKS];
   const auto ask = [&](int group) {
 #pragma unroll
@@ -587,7 +588,7 @@ __global__ void __launch_bounds__(CP_THREADS) compact_pages_kernel(const PagedVi
   const auto find = [&] {
 #pragma unroll
     for (int x = 0; x < C::LOOKS; ++x) {
-      page[x] = key[x] >= 0 ? table[key[x] >> c.shift] : -1;
+      page[x] = (uint32_t)key[x] < (uint32_t)n ? table[key[x] >> c.shift] : -1;
       if (target[x] <= -2) target[x] = w.list[off - 2 - target[x]];
     }
   };
@@ -596,7 +597,7 @@ __global__ void __launch_bounds__(CP_THREADS) compact_pages_kernel(const PagedVi
     for (int x = 0; x < C::LOOKS; ++x) {
       const int m = group * CP_GROUP * CP_TOK + x * CP_THREADS + tid, at = m & (C::PLACES - 1);
       longlong2 z = make_longlong2(-1, -1);
-      if (page[x] >= 0) {
+      if (page_ok(page[x], c) && page_ok(target[x], c)) {
         z.x = page[x] * pgs + (key[x] & (c.ps - 1)) * ts;
         z.y = target[x] * pgs + (m & (c.ps - 1)) * ts;
         if (z.x == z.y) z.x = z.y = -1;
