@@ -19,6 +19,10 @@
  * only the pages its kept tokens need: kvp_paged_init, kvp_paged_append,
  * kvp_paged_fork, kvp_paged_compact, kvp_paged_free and kvp_paged_decode_attn.
  *
+ * What stands between a model's projections and those: kvp_rope (rotary
+ * positions) and kvp_qk_norm_rope (norms of queries and keys with the rotation
+ * in the same pass; kvp_qk_norm_rope_backward its gradients).
+ *
  * Conventions shared by every entry point
  * ---------------------------------------
  * - Every pointer argument is a DEVICE pointer unless stated otherwise; the
@@ -448,6 +452,87 @@ int kvp_decode_attn(const void* q, const void* kc, const void* vc, int dtype, in
 int kvp_decode_attn_noalloc(const void* q, const void* kc, const void* vc, int dtype, int n_layers,
                             int h_q, int h_kv, int head_dim, int T_cap, const int32_t* len,
                             float sm_scale, float* out, kvp_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Rotary positions.
+ *
+ * The attention passes and the caches take queries and keys as the model's
+ * attention sees them: rotated by their positions.  With pairs (a, b) of the first
+ * rotary_dim values of a head -- (i, i + rotary_dim / 2), or (2i, 2i + 1) when
+ * interleaved -- and the angle t = position * inv_freq[i]:
+ *
+ *   a' = gain * (a cos t - b sin t),   b' = gain * (b cos t + a sin t)
+ *
+ * and the values behind rotary_dim unchanged.  inverse = 1 turns by -t (times gain):
+ * the gradient of the rotation, or, with the positions' differences, keys moved back
+ * to other positions when an eviction closes up the tokens it keeps.  Angles are
+ * exact to 2^-32 of a turn for every 32-bit position, negative ones among them;
+ * values are computed in 32 bits and rounded once.
+ *
+ * rope: HOST struct; inv_freq a HOST array of rotary_dim / 2 radians per position in
+ * [0, 1e6], which the call has read when it returns.  rotary_dim: a multiple of 16 up
+ * to head_dim.
+ * x, out [n_batch, n_heads, seq_len, head_dim] dtype with HOST element strides
+ * {batch, head, token}, NULL = dense (queries and keys of a fused projection, whose
+ * heads follow each other, are one call); multiples of 16 bytes below 2^40 bytes,
+ * those of an extent of 1 ignored; the output's elements must not overlap.  out may
+ * be x itself (same pointer and strides), else they must not overlap.
+ * positions int32 (device): of token s of batch b at [b * position_stride + s]
+ * (stride 0: the same for every batch), or NULL: start + s.
+ * ------------------------------------------------------------------------- */
+typedef struct kvp_rope_freqs {
+  const double* inv_freq;
+  int rotary_dim;
+  int interleaved;
+  double gain;           /* on cosine and sine; 1 but for some scalings */
+} kvp_rope_freqs;
+
+int kvp_rope(const void* x, void* out, int dtype, int n_batch, int n_heads, int seq_len,
+             int head_dim, const int64_t* x_strides, const int64_t* out_strides,
+             const kvp_rope_freqs* rope, const int32_t* positions, int64_t position_stride,
+             int start, int inverse, kvp_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Norms of queries and keys, with the rotation in the same pass.
+ *
+ * Every head of every token on its own, over its head_dim values:
+ *
+ *   n = x / sqrt(mean(x^2) + eps),   out = rotation of (weight * n)
+ *
+ * q, q_out [n_batch, h_q, seq_len, head_dim], k, k_out [n_batch, h_kv, ...] and their
+ * strides, positions and rope as in kvp_rope (rope NULL: norms alone).  q_weight,
+ * k_weight [head_dim] of weight_dtype (dtype or KVP_F32), each NULL for ones.
+ * Computed in 32 bits, rounded once.
+ *
+ * kvp_qk_norm_rope_backward: from the gradients of the outputs and the inputs q, k,
+ * with dz the gradient turned back,
+ *
+ *   dweight = sum over all rows of dz * n    (float32 [head_dim], each NULL: not wanted)
+ *   dx = (weight * dz - n * mean(weight * dz * n)) / sqrt(mean(x^2) + eps)
+ *
+ * dq may be dq_out or q itself, dk likewise.  Sums are taken in a fixed order:
+ * results do not depend on timing.  workspace:
+ * kvp_qk_norm_rope_backward_workspace_size() bytes, 256-byte aligned.
+ * ------------------------------------------------------------------------- */
+int kvp_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out, int dtype,
+                     int n_batch, int h_q, int h_kv, int seq_len, int head_dim,
+                     const int64_t* q_strides, const int64_t* k_strides,
+                     const int64_t* q_out_strides, const int64_t* k_out_strides,
+                     const void* q_weight, const void* k_weight, int weight_dtype, double eps,
+                     const kvp_rope_freqs* rope, const int32_t* positions, int64_t position_stride,
+                     int start, kvp_stream_t stream);
+size_t kvp_qk_norm_rope_backward_workspace_size(int dtype, int n_batch, int h_q, int h_kv,
+                                                int seq_len, int head_dim);
+int kvp_qk_norm_rope_backward(const void* dq_out, const void* dk_out, const void* q, const void* k,
+                              void* dq, void* dk, float* dq_weight, float* dk_weight, int dtype,
+                              int n_batch, int h_q, int h_kv, int seq_len, int head_dim,
+                              const int64_t* dq_out_strides, const int64_t* dk_out_strides,
+                              const int64_t* q_strides, const int64_t* k_strides,
+                              const int64_t* dq_strides, const int64_t* dk_strides,
+                              const void* q_weight, const void* k_weight, int weight_dtype,
+                              double eps, const kvp_rope_freqs* rope, const int32_t* positions,
+                              int64_t position_stride, int start, void* workspace,
+                              size_t workspace_bytes, kvp_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * The paged cache.

@@ -50,6 +50,10 @@ SIGNATURES = {
     "kvp_decode_attn": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _F, _P, _P, _P, _I, _I, _P,
                              _SZ, _P]),
     "kvp_decode_attn_noalloc": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _F, _P, _P]),
+    "kvp_rope": (_I, [_P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _I64, _I, _I, _P]),
+    "kvp_qk_norm_rope": (_I, [_P] * 4 + [_I] * 6 + [_P] * 6 + [_I, _D, _P, _P, _I64, _I, _P]),
+    "kvp_qk_norm_rope_backward_workspace_size": (_SZ, [_I] * 6),
+    "kvp_qk_norm_rope_backward": (_I, [_P] * 8 + [_I] * 6 + [_P] * 8 + [_I, _D, _P, _P, _I64, _I, _P, _SZ, _P]),
     # the first argument of the paged calls is a host kvp_paged_cache struct
     "kvp_paged_init": (_I, [_P, _P]),
     "kvp_paged_append_workspace_size": (_SZ, [_P, _I]),

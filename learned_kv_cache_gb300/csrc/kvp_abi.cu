@@ -206,6 +206,95 @@ int new_token_strides(const char* name, const int64_t* given, const kvp::PagedVi
   return KVP_OK;
 }
 
+// Element strides {batch, head, token} of a [n_batch, heads, seq_len, head_dim] tensor; NULL: dense.  An
+// output's elements must not overlap.
+int rope_strides(const char* name, const int64_t* given, bool output, int dtype, int n_batch, int heads, int S, int D,
+                 int64_t out[3]) {
+  out[2] = D;
+  out[1] = (int64_t)S * D;
+  out[0] = out[1] * heads;
+  if (!given) return KVP_OK;
+  const int elt = elem_size(dtype);
+  const int64_t extent[3] = {n_batch, heads, S};
+  for (int i = 0; i < 3; ++i) {
+    if (extent[i] <= 1) {
+      out[i] = 0;
+      continue;
+    }
+    if (given[i] < 0 || given[i] >= (1LL << 40) / elt || (given[i] * elt) % 16 != 0)
+      return fail(KVP_ERR_INVALID_ARG, "%s[%d]=%lld: strides must be multiples of 16 bytes in [0, 2^40) bytes", name, i,
+                  (long long)given[i]);
+    out[i] = given[i];
+  }
+  if (!output) return KVP_OK;
+  int order[3] = {0, 1, 2};
+  std::sort(order, order + 3, [&](int a, int b) { return out[a] < out[b]; });
+  int64_t span = D;                  // elements from the first to the last so far
+  for (int i : order) {
+    if (extent[i] <= 1) continue;
+    if (out[i] < span) return fail(KVP_ERR_INVALID_ARG, "%s: elements of the output overlap", name);
+    span += out[i] * (extent[i] - 1);
+  }
+  return KVP_OK;
+}
+
+// The arguments that the rotation and the norms share.
+int rope_args(const char* rope_name, int dtype, int n_batch, int seq_len, int head_dim, const kvp_rope_freqs* rope,
+              const int32_t* positions, int64_t position_stride, int start, kvp::RopeArgs* a) {
+  if (dtype != KVP_F32 && dtype != KVP_BF16 && dtype != KVP_F16)
+    return fail(KVP_ERR_UNSUPPORTED, "dtype %d is not one of KVP_F32/KVP_BF16/KVP_F16", dtype);
+  if (head_dim != 64 && head_dim != 128) return fail(KVP_ERR_UNSUPPORTED, "head_dim=%d", head_dim);
+  if (n_batch < 1 || seq_len < 1 || (long long)n_batch * seq_len > 0x7fffffffLL)
+    return fail(KVP_ERR_INVALID_ARG, "n_batch=%d seq_len=%d must be >= 1, with fewer than 2^31 tokens", n_batch, seq_len);
+  a->n_batch = n_batch;
+  a->seq_len = seq_len;
+  if (rope) {
+    if (rope->rotary_dim < 16 || rope->rotary_dim > head_dim || rope->rotary_dim % 16)
+      return fail(KVP_ERR_UNSUPPORTED, "%s: rotary_dim=%d (a multiple of 16 up to head_dim=%d is supported)", rope_name,
+                  rope->rotary_dim, head_dim);
+    if (!rope->inv_freq) return fail(KVP_ERR_INVALID_ARG, "%s: null inv_freq", rope_name);
+    for (int i = 0; i < rope->rotary_dim / 2; ++i)
+      if (!(rope->inv_freq[i] >= 0 && rope->inv_freq[i] <= 1e6))
+        return fail(KVP_ERR_INVALID_ARG, "%s: inv_freq[%d]=%g outside [0, 1e6]", rope_name, i, rope->inv_freq[i]);
+    if (rope->interleaved != 0 && rope->interleaved != 1)
+      return fail(KVP_ERR_INVALID_ARG, "%s: interleaved must be 0 or 1", rope_name);
+    if (!std::isfinite((float)rope->gain)) return fail(KVP_ERR_INVALID_ARG, "%s: gain not finite in 32 bits", rope_name);
+    a->inv_freq = rope->inv_freq;
+    a->rotary_dim = rope->rotary_dim;
+    a->interleaved = rope->interleaved;
+    a->gain = (float)rope->gain;
+  }
+  if (positions) {
+    if (position_stride != 0 && position_stride < seq_len)
+      return fail(KVP_ERR_INVALID_ARG, "position_stride=%lld: 0 or at least seq_len=%d", (long long)position_stride, seq_len);
+  } else if ((long long)start + seq_len - 1 > 0x7fffffffLL) {
+    return fail(KVP_ERR_INVALID_ARG, "start=%d + seq_len=%d passes 2^31", start, seq_len);
+  }
+  a->positions = positions;
+  a->position_stride = position_stride;
+  a->start = start;
+  return KVP_OK;
+}
+
+int norm_args(int h_q, int h_kv, int dtype, const void* q_weight, const void* k_weight, int weight_dtype, double eps,
+              kvp::RopeArgs* a) {
+  if (h_q < 1 || h_kv < 1) return fail(KVP_ERR_INVALID_ARG, "h_q=%d h_kv=%d must be >= 1", h_q, h_kv);
+  if ((q_weight || k_weight) && weight_dtype != dtype && weight_dtype != KVP_F32)
+    return fail(KVP_ERR_UNSUPPORTED, "weight_dtype %d is neither the tensors' dtype nor KVP_F32", weight_dtype);
+  const int elt = elem_size(weight_dtype);
+  if (((uintptr_t)q_weight | (uintptr_t)k_weight) & (uintptr_t)(elt - 1))
+    return fail(KVP_ERR_INVALID_ARG, "weights not aligned to their type");
+  if (!(eps >= 0) || !std::isfinite((float)eps)) return fail(KVP_ERR_INVALID_ARG, "eps=%g: >= 0 and finite in 32 bits", eps);
+  a->n_tensors = 2;
+  a->eps = (float)eps;
+  a->w_f32 = weight_dtype == KVP_F32;
+  a->t[0].heads = h_q;
+  a->t[1].heads = h_kv;
+  a->t[0].w = q_weight;
+  a->t[1].w = k_weight;
+  return KVP_OK;
+}
+
 std::atomic<unsigned long long> g_launches{0};
 
 #define KVP_TRY(x)            \
@@ -691,6 +780,96 @@ int kvp_decode_attn_noalloc(const void* q, const void* kc, const void* vc, int d
   e = kvp::launch_decode(q, kc, vc, dtype, n_layers, h_q, h_kv, head_dim, T_cap, len, sm_scale, out,
                          nullptr, nullptr, 0, 0, plan, scratch, st, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "kvp_decode_attn_noalloc launch");
+  return KVP_OK;
+}
+
+int kvp_rope(const void* x, void* out, int dtype, int n_batch, int n_heads, int seq_len, int head_dim,
+             const int64_t* x_strides, const int64_t* out_strides, const kvp_rope_freqs* rope,
+             const int32_t* positions, int64_t position_stride, int start, int inverse, kvp_stream_t stream) {
+  g_last_error.clear();
+  kvp::RopeArgs a{};
+  if (!rope) return fail(KVP_ERR_INVALID_ARG, "null rope");
+  KVP_TRY(rope_args("rope", dtype, n_batch, seq_len, head_dim, rope, positions, position_stride, start, &a));
+  if (!x || !out) return fail(KVP_ERR_INVALID_ARG, "null x/out");
+  if (n_heads < 1) return fail(KVP_ERR_INVALID_ARG, "n_heads=%d must be >= 1", n_heads);
+  if (!aligned16(x) || !aligned16(out)) return fail(KVP_ERR_INVALID_ARG, "x/out not 16-byte aligned");
+  if (inverse != 0 && inverse != 1) return fail(KVP_ERR_INVALID_ARG, "inverse must be 0 or 1");
+  a.n_tensors = 1;
+  a.inverse = inverse;
+  a.t[0].x = x;
+  a.t[0].y = out;
+  a.t[0].heads = n_heads;
+  KVP_TRY(rope_strides("x_strides", x_strides, false, dtype, n_batch, n_heads, seq_len, head_dim, a.t[0].xs));
+  KVP_TRY(rope_strides("out_strides", out_strides, true, dtype, n_batch, n_heads, seq_len, head_dim, a.t[0].ys));
+  cudaError_t e = kvp::launch_rope(a, dtype, head_dim, 0, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "kvp_rope launch");
+  return KVP_OK;
+}
+
+int kvp_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out, int dtype, int n_batch, int h_q, int h_kv,
+                     int seq_len, int head_dim, const int64_t* q_strides, const int64_t* k_strides,
+                     const int64_t* q_out_strides, const int64_t* k_out_strides, const void* q_weight,
+                     const void* k_weight, int weight_dtype, double eps, const kvp_rope_freqs* rope,
+                     const int32_t* positions, int64_t position_stride, int start, kvp_stream_t stream) {
+  g_last_error.clear();
+  kvp::RopeArgs a{};
+  KVP_TRY(rope_args("rope", dtype, n_batch, seq_len, head_dim, rope, positions, position_stride, start, &a));
+  KVP_TRY(norm_args(h_q, h_kv, dtype, q_weight, k_weight, weight_dtype, eps, &a));
+  if (!q || !k || !q_out || !k_out) return fail(KVP_ERR_INVALID_ARG, "null q/k/q_out/k_out");
+  if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(k_out))
+    return fail(KVP_ERR_INVALID_ARG, "q/k/q_out/k_out not 16-byte aligned");
+  a.t[0].x = q;
+  a.t[1].x = k;
+  a.t[0].y = q_out;
+  a.t[1].y = k_out;
+  KVP_TRY(rope_strides("q_strides", q_strides, false, dtype, n_batch, h_q, seq_len, head_dim, a.t[0].xs));
+  KVP_TRY(rope_strides("k_strides", k_strides, false, dtype, n_batch, h_kv, seq_len, head_dim, a.t[1].xs));
+  KVP_TRY(rope_strides("q_out_strides", q_out_strides, true, dtype, n_batch, h_q, seq_len, head_dim, a.t[0].ys));
+  KVP_TRY(rope_strides("k_out_strides", k_out_strides, true, dtype, n_batch, h_kv, seq_len, head_dim, a.t[1].ys));
+  cudaError_t e = kvp::launch_rope(a, dtype, head_dim, 1, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "kvp_qk_norm_rope launch");
+  return KVP_OK;
+}
+
+size_t kvp_qk_norm_rope_backward_workspace_size(int dtype, int n_batch, int h_q, int h_kv, int seq_len, int head_dim) {
+  kvp::RopeArgs a{};
+  if (rope_args("rope", dtype, n_batch, seq_len, head_dim, nullptr, nullptr, 0, 0, &a) != KVP_OK || h_q < 1 || h_kv < 1)
+    return 0;
+  a.t[0].heads = h_q;
+  a.t[1].heads = h_kv;
+  return kvp::norm_rope_backward_workspace(a, head_dim);
+}
+
+int kvp_qk_norm_rope_backward(const void* dq_out, const void* dk_out, const void* q, const void* k, void* dq, void* dk,
+                              float* dq_weight, float* dk_weight, int dtype, int n_batch, int h_q, int h_kv,
+                              int seq_len, int head_dim, const int64_t* dq_out_strides, const int64_t* dk_out_strides,
+                              const int64_t* q_strides, const int64_t* k_strides, const int64_t* dq_strides,
+                              const int64_t* dk_strides, const void* q_weight, const void* k_weight, int weight_dtype,
+                              double eps, const kvp_rope_freqs* rope, const int32_t* positions,
+                              int64_t position_stride, int start, void* workspace, size_t workspace_bytes,
+                              kvp_stream_t stream) {
+  g_last_error.clear();
+  kvp::RopeArgs a{};
+  KVP_TRY(rope_args("rope", dtype, n_batch, seq_len, head_dim, rope, positions, position_stride, start, &a));
+  KVP_TRY(norm_args(h_q, h_kv, dtype, q_weight, k_weight, weight_dtype, eps, &a));
+  if (!dq_out || !dk_out || !q || !k || !dq || !dk) return fail(KVP_ERR_INVALID_ARG, "null dq_out/dk_out/q/k/dq/dk");
+  if (!aligned16(dq_out) || !aligned16(dk_out) || !aligned16(q) || !aligned16(k) || !aligned16(dq) || !aligned16(dk))
+    return fail(KVP_ERR_INVALID_ARG, "dq_out/dk_out/q/k/dq/dk not 16-byte aligned");
+  a.t[0].x = q;
+  a.t[1].x = k;
+  a.t[0].dy = dq_out;
+  a.t[1].dy = dk_out;
+  a.t[0].y = dq;
+  a.t[1].y = dk;
+  KVP_TRY(rope_strides("dq_out_strides", dq_out_strides, false, dtype, n_batch, h_q, seq_len, head_dim, a.t[0].dys));
+  KVP_TRY(rope_strides("dk_out_strides", dk_out_strides, false, dtype, n_batch, h_kv, seq_len, head_dim, a.t[1].dys));
+  KVP_TRY(rope_strides("q_strides", q_strides, false, dtype, n_batch, h_q, seq_len, head_dim, a.t[0].xs));
+  KVP_TRY(rope_strides("k_strides", k_strides, false, dtype, n_batch, h_kv, seq_len, head_dim, a.t[1].xs));
+  KVP_TRY(rope_strides("dq_strides", dq_strides, true, dtype, n_batch, h_q, seq_len, head_dim, a.t[0].ys));
+  KVP_TRY(rope_strides("dk_strides", dk_strides, true, dtype, n_batch, h_kv, seq_len, head_dim, a.t[1].ys));
+  KVP_TRY(check_workspace(workspace, workspace_bytes, kvp::norm_rope_backward_workspace(a, head_dim)));
+  cudaError_t e = kvp::launch_norm_rope_backward(a, dtype, head_dim, dq_weight, dk_weight, workspace, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "kvp_qk_norm_rope_backward launch");
   return KVP_OK;
 }
 

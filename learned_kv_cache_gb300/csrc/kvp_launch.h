@@ -181,6 +181,32 @@ cudaError_t launch_decode(const void* q, const void* kc, const void* vc, int dty
                           int T_src, int accumulate, const DecodePlan& plan, void* ws,
                           int* status, cudaStream_t st);
 
+// ------------------------------------------------------------------ rotary positions, norms of Q and K
+// One tensor [n_batch, heads, seq_len, head_dim] by element strides {batch, head, token}: x -> y, or
+// (gradients) x, dy -> y = dx.
+struct RopeTensor {
+  const void *x, *dy;
+  void* y;
+  int64_t xs[3], dys[3], ys[3];
+  const void* w;         // [head_dim] or null
+  int heads;
+};
+struct RopeArgs {
+  RopeTensor t[2];
+  int n_tensors, n_batch, seq_len;
+  const double* inv_freq;   // host, [rotary_dim / 2]
+  int rotary_dim, interleaved, inverse;
+  float gain, eps;
+  int w_f32;             // weights are float, not the tensors' type
+  const int32_t* positions;
+  int64_t position_stride;
+  int start;
+};
+cudaError_t launch_rope(const RopeArgs& a, int dtype, int head_dim, int norm, cudaStream_t st);
+size_t norm_rope_backward_workspace(const RopeArgs& a, int head_dim);
+cudaError_t launch_norm_rope_backward(const RopeArgs& a, int dtype, int head_dim, float* dw0, float* dw1, void* ws,
+                                      cudaStream_t st);
+
 // ------------------------------------------------------------------ paged cache
 // A validated kvp_paged_cache with its strides filled in (elements).
 struct PagedView {

@@ -1,0 +1,270 @@
+"""Rotary positions and the norms of queries and keys (see include/kvp.h).
+
+:class:`Rope` holds a model's frequencies; the functions beside it are the C ABI's calls, with the
+checks of shapes, types and devices that need no look at the data.  Gradients are calls of their
+own (``kvp_rope`` with ``inverse``, ``kvp_qk_norm_rope_backward``): like the rest of this package
+they are not recorded by autograd.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+from ._lib import _DTYPE, _check, _dtype, _need, load
+from .paged import _raw_stream
+
+
+class _Freqs(ctypes.Structure):
+    """kvp_rope_freqs."""
+    _fields_ = [("inv_freq", ctypes.POINTER(ctypes.c_double)), ("rotary_dim", ctypes.c_int),
+                ("interleaved", ctypes.c_int), ("gain", ctypes.c_double)]
+
+
+class Rope:
+    """The frequencies of a rotation of the first ``rotary_dim`` values of a head.
+
+    inv_freq[i] = theta ** (-2 i / rotary_dim) radians per position for the pairs (i, i + rotary_dim / 2),
+    or (2i, 2i + 1) when ``interleaved``; for contexts ``factor`` times longer than the ``original_len``
+    a model was trained on, with ``scaling``:
+
+    * ``"linear"``: every frequency divided by the factor (positions interpolated);
+    * ``"ntk"``: theta times factor ** (rotary_dim / (rotary_dim - 2)), which leaves the fastest pair as it
+      is and divides the slowest by the factor;
+    * ``"bands"``: wavelengths above original_len / low divided, those below original_len / high left,
+      between them a blend that is linear in the turns within original_len;
+    * ``"yarn"``: a ramp over the pairs that turn beta_fast ... beta_slow times within original_len, and
+      cosine and sine times 0.1 ln(factor) + 1 (or ``gain``).
+
+    ``inv_freq`` (a sequence of rotary_dim / 2 numbers) gives the frequencies instead.
+    """
+
+    def __init__(self, rotary_dim, theta=10000.0, interleaved=False, scaling="none", factor=1.0, original_len=None,
+                 low=1.0, high=4.0, beta_fast=32.0, beta_slow=1.0, gain=None, inv_freq=None):
+        r = int(rotary_dim)
+        if r < 16 or r > 128 or r % 16:
+            raise ValueError(f"rotary_dim must be a multiple of 16 in [16, 128], got {rotary_dim}")
+        if scaling not in ("none", "linear", "ntk", "bands", "yarn"):
+            raise ValueError(f"unknown scaling {scaling!r}")
+        if scaling == "none":
+            factor = 1.0
+        if not (factor > 0 and math.isfinite(factor)):
+            raise ValueError(f"factor must be positive and finite, got {factor}")
+        if scaling in ("bands", "yarn") and (original_len is None or original_len < 1):
+            raise ValueError(f"scaling {scaling!r} needs original_len >= 1")
+        if inv_freq is None:
+            if not (theta > 1 and math.isfinite(theta)):
+                raise ValueError(f"theta must be above 1 and finite, got {theta}")
+            inv_freq = self._scaled(r, theta, scaling, factor, original_len, low, high, beta_fast, beta_slow)
+        elif scaling != "none":
+            raise ValueError("inv_freq is given: it takes no scaling")
+        inv_freq = [float(f) for f in inv_freq]
+        if len(inv_freq) != r // 2:
+            raise ValueError(f"inv_freq must hold {r // 2} numbers, got {len(inv_freq)}")
+        if not all(0 <= f <= 1e6 for f in inv_freq):
+            raise ValueError("inv_freq must lie in [0, 1e6]")
+        if gain is None:
+            gain = 0.1 * math.log(factor) + 1.0 if scaling == "yarn" and factor > 1 else 1.0
+        if not math.isfinite(gain):
+            raise ValueError("gain must be finite")
+        self.rotary_dim, self.interleaved, self.gain, self.inv_freq = r, bool(interleaved), float(gain), tuple(inv_freq)
+        self._array = (ctypes.c_double * (r // 2))(*inv_freq)
+        self._desc = _Freqs(self._array, r, int(self.interleaved), self.gain)
+        self._ref = ctypes.byref(self._desc)
+
+    @staticmethod
+    def _scaled(r, theta, scaling, factor, n, low, high, beta_fast, beta_slow):
+        if scaling == "ntk":
+            if r <= 2:
+                raise ValueError("ntk scaling needs more than one pair")
+            theta *= factor ** (r / (r - 2))
+        inv = [theta ** (-2 * i / r) for i in range(r // 2)]
+        if scaling == "linear":
+            return [f / factor for f in inv]
+        if scaling == "bands":
+            if not high > low:
+                raise ValueError("bands need high > low")
+            keep = [min(max((n * f / (2 * math.pi) - low) / (high - low), 0.0), 1.0) for f in inv]
+            return [(1 - s) * f / factor + s * f for f, s in zip(inv, keep)]
+        if scaling == "yarn":
+            if not beta_fast > beta_slow > 0:
+                raise ValueError("yarn needs beta_fast > beta_slow > 0")
+
+            def pair(turns):             # the (fractional) pair that turns so often within n positions
+                return r * math.log(n / (turns * 2 * math.pi)) / (2 * math.log(theta))
+            lo, hi = max(math.floor(pair(beta_fast)), 0), min(math.ceil(pair(beta_slow)), r - 1)
+            ramp = [min(max((i - lo) / max(hi - lo, 1e-3), 0.0), 1.0) for i in range(r // 2)]
+            return [f / factor * t + f * (1 - t) for f, t in zip(inv, ramp)]
+        return inv
+
+
+def _elsewhere(device, stream):
+    return stream is not None or torch.cuda.current_device() != device.index
+
+
+def _there(device, stream):
+    """The call's device and stream made the current ones, so that its temporaries belong to them."""
+    if stream is None:
+        return torch.cuda.device(device)
+    if stream.device != device:
+        raise ValueError(f"stream must be on {device}, got {stream.device}")
+    return torch.cuda.stream(stream)
+
+
+def _rows(t, name, like=None, heads=None):
+    """[B, H, S, D] or [H, S, D] with a contiguous last axis: (the 4-dim view, strides or None)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() == 3:
+        t = t.unsqueeze(0)
+    if t.dim() != 4:
+        raise ValueError(f"{name} must be [B, H, S, D] or [H, S, D]")
+    if like is not None:
+        if t.device != like.device:
+            raise ValueError(f"{name} must be on {like.device}, got {t.device}")
+        if t.dtype != like.dtype:
+            raise ValueError(f"{name} must be {like.dtype}, got {t.dtype}")
+        shape = (like.shape[0], like.shape[1] if heads is None else heads, like.shape[2], like.shape[3])
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.is_contiguous():
+        return t, None
+    s = t.stride()
+    if s[3] != 1:
+        raise ValueError(f"{name}: the head_dim axis must be contiguous")
+    return t, (ctypes.c_int64 * 3)(s[0], s[1], s[2])
+
+
+def _positions(positions, like):
+    """int32 [S] or [B, S] (rows of consecutive positions in memory): (pointer, stride)."""
+    if positions is None:
+        return None, 0
+    if not isinstance(positions, torch.Tensor):
+        raise TypeError("positions must be a torch.Tensor")
+    B, S = like.shape[0], like.shape[2]
+    if positions.device != like.device:
+        raise ValueError(f"positions must be on {like.device}, got {positions.device}")
+    if positions.dtype != torch.int32:
+        raise ValueError(f"positions must be torch.int32, got {positions.dtype}")
+    if positions.shape != (S,) and positions.shape != (B, S):
+        raise ValueError(f"positions must have shape ({S},) or ({B}, {S}), got {tuple(positions.shape)}")
+    if S > 1 and positions.stride(-1) != 1:
+        raise ValueError("positions must be contiguous along the tokens")
+    return positions.data_ptr(), positions.stride(0) if positions.dim() == 2 and B > 1 else 0
+
+
+def _rope_ref(rope):
+    if rope is None:
+        return None
+    if not isinstance(rope, Rope):
+        raise TypeError("rope must be a Rope")
+    return rope._ref
+
+
+def kvp_rope(x, rope, positions=None, start=0, inverse=False, out=None, stream=None):
+    """Rotate x [B, H, S, D] (or [H, S, D]; strided views are read in place) by the positions of its tokens:
+    int32 [S] or [B, S], or start, start + 1, ...  ``inverse`` turns back (the rotation's gradient).  ``out`` may
+    be x itself; by default a new dense tensor."""
+    x4, xs = _rows(x, "x")
+    if _elsewhere(x4.device, stream):
+        with _there(x4.device, stream):
+            return kvp_rope(x, rope, positions, start, inverse, out)
+    if rope is None:
+        raise TypeError("rope must be a Rope")
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    out4, os = _rows(out, "out", x4)
+    pos, ps = _positions(positions, x4)
+    B, H, S, D = x4.shape
+    rc = load().kvp_rope(x4.data_ptr(), out4.data_ptr(), _dtype(x4), B, H, S, D, xs, os, _rope_ref(rope), pos, ps,
+                         int(start), int(bool(inverse)), _raw_stream(x4.device.index))
+    _check("kvp_rope", rc)
+    return out
+
+
+def _weights(q_weight, k_weight, q4):
+    D, dtype = q4.shape[3], q4.dtype
+    given = [(n, w) for n, w in (("q_weight", q_weight), ("k_weight", k_weight)) if w is not None]
+    for name, w in given:
+        _need(w, name, None, (D,))
+        if w.device != q4.device:
+            raise ValueError(f"{name} must be on {q4.device}, got {w.device}")
+        if w.dtype not in (q4.dtype, torch.float32):
+            raise ValueError(f"{name} must be {q4.dtype} or torch.float32, got {w.dtype}")
+        if w.dtype != given[0][1].dtype:
+            raise ValueError("q_weight and k_weight must have the same dtype")
+        dtype = w.dtype
+    return (None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(),
+            _DTYPE[dtype])
+
+
+def kvp_qk_norm_rope(q, k, q_weight=None, k_weight=None, eps=1e-6, rope=None, positions=None, start=0, q_out=None,
+                     k_out=None, stream=None):
+    """Norms of every head of q [B, H_q, S, D] and k [B, H_kv, S, D] (or without B; strided views are read in
+    place) over its D values, times the weights [D] (of q's dtype or float32; None: ones), rotated as by
+    :func:`kvp_rope` (rope None: not rotated) -> (q_out, k_out).  The outputs may be q and k themselves."""
+    q4, qs = _rows(q, "q")
+    if _elsewhere(q4.device, stream):
+        with _there(q4.device, stream):
+            return kvp_qk_norm_rope(q, k, q_weight, k_weight, eps, rope, positions, start, q_out, k_out)
+    dtype = _dtype(q4)
+    B, Hq, S, D = q4.shape
+    Hkv = k.shape[-3] if isinstance(k, torch.Tensor) and k.dim() >= 3 else 0
+    k4, ks = _rows(k, "k", q4, Hkv)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if k_out is None:
+        k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+    qo4, qos = _rows(q_out, "q_out", q4)
+    ko4, kos = _rows(k_out, "k_out", k4)
+    pos, ps = _positions(positions, q4)
+    qw, kw, wd = _weights(q_weight, k_weight, q4)
+    rc = load().kvp_qk_norm_rope(q4.data_ptr(), k4.data_ptr(), qo4.data_ptr(), ko4.data_ptr(), dtype, B, Hq, Hkv, S, D,
+                                 qs, ks, qos, kos, qw, kw, wd, float(eps), _rope_ref(rope), pos, ps, int(start),
+                                 _raw_stream(q4.device.index))
+    _check("kvp_qk_norm_rope", rc)
+    return q_out, k_out
+
+
+def kvp_qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight=None, k_weight=None, eps=1e-6, rope=None, positions=None,
+                              start=0, dq=None, dk=None, workspace=None, stream=None):
+    """Gradients of :func:`kvp_qk_norm_rope` from those of its outputs and its inputs ->
+    (dq, dk, dq_weight, dk_weight), the last two float32 [D] (of weights that are None as of ones).
+    dq may be dq_out or q itself, dk likewise."""
+    q4, qs = _rows(q, "q")
+    if _elsewhere(q4.device, stream):
+        with _there(q4.device, stream):
+            return kvp_qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, eps, rope, positions, start, dq,
+                                             dk, workspace)
+    dtype = _dtype(q4)
+    B, Hq, S, D = q4.shape
+    Hkv = k.shape[-3] if isinstance(k, torch.Tensor) and k.dim() >= 3 else 0
+    k4, ks = _rows(k, "k", q4, Hkv)
+    gq4, gqs = _rows(dq_out, "dq_out", q4)
+    gk4, gks = _rows(dk_out, "dk_out", k4)
+    if dq is None:
+        dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if dk is None:
+        dk = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+    dq4, dqs = _rows(dq, "dq", q4)
+    dk4, dks = _rows(dk, "dk", k4)
+    pos, ps = _positions(positions, q4)
+    qw, kw, wd = _weights(q_weight, k_weight, q4)
+    dw = torch.empty(2, D, dtype=torch.float32, device=q4.device)
+    if workspace is None:
+        need = int(load().kvp_qk_norm_rope_backward_workspace_size(dtype, B, Hq, Hkv, S, D))
+        workspace = torch.empty(need, dtype=torch.uint8, device=q4.device)
+    else:
+        _need(workspace, "workspace", torch.uint8)
+        if workspace.device != q4.device:
+            raise ValueError(f"workspace must be on {q4.device}, got {workspace.device}")
+    rc = load().kvp_qk_norm_rope_backward(gq4.data_ptr(), gk4.data_ptr(), q4.data_ptr(), k4.data_ptr(), dq4.data_ptr(),
+                                          dk4.data_ptr(), dw.data_ptr(), dw.data_ptr() + 4 * D, dtype, B, Hq, Hkv, S, D,
+                                          gqs, gks, qs, ks, dqs, dks, qw, kw, wd, float(eps), _rope_ref(rope), pos, ps,
+                                          int(start), workspace.data_ptr(), workspace.numel(),
+                                          _raw_stream(q4.device.index))
+    _check("kvp_qk_norm_rope_backward", rc)
+    return dq, dk, dw[0], dw[1]

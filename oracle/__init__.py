@@ -27,6 +27,8 @@ Functions and the passages they follow:
   Scoring" (the sparse log-normalisers).
 * :mod:`oracle.paged` -- LKV, "LKV-H" and How much KV cache can you prune, "Conclusion" (rows of
   different budgets on one pool of pages).
+* :func:`rotate`, :func:`norm_rope`, :func:`norm_rope_backward` -- the rotary positions and the per-head
+  norms of the queries and keys that all of these take (the formulas stand in :mod:`oracle.rope`).
 * :func:`soft_topk`, :func:`head_budgets` -- LKV, "The Differentiable Soft-TopK
   Operator" and "LKV-H".
 
@@ -42,6 +44,7 @@ from .auc import eviction_auc, eviction_cost_curve, normalized_auc, optimal_auc,
 from .chunked import chunk_compress_step, chunked_prefill_compress
 from .fenwick import fenwick_cutoffs, sparse_mask, sparse_row_lse
 from .ring import ring_insert, ring_victim
+from .rope import norm_rope, norm_rope_backward, rotate
 from .selection import compact_kv, effective_budget, select_row, select_topk
 
 __all__ = [
@@ -49,4 +52,5 @@ __all__ = [
     "compact_kv", "decode_attn", "soft_topk", "head_budgets", "ring_insert", "ring_victim",
     "fenwick_cutoffs", "sparse_mask", "sparse_row_lse", "chunk_compress_step", "chunked_prefill_compress",
     "paged", "rank_by_scores", "eviction_cost_curve", "eviction_auc", "optimal_auc", "normalized_auc",
+    "rotate", "norm_rope", "norm_rope_backward",
 ]
