@@ -657,6 +657,34 @@ int kvp_paged_decode_attn(const void* q, int64_t q_stride, const kvp_paged_cache
                           int add_scores, void* workspace, size_t workspace_bytes,
                           kvp_stream_t stream);
 
+/* Decode attention of sequences that share a long prefix: kvp_paged_decode_attn's
+ * out and lse, with the pages that several rows hold in common read once for all of
+ * them.
+ *
+ * lead [n_rows / h_kv] int32 (device): the sequence whose leading pages a sequence may
+ * share (kvp_paged_fork's src, by sequences), itself or a negative number for one that
+ * follows nobody.  It only says where to look: for every KV head, the pages that the
+ * tables of the two rows have in common from the start on, and that both have filled,
+ * are the shared prefix, so rows that were evicted or grew on their own since the fork
+ * are served as they are.  Of the members' shared lengths of a family the one that
+ * saves most reads is taken (out of more than 32 members, 32 lengths are looked at),
+ * and members that share less read all their tokens themselves.  A sequence whose lead
+ * follows a third one reads for itself; a lead >= n_rows / h_kv does too, and raises
+ * KVP_ERR_DEVICE_CHECK.
+ *
+ * q, q_stride, sm_scale and lse as in kvp_paged_decode_attn; out [n_rows / h_kv, h_q,
+ * head_dim] of the cache's dtype.  G = h_q / h_kv <= 16; at most KVP_PREFIX_MAX_SEQS
+ * sequences.  The plan of the work is made on the device: a captured call serves a
+ * cache and families that change.  workspace:
+ * kvp_paged_prefix_decode_attn_workspace_size() bytes, 256-byte aligned (some 4
+ * outputs of float32 per query, and 20 or 40 MB). */
+#define KVP_PREFIX_MAX_SEQS 16384
+size_t kvp_paged_prefix_decode_attn_workspace_size(const kvp_paged_cache* cache, int h_q, int h_kv);
+int kvp_paged_prefix_decode_attn(const void* q, int64_t q_stride, const kvp_paged_cache* cache,
+                                 const int32_t* lead, int h_q, int h_kv, double sm_scale, void* out,
+                                 float* lse, void* workspace, size_t workspace_bytes,
+                                 kvp_stream_t stream);
+
 /* ---------------------------------------------------------------------------
  * Status and diagnostics.
  * ------------------------------------------------------------------------- */

@@ -65,6 +65,8 @@ SIGNATURES = {
     "kvp_paged_free": (_I, [_P, _P, _P]),
     "kvp_paged_decode_attn_workspace_size": (_SZ, [_P, _I, _I, _I]),
     "kvp_paged_decode_attn": (_I, [_P, _I64, _P, _I, _I, _D, _P, _I, _P, _I, _P, _SZ, _P]),
+    "kvp_paged_prefix_decode_attn_workspace_size": (_SZ, [_P, _I, _I]),
+    "kvp_paged_prefix_decode_attn": (_I, [_P, _I64, _P, _P, _I, _I, _D, _P, _P, _P, _SZ, _P]),
     "kvp_status_string": (ctypes.c_char_p, [_I]),
     "kvp_last_error": (ctypes.c_char_p, []),
     "kvp_check_device_status": (_I, [_P]),

@@ -1013,4 +1013,43 @@ int kvp_paged_decode_attn(const void* q, int64_t q_stride, const kvp_paged_cache
   return KVP_OK;
 }
 
+size_t kvp_paged_prefix_decode_attn_workspace_size(const kvp_paged_cache* cache, int h_q, int h_kv) {
+  kvp::PagedView v;
+  if (paged_view(cache, &v) != KVP_OK || h_q < 1 || h_kv < 1 || h_q % h_kv || h_q / h_kv > 16 || v.R % h_kv ||
+      v.R / h_kv > KVP_PREFIX_MAX_SEQS)
+    return 0;
+  return kvp::paged_prefix_workspace(v, h_q, h_kv);
+}
+
+int kvp_paged_prefix_decode_attn(const void* q, int64_t q_stride, const kvp_paged_cache* cache, const int32_t* lead,
+                                 int h_q, int h_kv, double sm_scale, void* out, float* lse, void* workspace,
+                                 size_t workspace_bytes, kvp_stream_t stream) {
+  g_last_error.clear();
+  kvp::PagedView v;
+  KVP_TRY(paged_view(cache, &v));
+  if (!q || !lead || !out) return fail(KVP_ERR_INVALID_ARG, "null q/lead/out");
+  if (h_q < 1 || h_kv < 1) return fail(KVP_ERR_INVALID_ARG, "h_q=%d h_kv=%d must be >= 1", h_q, h_kv);
+  if (h_q % h_kv) return fail(KVP_ERR_INVALID_ARG, "h_q=%d not a multiple of h_kv=%d", h_q, h_kv);
+  if (v.R % h_kv) return fail(KVP_ERR_INVALID_ARG, "n_rows=%d not a multiple of h_kv=%d", v.R, h_kv);
+  if (h_q / h_kv > 16) return fail(KVP_ERR_UNSUPPORTED, "group size %d > 16", h_q / h_kv);
+  if (v.R / h_kv > KVP_PREFIX_MAX_SEQS)
+    return fail(KVP_ERR_UNSUPPORTED, "%d sequences in one call (at most %d)", v.R / h_kv, KVP_PREFIX_MAX_SEQS);
+  const int64_t dense = (int64_t)h_q * v.D;
+  if (q_stride == 0) q_stride = dense;
+  const int elt = elem_size(v.dtype);
+  if (q_stride < dense || q_stride >= (1LL << 40) / elt || (q_stride * elt) % 16 != 0)
+    return fail(KVP_ERR_INVALID_ARG, "q_stride=%lld: at least h_q * head_dim and a multiple of 16 bytes below 2^40 bytes",
+                (long long)q_stride);
+  if (!aligned16(q) || !aligned16(out)) return fail(KVP_ERR_INVALID_ARG, "q/out not 16-byte aligned");
+  if (!std::isfinite((float)(sm_scale * 1.4426950408889634)))
+    return fail(KVP_ERR_INVALID_ARG, "sm_scale=%g: sm_scale * log2(e) must be finite in 32 bits", sm_scale);
+  KVP_TRY(check_workspace(workspace, workspace_bytes, kvp::paged_prefix_workspace(v, h_q, h_kv)));
+  int* st = nullptr;
+  KVP_TRY(status_ptr(&st));
+  const kvp::PagedPrefixArgs a{q, q_stride, lead, h_q, h_kv, sm_scale, out, lse};
+  cudaError_t e = kvp::launch_paged_prefix_decode(v, a, workspace, st, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "kvp_paged_prefix_decode_attn launch");
+  return KVP_OK;
+}
+
 }  // extern "C"

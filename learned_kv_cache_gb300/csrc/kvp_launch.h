@@ -250,5 +250,17 @@ struct PagedDecodeArgs {
 size_t paged_decode_workspace(const PagedView& c, int h_q, int h_kv, int add_scores);
 cudaError_t launch_paged_decode(const PagedView& c, const PagedDecodeArgs& a, void* ws, int* status,
                                 cudaStream_t st);
+struct PagedPrefixArgs {
+  const void* q;
+  int64_t q_stride;
+  const int32_t* lead;   // [R / h_kv]
+  int h_q, h_kv;
+  double scale;
+  void* out;             // of the cache's type
+  float* lse;
+};
+size_t paged_prefix_workspace(const PagedView& c, int h_q, int h_kv);
+cudaError_t launch_paged_prefix_decode(const PagedView& c, const PagedPrefixArgs& a, void* ws, int* status,
+                                       cudaStream_t st);
 
 }  // namespace kvp

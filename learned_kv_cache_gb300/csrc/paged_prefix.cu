@@ -1,0 +1,613 @@
+// One-token decode attention for sequences that share a long prefix: the pages that rows hold in common are
+// read once for all of them.
+//
+//   out = sum_t softmax_t(scale * q . k_t) v_t,  lse = ln sum_t exp(scale * q . k_t)
+//
+// over the row's tokens t, in two parts joined by their log-sum-exps: the prefix, a product of all the
+// family's queries with each tile of keys, and the row's own tokens.  What is shared is seen in the tables
+// (equal page ids), so a wrong `lead` costs time and no correctness.
+#include <cmath>
+
+#include "kvp_common.cuh"
+#include "kvp_launch.h"
+#include "paged_prefix.cuh"
+
+namespace kvp {
+namespace {
+
+using prefix::Item;
+using prefix::Params;
+using prefix::Piece;
+using prefix::TILE;
+
+constexpr int LOOK_THREADS = 256;
+
+// The sequence that l follows: its lead, if that follows nobody itself.
+__device__ __forceinline__ int root_of(const Params& p, int l) {
+  const int x = p.lead[l];
+  if (x < 0 || x == l || x >= p.N) return l;
+  const int y = p.lead[x];
+  return y < 0 || y == x ? x : l;
+}
+
+// Block r: how many leading tokens row r has on pages of its root's row (whole pages, that both rows have
+// filled).  The blocks of head 0 put their sequence into the families' order, by counting.
+__global__ void __launch_bounds__(LOOK_THREADS) prefix_look_kernel(const Params p) {
+  __shared__ int sh[LOOK_THREADS / 32][3];
+  __shared__ int mismatch;
+  wait_prior_grid();
+  allow_next_grid();
+  const int r = blockIdx.x, l = r / p.Hkv, h = r % p.Hkv, tid = threadIdx.x;
+  const int f = root_of(p, l);
+  if (tid == 0) {
+    mismatch = 0x7fffffff;
+    const int n = p.c.lens[r];
+    if (n < 0 || n > p.c.cap || p.lead[l] >= p.N) raise_status(p.status, KVP_ERR_DEVICE_CHECK);
+  }
+  if (h == 0) {
+    int before = 0, rank = 0, mine = 0;        // sequences of earlier families; of this one before l; of l's own
+    for (int x = tid; x < p.N; x += LOOK_THREADS) {
+      const int y = root_of(p, x);
+      before += y < f;
+      rank += y == f && x < l;
+      mine += y == f;
+    }
+    before = __reduce_add_sync(0xffffffffu, before);
+    rank = __reduce_add_sync(0xffffffffu, rank);
+    mine = __reduce_add_sync(0xffffffffu, mine);
+    if ((tid & 31) == 0) {
+      sh[tid >> 5][0] = before;
+      sh[tid >> 5][1] = rank;
+      sh[tid >> 5][2] = mine;
+    }
+    __syncthreads();
+    if (tid == 0) {
+      before = rank = mine = 0;
+      for (int w = 0; w < LOOK_THREADS / 32; ++w) {
+        before += sh[w][0];
+        rank += sh[w][1];
+        mine += sh[w][2];
+      }
+      p.root[l] = f;
+      p.order[before + rank] = l;
+      p.base[l] = before;
+      p.count[l] = mine;
+    }
+  }
+  __syncthreads();
+  if (f == l) {
+    if (tid == 0) p.shared[r] = 0;
+    return;
+  }
+  const int rf = f * p.Hkv + h;
+  const int most = min(prefix::row_len(p, r), prefix::row_len(p, rf)) >> p.c.shift;
+  const int32_t* a = p.c.table + (size_t)r * p.c.max_pages;
+  const int32_t* b = p.c.table + (size_t)rf * p.c.max_pages;
+  constexpr int U = 8;
+  for (int i0 = 0; i0 < most; i0 += U * LOOK_THREADS) {
+    int x[U], y[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int i = i0 + k * LOOK_THREADS + tid;
+      x[k] = i < most ? a[i] : 0;
+      y[k] = i < most ? b[i] : 0;
+    }
+    int at = 0x7fffffff;
+#pragma unroll
+    for (int k = U - 1; k >= 0; --k) {
+      const int i = i0 + k * LOOK_THREADS + tid;
+      if (i < most && (x[k] != y[k] || x[k] < 0 || x[k] >= p.c.n_pages)) at = i;
+    }
+    at = __reduce_min_sync(0xffffffffu, at);
+    if ((tid & 31) == 0 && at != 0x7fffffff) atomicMin(&mismatch, at);
+    __syncthreads();
+    if (mismatch != 0x7fffffff) break;
+    __syncthreads();
+  }
+  if (tid == 0) p.shared[r] = min(mismatch, most) << p.c.shift;
+}
+
+constexpr int PLAN_THREADS = 1024;
+
+// Saved tokens below which a prefix is not worth an item of its own.
+constexpr int MIN_SAVED = 2 * TILE;
+
+// The prefix of root row r: of the members' shared lengths the one that saves most when the members that
+// share at least so much take part.  A warp; more than 32 members offer 32 of theirs.
+__device__ void choose_prefix(const Params& p, int r) {
+  const int lane = threadIdx.x & 31, l = r / p.Hkv, h = r % p.Hkv;
+  const int base = p.base[l], count = p.count[l];
+  const auto row_at = [&](int j) { return p.order[base + j] * p.Hkv + h; };
+  const int pick = count <= 32 ? lane : (int)((long long)lane * count / 32);
+  const int mine = pick < count ? p.shared[row_at(pick)] : 0;      // (the root's own is 0)
+  int others = 0;
+  for (int j0 = 0; j0 < count; j0 += 32) {
+    const int s = j0 + lane < count ? p.shared[row_at(j0 + lane)] : 0;
+    for (int k = 0; k < 32; ++k) others += __shfl_sync(0xffffffffu, s, k) >= mine;
+  }
+  long long best = mine > 0 ? (long long)mine * others : 0;
+  int tokens = mine;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    const long long b = __shfl_xor_sync(0xffffffffu, best, off);
+    const int t = __shfl_xor_sync(0xffffffffu, tokens, off);
+    if (b > best || (b == best && t > tokens)) {
+      best = b;
+      tokens = t;
+    }
+  }
+  if (best < MIN_SAVED) tokens = 0;
+  int k = 0;
+  for (int j0 = 0; j0 < count; j0 += 32) {
+    const int j = j0 + lane, row = j < count ? row_at(j) : 0;
+    const bool in = tokens > 0 && j < count && (row == r || p.shared[row] >= tokens);
+    const uint32_t b = __ballot_sync(0xffffffffu, in);
+    if (j < count) {
+      const int at = k + __popc(b & ((1u << lane) - 1));
+      p.place[row] = in ? at : -1;
+      p.start[row] = in ? tokens : 0;
+      if (in) p.list[(size_t)h * p.N + base + at] = row / p.Hkv;
+    }
+    k += __popc(b);
+  }
+  if (lane == 0) p.pre_item[r] = k;            // for now: participants
+}
+
+// One block: the prefixes, the items in order with their places in the tile sequence, the CTAs' first items.
+__global__ void __launch_bounds__(PLAN_THREADS) prefix_plan_kernel(const Params p) {
+  __shared__ int scan_sh[33];
+  wait_prior_grid();
+  allow_next_grid();
+  const int tid = threadIdx.x, lane = tid & 31;
+  for (int r0 = tid - lane; r0 < p.c.R; r0 += PLAN_THREADS) {
+    const int r = r0 + lane, l = r / p.Hkv;
+    const bool root = r < p.c.R && p.root[l] == l;
+    const bool family = root && p.count[l] > 1;
+    if (r < p.c.R && !root) p.pre_item[r] = 0;
+    if (root && !family) {
+      p.place[r] = -1;
+      p.start[r] = 0;
+      p.pre_item[r] = 0;
+    }
+    for (uint32_t b = __ballot_sync(0xffffffffu, family); b; b &= b - 1) choose_prefix(p, r0 + __ffs(b) - 1);
+  }
+  __syncthreads();
+  int tiles = 0, items = 0;
+  for (long long i0 = 0; i0 < 2LL * p.c.R; i0 += PLAN_THREADS) {
+    const long long i = i0 + tid;
+    const bool own = i >= p.c.R, live = i < 2LL * p.c.R;
+    const int r = live ? (int)(own ? i - p.c.R : i) : 0;
+    int nq = 0, n = 0, tok0 = 0, tok1 = 0;
+    if (live && own) {
+      tok0 = p.start[r];
+      tok1 = prefix::row_len(p, r);
+      nq = p.G;
+      n = tok1 > tok0 ? 1 : 0;
+    } else if (live) {
+      const int k = p.pre_item[r];
+      if (k > 0) {
+        tok1 = p.start[r];
+        nq = k * p.G;
+        n = (nq + p.qt - 1) / p.qt;
+      }
+    }
+    const int t = prefix::tiles_of(tok1 - tok0);
+    int all_t, all_n;
+    const int at_t = tiles + block_exclusive_scan(n * t, scan_sh, &all_t);
+    const int at_n = items + block_exclusive_scan(n, scan_sh, &all_n);
+    for (int k = 0; k < n; ++k) {
+      Item it;
+      it.tile0 = at_t + k * t;
+      it.row = r;
+      it.tok0 = tok0;
+      it.tok1 = tok1;
+      it.q0 = k * p.qt;
+      it.nq = min(p.qt, nq - k * p.qt);
+      it.list = own ? -1 : (r % p.Hkv) * p.N + p.base[r / p.Hkv];
+      it.pad = 0;
+      p.items[at_n + k] = it;
+    }
+    if (live) (own ? p.own_item : p.pre_item)[r] = n > 0 ? at_n : -1;
+    tiles += all_t;
+    items += all_n;
+  }
+  __syncthreads();
+  const int active = min((tiles + 1) / 2, p.ctas);
+  if (tid == 0) *p.head = prefix::Head{tiles, active, items, 0};
+  for (int c = tid; c < active; c += PLAN_THREADS) {
+    const int x = paged::cta_begin(c, tiles, active);
+    int lo = 0, hi = items - 1;                // the last item that begins at or before x
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (p.items[mid].tile0 <= x) lo = mid;
+      else hi = mid - 1;
+    }
+    p.cta_item[c] = lo;
+  }
+}
+
+// ------------------------------------------------------------------ fp32 caches
+constexpr int F_THREADS = 256;
+constexpr int F_QT = 32;                 // queries of an item
+constexpr int F_KEYS = 64;               // keys at a time
+
+template <int D>
+struct Pf32 {
+  static constexpr int ROW = D + 4;                       // padded rows
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_K = OFF_Q + F_QT * ROW;
+  static constexpr int OFF_V = OFF_K + F_KEYS * ROW;
+  static constexpr int OFF_P = OFF_V + F_KEYS * ROW;      // [F_QT][F_KEYS + 4]
+  static constexpr int OFF_M = OFF_P + F_QT * (F_KEYS + 4);   // m, l, factor
+  static constexpr int SMEM = (OFF_M + 3 * F_QT) * 4;
+};
+
+// The items of an fp32 cache (the tensor cores have no fp32 products): 32 queries with 64 keys at a time,
+// logits and outputs by FFMA from shared memory.
+template <int D>
+__global__ void __launch_bounds__(F_THREADS) prefix_f32_kernel(const Params p) {
+  using C = Pf32<D>;
+  extern __shared__ __align__(16) float sm[];
+  float *qs = sm + C::OFF_Q, *ks = sm + C::OFF_K, *vs = sm + C::OFF_V, *ps = sm + C::OFF_P;
+  float *ms = sm + C::OFF_M, *ls = ms + F_QT, *fs = ls + F_QT;
+  const int tid = threadIdx.x, cta = blockIdx.x;
+  wait_prior_grid();
+  prefix::Walk walk(p, cta);
+  Piece a;
+  while (walk.step(a)) {
+    const bool own = a.it.list < 0;
+    __syncthreads();
+    for (int e = tid; e < F_QT * D / 4; e += F_THREADS) {
+      const int i = e / (D / 4), d = e % (D / 4) * 4;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < a.it.nq) {
+        int g;
+        const int r = prefix::query_row(p, a.it, i, g);
+        x = *reinterpret_cast<const float4*>((const float*)p.q + (r / p.Hkv) * p.q_stride +
+                                             (size_t)((r % p.Hkv) * p.G + g) * D + d);
+        if (p.zero) x = make_float4(0.f, 0.f, 0.f, 0.f);
+        else if (p.flip) x = make_float4(-x.x, -x.y, -x.z, -x.w);
+      }
+      *reinterpret_cast<float4*>(qs + i * C::ROW + d) = x;
+    }
+    if (tid < F_QT) {
+      ms[tid] = -INFINITY;
+      ls[tid] = 0.f;
+    }
+    // outputs: four queries by D / 32 values of a thread
+    constexpr int W = D / 32;
+    float o[4][W];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < W; ++j) o[i][j] = 0.f;
+    const int oq = tid / 32 * 4, od = tid % 32 * W;
+    const int tok_end = min(a.it.tok1, a.it.tok0 + a.u1 * TILE);
+    const int32_t* table = p.c.table + (size_t)a.it.row * p.c.max_pages;
+    for (int t0 = a.it.tok0 + a.u0 * TILE; t0 < tok_end; t0 += F_KEYS) {
+      __syncthreads();                         // the keys before have been used
+      for (int e = tid; e < 2 * F_KEYS * D / 4; e += F_THREADS) {
+        const int which = e / (F_KEYS * D / 4), x = e % (F_KEYS * D / 4), i = x / (D / 4), d = x % (D / 4) * 4;
+        const int t = t0 + i;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (t < tok_end) {
+          const int page = table[t >> p.c.shift];
+          if (page >= 0 && page < p.c.n_pages)
+            v = *reinterpret_cast<const float4*>((const float*)(which ? p.c.v : p.c.k) + page * p.c.page_stride +
+                                                 (t & (p.c.ps - 1)) * p.c.token_stride + d);
+          else raise_status(p.status, KVP_ERR_DEVICE_CHECK);
+        }
+        *reinterpret_cast<float4*>((which ? vs : ks) + i * C::ROW + d) = v;
+      }
+      __syncthreads();
+      // logits: two queries by four keys of a thread, 16 lanes side by side
+      const int lq = tid / 16 * 2, lk = tid % 16;
+      float s[2][4] = {};
+#pragma unroll 8
+      for (int d = 0; d < D; d += 4) {
+        const float4 q0 = *reinterpret_cast<const float4*>(qs + lq * C::ROW + d);
+        const float4 q1 = *reinterpret_cast<const float4*>(qs + (lq + 1) * C::ROW + d);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float4 k = *reinterpret_cast<const float4*>(ks + (lk + 16 * j) * C::ROW + d);
+          s[0][j] = fmaf(q0.x, k.x, fmaf(q0.y, k.y, fmaf(q0.z, k.z, fmaf(q0.w, k.w, s[0][j]))));
+          s[1][j] = fmaf(q1.x, k.x, fmaf(q1.y, k.y, fmaf(q1.z, k.z, fmaf(q1.w, k.w, s[1][j]))));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s[i][j] = t0 + lk + 16 * j < tok_end ? s[i][j] * p.c2 : -INFINITY;
+          top = fmaxf(top, s[i][j]);
+        }
+#pragma unroll
+        for (int off = 8; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        const float old = ms[lq + i], m = fmaxf(old, top);
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float w = s[i][j] == -INFINITY ? 0.f : fast_exp2(s[i][j] - m);
+          ps[(lq + i) * (F_KEYS + 4) + lk + 16 * j] = w;
+          sum += w;
+        }
+#pragma unroll
+        for (int off = 8; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        __syncwarp();
+        if (lk == 0) {
+          const float f = paged::weight(old, m);
+          fs[lq + i] = f;
+          ls[lq + i] = fmaf(ls[lq + i], f, sum);
+          ms[lq + i] = m;
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float f = fs[oq + i];
+#pragma unroll
+        for (int j = 0; j < W; ++j) o[i][j] *= f;
+      }
+#pragma unroll 4
+      for (int k = 0; k < F_KEYS; ++k) {
+        float w[4], v[W];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = ps[(oq + i) * (F_KEYS + 4) + k];
+#pragma unroll
+        for (int j = 0; j < W; ++j) v[j] = vs[k * C::ROW + od + j];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < W; ++j) o[i][j] = fmaf(w[i], v[j], o[i][j]);
+      }
+    }
+    for (int i = 0; i < 4; ++i) {
+      if (oq + i >= a.it.nq) break;
+      int g;
+      const int r = prefix::query_row(p, a.it, oq + i, g);
+      const size_t at = a.u0 == 0 ? prefix::first_slot(p, own, r, g, 0) : prefix::cont_slot(p, cta, oq + i);
+      float* to = (a.u0 == 0 ? p.first_o : p.cont_o) + at * D + od;
+#pragma unroll
+      for (int j = 0; j < W; ++j) to[j] = o[i][j];
+      if (tid % 32 == 0) (a.u0 == 0 ? p.first_ml : p.cont_ml)[at] = make_float2(ms[oq + i], ls[oq + i]);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ join
+constexpr int JOIN_THREADS = 256;
+
+// Results of the queries from their parts: `warps` warps a query share its parts, a lane has four outputs.
+template <typename T, int D>
+__global__ void __launch_bounds__(JOIN_THREADS) prefix_join_kernel(const Params p, int warps) {
+  constexpr int LANES = D / 4;                 // of a part
+  constexpr int HALF = 32 / LANES;             // parts a warp reads at once
+  __shared__ float red_m[JOIN_THREADS / 32], red_l[JOIN_THREADS / 32];
+  __shared__ float4 red_o[JOIN_THREADS / 32][LANES];
+  wait_prior_grid();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % warps;
+  const long long query = (long long)blockIdx.x * (JOIN_THREADS / 32 / warps) + warp / warps;
+  const bool live = query < (long long)p.c.R * p.G;
+  const int r = live ? (int)(query / p.G) : 0, g = (int)(query % p.G);
+  const int l = r / p.Hkv, h = r % p.Hkv;
+  const prefix::Head head = *p.head;
+  // the parts: [0, n0) of the prefix, then [0, n1) of the row's own tokens
+  int n[2] = {0, 0}, lo[2] = {0, 0}, parts[2] = {1, 1}, local[2] = {0, g};
+  if (live) {
+#pragma unroll
+    for (int kind = 0; kind < 2; ++kind) {
+      int item = -1;
+      if (kind == 1) {
+        item = p.own_item[r];
+      } else if (p.place[r] >= 0) {
+        const int x = p.place[r] * p.G + g;
+        item = p.pre_item[p.root[l] * p.Hkv + h] + x / p.qt;
+        local[0] = x % p.qt;
+      }
+      if (item < 0) continue;
+      const Item it = p.items[item];
+      lo[kind] = paged::cta_of(it.tile0, head.total, head.active);
+      const int hi = paged::cta_of(it.tile0 + prefix::tiles_of(it.tok1 - it.tok0) - 1, head.total, head.active);
+      parts[kind] = prefix::parts_of(p, it.nq);
+      n[kind] = (hi - lo[kind] + 1) * parts[kind];
+    }
+  }
+  const int all = n[0] + n[1];
+  // where part i lies
+  const auto at = [&](int i, bool& first) {
+    const int kind = i >= n[0], x = kind ? i - n[0] : i, c = x / parts[kind], part = x - c * parts[kind];
+    first = c == 0;
+    return first ? prefix::first_slot(p, kind, r, g, part)
+                 : prefix::cont_slot(p, lo[kind] + c, local[kind] + part * (p.qt / 2));
+  };
+  const auto ml_of = [&](int i) {
+    bool first;
+    const size_t x = at(i, first);
+    return (first ? p.first_ml : p.cont_ml)[x];
+  };
+  // this warp's maximum and sum, and the weighted outputs relative to its maximum
+  float M = -INFINITY, L = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int hl = lane / LANES, d = lane % LANES;
+  for (int i0 = sub * 32; i0 < all; i0 += warps * 32) {
+    const int i = i0 + lane;
+    const float2 ml = i < all ? ml_of(i) : make_float2(-INFINITY, 0.f);
+    float top = ml.x;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    top = fmaxf(top, M);
+    const float f = paged::weight(M, top), w = paged::weight(ml.x, top);
+    float s = ml.y * w;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    L = fmaf(L, f, s);
+    M = top;
+    o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+    const int m = min(32, all - i0);
+#pragma unroll 4
+    for (int k = 0; k < m; k += HALF) {
+      const int j = k + hl;
+      const float wj = __shfl_sync(0xffffffffu, w, j & 31), mj = __shfl_sync(0xffffffffu, ml.x, j & 31);
+      if (j < m && mj != -INFINITY) {
+        bool first;
+        const size_t x = at(i0 + j, first);
+        const float4 y = *reinterpret_cast<const float4*>((first ? p.first_o : p.cont_o) + x * D + 4 * d);
+        o.x = fmaf(y.x, wj, o.x);
+        o.y = fmaf(y.y, wj, o.y);
+        o.z = fmaf(y.z, wj, o.z);
+        o.w = fmaf(y.w, wj, o.w);
+      }
+    }
+  }
+#pragma unroll
+  for (int off = LANES; off < 32; off <<= 1) {
+    o.x += __shfl_xor_sync(0xffffffffu, o.x, off);
+    o.y += __shfl_xor_sync(0xffffffffu, o.y, off);
+    o.z += __shfl_xor_sync(0xffffffffu, o.z, off);
+    o.w += __shfl_xor_sync(0xffffffffu, o.w, off);
+  }
+  if (warps > 1) {
+    if (lane == 0) {
+      red_m[warp] = M;
+      red_l[warp] = L;
+    }
+    if (lane < LANES) red_o[warp][lane] = o;
+    __syncthreads();
+    if (sub != 0) return;
+    float top = M;
+    for (int k = 1; k < warps; ++k) top = fmaxf(top, red_m[warp + k]);
+    const float f = paged::weight(M, top);
+    L *= f;
+    o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+    for (int k = 1; k < warps; ++k) {
+      const float w = paged::weight(red_m[warp + k], top);
+      const float4 y = red_o[warp + k][d];
+      L = fmaf(red_l[warp + k], w, L);
+      o.x = fmaf(y.x, w, o.x);
+      o.y = fmaf(y.y, w, o.y);
+      o.z = fmaf(y.z, w, o.z);
+      o.w = fmaf(y.w, w, o.w);
+    }
+    M = top;
+  }
+  if (!live) return;
+  const size_t q = (size_t)l * p.Hq + (size_t)h * p.G + g;
+  if (lane < LANES) {
+    // (the sum, not its reciprocal: an fp32 result keeps the division's half step)
+    const float4 y = L == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x / L, o.y / L, o.z / L, o.w / L);
+    T* out = (T*)p.out + q * D + 4 * d;
+    if constexpr (sizeof(T) == 4) {
+      *reinterpret_cast<float4*>(out) = y;
+    } else {
+      paged::Params as{};
+      as.out = p.out;
+      paged::store_out4<T>(as, q * D + 4 * d, y);
+    }
+  }
+  if (lane == 0 && p.lse) p.lse[q] = L == 0.f ? -INFINITY : (M + log2f(L)) * KVP_LN2;
+}
+
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+int sm_count() {
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms;
+}
+
+size_t layout(const PagedView& c, int G, int h_kv, Params* p, void* ws) {
+  char* base = (char*)ws;
+  size_t at = 0;
+  const auto take = [&](size_t bytes) {
+    char* x = base ? base + at : nullptr;
+    at += align256(bytes);
+    return x;
+  };
+  const size_t R = c.R, N = c.R / h_kv, D = c.D;
+  const int sms = sm_count();
+  p->N = (int)N;
+  p->two = c.dtype != KVP_F32;
+  p->qt = c.dtype == KVP_F32 ? F_QT : 256;
+  p->ctas = c.dtype == KVP_F32 ? 2 * sms : sms;
+  const size_t items = 2 * R + R * G / p->qt + 1;
+  p->root = (int*)take(N * 4);
+  p->order = (int*)take(N * 4);
+  p->base = (int*)take(N * 4);
+  p->count = (int*)take(N * 4);
+  p->shared = (int*)take(R * 4);
+  p->start = (int*)take(R * 4);
+  p->place = (int*)take(R * 4);
+  p->list = (int*)take(R * 4);
+  p->pre_item = (int*)take(R * 4);
+  p->own_item = (int*)take(R * 4);
+  p->items = (Item*)take(items * sizeof(Item));
+  p->head = (prefix::Head*)take(sizeof(prefix::Head));
+  p->cta_item = (int*)take(p->ctas * 4);
+  p->first_ml = (float2*)take(4 * R * G * sizeof(float2));
+  p->first_o = (float*)take(4 * R * G * D * 4);
+  p->cont_ml = (float2*)take((size_t)p->ctas * p->qt * sizeof(float2));
+  p->cont_o = (float*)take((size_t)p->ctas * p->qt * D * 4);
+  return at;
+}
+
+template <int D>
+cudaError_t run_f32(const Params& p, cudaStream_t st) {
+  const auto kern = prefix_f32_kernel<D>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Pf32<D>::SMEM);
+  if (e != cudaSuccess) return e;
+  count_launches(1);
+  return launch_with_pdl(kern, dim3((unsigned)p.ctas), dim3(F_THREADS), Pf32<D>::SMEM, st, p);
+}
+
+template <typename T, int D>
+cudaError_t run(const Params& p, cudaStream_t st) {
+  count_launches(1);
+  cudaError_t e = launch_with_pdl(prefix_look_kernel, dim3((unsigned)p.c.R), dim3(LOOK_THREADS), 0, st, p);
+  if (e != cudaSuccess) return e;
+  count_launches(1);
+  e = launch_with_pdl(prefix_plan_kernel, dim3(1), dim3(PLAN_THREADS), 0, st, p);
+  if (e != cudaSuccess) return e;
+  if constexpr (sizeof(T) == 2) e = launch_paged_prefix_tc(p, st);
+  else e = run_f32<D>(p, st);
+  if (e != cudaSuccess) return e;
+  // A query can have a part or two from every CTA: few queries take a block each, many a warp.
+  const long long queries = (long long)p.c.R * p.G;
+  const int warps = queries <= 2048 ? JOIN_THREADS / 32 : 1, per = JOIN_THREADS / 32 / warps;
+  count_launches(1);
+  return launch_with_pdl(prefix_join_kernel<T, D>, dim3((unsigned)((queries + per - 1) / per)), dim3(JOIN_THREADS), 0,
+                         st, p, warps);
+}
+
+}  // namespace
+
+size_t paged_prefix_workspace(const PagedView& c, int h_q, int h_kv) {
+  Params p{};
+  return layout(c, h_q / h_kv, h_kv, &p, nullptr);
+}
+
+cudaError_t launch_paged_prefix_decode(const PagedView& c, const PagedPrefixArgs& a, void* ws, int* status,
+                                       cudaStream_t st) {
+  Params p{};
+  p.c = c;
+  p.q = a.q;
+  p.q_stride = a.q_stride;
+  p.lead = a.lead;
+  p.Hq = a.h_q;
+  p.Hkv = a.h_kv;
+  p.G = a.h_q / a.h_kv;
+  p.c2 = (float)(std::fabs(a.scale) * 1.4426950408889634);
+  p.flip = a.scale < 0;
+  p.zero = p.c2 == 0.f;
+  if (p.zero) p.c2 = 1.f;
+  p.out = a.out;
+  p.lse = a.lse;
+  p.status = status;
+  layout(c, p.G, a.h_kv, &p, ws);
+  if (c.dtype == KVP_BF16) return c.D == 128 ? run<__nv_bfloat16, 128>(p, st) : run<__nv_bfloat16, 64>(p, st);
+  if (c.dtype == KVP_F16) return c.D == 128 ? run<__half, 128>(p, st) : run<__half, 64>(p, st);
+  return c.D == 128 ? run<float, 128>(p, st) : run<float, 64>(p, st);
+}
+
+}  // namespace kvp

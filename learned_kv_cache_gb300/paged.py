@@ -245,15 +245,8 @@ def kvp_paged_free(cache, keep=None, stream=None):
                                                    _raw_stream(cache._index)))
 
 
-def kvp_paged_decode_attn(q, cache, sm_scale=None, out=None, out_dtype=None, lse=None, return_lse=False,
-                          add_scores=False, workspace=None, stream=None):
-    """One-token attention over the paged rows: q [L, H_q, D] (the layer axis may be strided), rows
-    r = l * h_kv + h -> out [L, H_q, D] float32 (or ``out_dtype`` = the cache's dtype); with
-    ``return_lse`` (out, lse float32 [L, H_q]).  ``add_scores`` adds every token's probability,
-    summed over its group, to ``cache.score``."""
-    if _cache(cache)._elsewhere(stream):
-        with cache._there(stream):
-            return kvp_paged_decode_attn(q, cache, sm_scale, out, out_dtype, lse, return_lse, add_scores, workspace)
+def _decode_queries(cache, q):
+    """q [L, H_q, D] of the cache's dtype: (L, H_q, h_kv, elements from layer to layer, 0 = dense)."""
     if not isinstance(q, torch.Tensor):
         raise TypeError("q must be a torch.Tensor")
     if q.device != cache.device:
@@ -272,7 +265,20 @@ def kvp_paged_decode_attn(q, cache, sm_scale=None, out=None, out_dtype=None, lse
             q_stride = q.stride(0)
             if q_stride == 0:
                 raise ValueError("q: the layer axis must not be broadcast")
-    h_kv = cache.n_rows // L
+    return L, Hq, cache.n_rows // L, q_stride
+
+
+def kvp_paged_decode_attn(q, cache, sm_scale=None, out=None, out_dtype=None, lse=None, return_lse=False,
+                          add_scores=False, workspace=None, stream=None):
+    """One-token attention over the paged rows: q [L, H_q, D] (the layer axis may be strided), rows
+    r = l * h_kv + h -> out [L, H_q, D] float32 (or ``out_dtype`` = the cache's dtype); with
+    ``return_lse`` (out, lse float32 [L, H_q]).  ``add_scores`` adds every token's probability,
+    summed over its group, to ``cache.score``."""
+    if _cache(cache)._elsewhere(stream):
+        with cache._there(stream):
+            return kvp_paged_decode_attn(q, cache, sm_scale, out, out_dtype, lse, return_lse, add_scores, workspace)
+    L, Hq, h_kv, q_stride = _decode_queries(cache, q)
+    D = cache.head_dim
     add_scores = int(bool(add_scores))
     if out is None:
         out = torch.empty((L, Hq, D), dtype=out_dtype or torch.float32, device=cache.device)
@@ -294,4 +300,36 @@ def kvp_paged_decode_attn(q, cache, sm_scale=None, out=None, out_dtype=None, lse
                                       _DTYPE[out.dtype], None if lse is None else lse.data_ptr(), add_scores, ws_ptr,
                                       ws_bytes, _raw_stream(cache._index))
     _check("kvp_paged_decode_attn", rc)
+    return (out, lse) if return_lse else out
+
+
+def kvp_paged_prefix_decode_attn(q, cache, lead, sm_scale=None, out=None, lse=None, return_lse=False, workspace=None,
+                                 stream=None):
+    """:func:`kvp_paged_decode_attn` for sequences that share a long prefix: q [N, H_q, D], rows
+    r = n * h_kv + h -> out [N, H_q, D] of the cache's dtype (with ``return_lse`` also lse float32
+    [N, H_q]).  lead int32 [N]: the sequence that each one was forked from (itself or negative: none).
+    The leading pages that its rows still hold in common with that sequence's are read once for all."""
+    if _cache(cache)._elsewhere(stream):
+        with cache._there(stream):
+            return kvp_paged_prefix_decode_attn(q, cache, lead, sm_scale, out, lse, return_lse, workspace)
+    N, Hq, h_kv, q_stride = _decode_queries(cache, q)
+    cache._need(lead, "lead", torch.int32, (N,))
+    if out is None:
+        out = torch.empty((N, Hq, cache.head_dim), dtype=cache.dtype, device=cache.device)
+    else:
+        cache._need(out, "out", cache.dtype, (N, Hq, cache.head_dim))
+    if lse is not None:
+        cache._need(lse, "lse", torch.float32, (N, Hq))
+    elif return_lse:
+        lse = torch.empty((N, Hq), dtype=torch.float32, device=cache.device)
+    if workspace is None:
+        workspace, ws_ptr, ws_bytes = cache._workspace("kvp_paged_prefix_decode_attn", Hq, h_kv)
+    else:
+        cache._need(workspace, "workspace", torch.uint8, None)
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel()
+    rc = load().kvp_paged_prefix_decode_attn(q.data_ptr(), q_stride, cache._ref, lead.data_ptr(), Hq, h_kv,
+                                             cache.head_dim ** -0.5 if sm_scale is None else float(sm_scale),
+                                             out.data_ptr(), None if lse is None else lse.data_ptr(), ws_ptr, ws_bytes,
+                                             _raw_stream(cache._index))
+    _check("kvp_paged_prefix_decode_attn", rc)
     return (out, lse) if return_lse else out
