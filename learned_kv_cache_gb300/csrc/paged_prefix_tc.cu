@@ -92,6 +92,31 @@ __device__ __forceinline__ void loaded(uint32_t (&r)[32]) {
                       "+r"(r[i + 6]), "+r"(r[i + 7]));
 }
 
+// Packed fp32 pairs (sm_100 family): two lanes of arithmetic per instruction.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t r, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // A pair of weights as 16-bit values, and what that leaves of them.
 __device__ __forceinline__ uint32_t pack_rest(__nv_bfloat16, float& a, float& b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
@@ -219,13 +244,18 @@ __global__ void __launch_bounds__(X_THREADS, 1)
       prefix::Walk walk(p, cta);
       Piece a;
       int li = 0;                        // tiles
-      int pend[2] = {-1, -1};            // the tile whose weights a group has still to bring
-      bool first[2] = {}, last[2] = {};  // of its piece
-      int uses_q[2] = {0, 0}, uses_p[2] = {0, 0};
+      // of either group: the tile whose weights it has still to bring, and whether that is the first or
+      // the last of its piece; the weights and queries it has brought
+      struct Group {
+        int pend = -1;
+        bool first = false, last = false;
+        int uses_q = 0, uses_p = 0;
+      } ga, gb;
       bool ok = true;
-      const auto outputs = [&](int g) {
-        const int unit = 2 * pend[g] + 1, s = unit % C::UNITS;
-        ok = ok && ptx::mbar_wait(bar_p + 8 * g, uses_p[g]++ & 1, flags, p.status) &&
+      const auto outputs = [&](auto which, Group& me, const Group& other) {
+        constexpr int g = decltype(which)::value;
+        const int unit = 2 * me.pend + 1, s = unit % C::UNITS;
+        ok = ok && ptx::mbar_wait(bar_p + 8 * g, me.uses_p++ & 1, flags, p.status) &&
              ptx::mbar_wait(bar_full + 8 * s, (unit / C::UNITS) & 1, flags, p.status);
         if (!ok) return;
         ptx::tc_fence_after();
@@ -234,15 +264,16 @@ __global__ void __launch_bounds__(X_THREADS, 1)
         for (int part = 1; part >= 0; --part)
 #pragma unroll
           for (int k = 0; k < TILE / 16; ++k)
-            mma_f16_ts(o, w + 64 * part + 8 * k, desc_mn_sw128(v + 2048 * k, C::HALF_BYTES), id_o,
-                       !(first[g] && part == 1 && k == 0));
-        if (last[g]) ptx::mma_commit(bar_o + 8 * g);
-        if (pend[g ^ 1] != pend[g]) ptx::mma_commit(bar_empty + 8 * s);
-        pend[g] = -1;
+            mma_f16_ts(o, w + 32 * (k >> 1) + 16 * part + 8 * (k & 1), desc_mn_sw128(v + 2048 * k, C::HALF_BYTES), id_o,
+                       !(me.first && part == 1 && k == 0));
+        if (me.last) ptx::mma_commit(bar_o + 8 * g);
+        if (other.pend != me.pend) ptx::mma_commit(bar_empty + 8 * s);
+        me.pend = -1;
       };
-      const auto scores = [&](int g, bool both) {
+      const auto scores = [&](auto which, Group& me, bool both) {
+        constexpr int g = decltype(which)::value;
         const int unit = 2 * li, s = unit % C::UNITS;
-        if (first[g]) ok = ok && ptx::mbar_wait(bar_q + 8 * g, uses_q[g]++ & 1, flags, p.status);
+        if (me.first) ok = ok && ptx::mbar_wait(bar_q + 8 * g, me.uses_q++ & 1, flags, p.status);
         ok = ok && ptx::mbar_wait(bar_full + 8 * s, (unit / C::UNITS) & 1, flags, p.status);
         if (!ok) return;
         ptx::tc_fence_after();
@@ -254,24 +285,34 @@ __global__ void __launch_bounds__(X_THREADS, 1)
         }
         ptx::mma_commit(bar_s + 8 * g);
         if (!both || g == 1) ptx::mma_commit(bar_empty + 8 * s);
-        pend[g] = li;
+        me.pend = li;
       };
+      const std::integral_constant<int, 0> A{};
+      const std::integral_constant<int, 1> B{};
       while (ok && walk.step(a)) {
         const bool both = a.it.nq > ROWS;
         const int step = both ? 1 : 2;
         for (int u = a.u0; ok && u < a.u1; ++u, ++li) {
-          for (int g = both ? 0 : li & 1; g <= (both ? 1 : li & 1); ++g) {
-            if (pend[g] >= 0) outputs(g);
-            first[g] = u - a.u0 < step;
-            last[g] = a.u1 - 1 - u < step;
-            if (ok) scores(g, both);
+          const bool first = u - a.u0 < step, last = a.u1 - 1 - u < step;
+          if (both || !(li & 1)) {
+            if (ga.pend >= 0) outputs(A, ga, gb);
+            ga.first = first;
+            ga.last = last;
+            if (ok) scores(A, ga, both);
+          }
+          if (ok && (both || (li & 1))) {
+            if (gb.pend >= 0) outputs(B, gb, ga);
+            gb.first = first;
+            gb.last = last;
+            if (ok) scores(B, gb, both);
           }
         }
       }
-      for (int i = 0; i < 2; ++i) {      // the older one first
-        const int g = pend[0] >= 0 && (pend[1] < 0 || pend[0] <= pend[1]) ? 0 : 1;
-        if (ok && pend[g] >= 0) outputs(g);
-      }
+      // the older one first
+      const bool second = ga.pend >= 0 && (gb.pend < 0 || ga.pend <= gb.pend);
+      if (!second && ok && gb.pend >= 0) outputs(B, gb, ga);
+      if (ok && ga.pend >= 0) outputs(A, ga, gb);
+      if (second && ok && gb.pend >= 0) outputs(B, gb, ga);
     }
     __syncwarp();
   } else if (warp >= 4) {
@@ -335,25 +376,23 @@ __global__ void __launch_bounds__(X_THREADS, 1)
         const int valid = a.it.tok1 - a.it.tok0 - u * TILE;
         if (busy) {
           ptx::tc_fence_after();
-          uint32_t raw[4][32];
+          // the largest score, then the weights chunk by chunk: 32 scores make way for 16 + 16 columns of weights
+          float top = -INFINITY;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) ptx::tmem_ld32(ts + 32 * k, raw[k]);
-          ptx::tmem_ld_wait();
-          float s[TILE];
+          for (int k = 0; k < TILE; k += 32) {
+            uint32_t s[32];
+            ptx::tmem_ld32(ts + k, s);
+            ptx::tmem_ld_wait();
+            loaded(s);
+            if (valid < TILE) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            loaded(raw[k]);
+              for (int i = 0; i < 32; ++i)
+                if (k + i >= valid) s[i] = 0xff800000u;
+            }
 #pragma unroll
-            for (int i = 0; i < 32; ++i) s[32 * k + i] = __uint_as_float(raw[k][i]);
+            for (int i = 0; i < 32; i += 2) top = max3(top, __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
           }
-          if (valid < TILE) {
-#pragma unroll
-            for (int k = 0; k < TILE; ++k) s[k] = k < valid ? s[k] : -INFINITY;
-          }
-          float top[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-          for (int k = 4; k < TILE; ++k) top[k & 3] = fmaxf(top[k & 3], s[k]);
-          const float x = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.c2;
+          const float x = top * p.c2;
           if (u == u0) {
             m = x;
           } else if (__any_sync(0xffffffffu, x > m + LAG)) {
@@ -361,7 +400,7 @@ __global__ void __launch_bounds__(X_THREADS, 1)
             m = up;
             l *= f;
             // the tile before has been added up: the scores' barrier follows its products
-#pragma unroll
+#pragma unroll 1
             for (int k = 0; k < D; k += 32) {
               uint32_t o[32], w[2][16];
               ptx::tmem_ld32(to + k, o);
@@ -373,23 +412,37 @@ __global__ void __launch_bounds__(X_THREADS, 1)
               tmem_st16(to + k + 16, w[1]);
             }
           }
-          const float off = m == -INFINITY ? 0.f : m;      // nothing but -inf so far: weights of 0
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          const float off = m == -INFINITY ? 0.f : -m;     // nothing but -inf so far: weights of 0
+          const uint64_t c2 = pack2(p.c2, p.c2), off2 = pack2(off, off);
+          uint64_t sum[2] = {0, 0};
 #pragma unroll
           for (int k = 0; k < TILE; k += 32) {
-            uint32_t hi[16], lo[16];
+            uint32_t s[32], hi[16], lo[16];
+            ptx::tmem_ld32(ts + k, s);
+            ptx::tmem_ld_wait();
+            loaded(s);
+            if (valid < TILE) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (k + i >= valid) s[i] = 0xff800000u;
+            }
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              float w0 = fast_exp2(fmaf(s[k + 2 * i], p.c2, -off)), w1 = fast_exp2(fmaf(s[k + 2 * i + 1], p.c2, -off));
-              sum[(2 * i) & 3] += w0;
-              sum[(2 * i + 1) & 3] += w1;
+              float w0, w1;
+              unpack2(ffma2(pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c2, off2), w0, w1);
+              w0 = fast_exp2(w0);
+              w1 = fast_exp2(w1);
+              sum[i & 1] = fadd2(sum[i & 1], pack2(w0, w1));
               hi[i] = pack_rest(T(), w0, w1);
               lo[i] = pack(T(), w0, w1);
             }
-            tmem_st16(ts + k / 2, hi);
-            tmem_st16(ts + 64 + k / 2, lo);
+            tmem_st16(ts + k, hi);
+            tmem_st16(ts + k + 16, lo);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          float a0, a1, b0, b1;
+          unpack2(sum[0], a0, a1);
+          unpack2(sum[1], b0, b1);
+          l += (a0 + a1) + (b0 + b1);
           tmem_st_wait();
           ptx::tc_fence_before();
         }
