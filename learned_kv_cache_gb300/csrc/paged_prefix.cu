@@ -108,21 +108,38 @@ __global__ void __launch_bounds__(LOOK_THREADS) prefix_look_kernel(const Params 
 }
 
 constexpr int PLAN_THREADS = 1024;
+constexpr int CHOOSE_THREADS = 128;
 
 // Saved tokens below which a prefix is not worth an item of its own.
 constexpr int MIN_SAVED = 2 * TILE;
 
-// The prefix of root row r: of the members' shared lengths the one that saves most when the members that
-// share at least so much take part.  A warp; more than 32 members offer 32 of theirs.
-__device__ void choose_prefix(const Params& p, int r) {
-  const int lane = threadIdx.x & 31, l = r / p.Hkv, h = r % p.Hkv;
-  const int base = p.base[l], count = p.count[l];
+// A warp for every row; those of a family's lead choose its prefix: of the members' shared lengths the one
+// that saves most when the members that share at least so much take part.  More than 32 members offer 32
+// of theirs.  (In the plan's one block, 8 heads' rows were one warp's: 25 us of 4 families' 35.)
+__global__ void __launch_bounds__(CHOOSE_THREADS) prefix_choose_kernel(const Params p) {
+  wait_prior_grid();
+  allow_next_grid();
+  const int r = blockIdx.x * (CHOOSE_THREADS / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (r >= p.c.R) return;
+  const int l = r / p.Hkv, h = r % p.Hkv;
+  const int root = p.root[l], base = p.base[l], count = p.count[l];
+  if (root != l || count < 2) {
+    if (lane == 0) {
+      p.pre_item[r] = 0;
+      if (root == l) {
+        p.place[r] = -1;
+        p.start[r] = 0;
+      }
+    }
+    return;
+  }
   const auto row_at = [&](int j) { return p.order[base + j] * p.Hkv + h; };
   const int pick = count <= 32 ? lane : (int)((long long)lane * count / 32);
   const int mine = pick < count ? p.shared[row_at(pick)] : 0;      // (the root's own is 0)
   int others = 0;
   for (int j0 = 0; j0 < count; j0 += 32) {
     const int s = j0 + lane < count ? p.shared[row_at(j0 + lane)] : 0;
+#pragma unroll
     for (int k = 0; k < 32; ++k) others += __shfl_sync(0xffffffffu, s, k) >= mine;
   }
   long long best = mine > 0 ? (long long)mine * others : 0;
@@ -153,76 +170,87 @@ __device__ void choose_prefix(const Params& p, int r) {
   if (lane == 0) p.pre_item[r] = k;            // for now: participants
 }
 
-// One block: the prefixes, the items in order with their places in the tile sequence, the CTAs' first items.
+// One block: the items in order with their places in the tile sequence, the CTAs' first items.  A warp
+// has a run of the 2 R places (prefixes, then own tokens): it adds its tiles and items up, and writes them
+// once the block has added up the warps'.
 __global__ void __launch_bounds__(PLAN_THREADS) prefix_plan_kernel(const Params p) {
-  __shared__ int scan_sh[33];
+  constexpr int WARPS = PLAN_THREADS / 32, AHEAD = 4;
+  __shared__ int sums[2][WARPS];
   wait_prior_grid();
   allow_next_grid();
-  const int tid = threadIdx.x, lane = tid & 31;
-  for (int r0 = tid - lane; r0 < p.c.R; r0 += PLAN_THREADS) {
-    const int r = r0 + lane, l = r / p.Hkv;
-    const bool root = r < p.c.R && p.root[l] == l;
-    const bool family = root && p.count[l] > 1;
-    if (r < p.c.R && !root) p.pre_item[r] = 0;
-    if (root && !family) {
-      p.place[r] = -1;
-      p.start[r] = 0;
-      p.pre_item[r] = 0;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, R = p.c.R;
+  const int run = (2 * R + 32 * WARPS - 1) / (32 * WARPS) * 32, begin = min(warp * run, 2 * R), end = min(begin + run, 2 * R);
+  struct Place {
+    int tok0, tok1, nq, n;               // tokens, queries, items
+  };
+  const auto place = [&](int i) {
+    Place x{0, 0, 0, 0};
+    if (i >= end) return x;
+    if (i >= R) {
+      x.tok0 = p.start[i - R];
+      x.tok1 = prefix::row_len(p, i - R);
+      x.nq = p.G;
+      x.n = x.tok1 > x.tok0 ? 1 : 0;
+    } else {
+      const int k = p.pre_item[i], s = p.start[i];
+      x.tok1 = k > 0 ? s : 0;
+      x.nq = k * p.G;
+      x.n = (x.nq + p.qt - 1) / p.qt;
     }
-    for (uint32_t b = __ballot_sync(0xffffffffu, family); b; b &= b - 1) choose_prefix(p, r0 + __ffs(b) - 1);
+    return x;
+  };
+  int tiles = 0, items = 0;
+  for (int i0 = begin; i0 < end; i0 += 32 * AHEAD) {
+    Place x[AHEAD];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) x[k] = place(i0 + 32 * k + lane);
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      tiles += x[k].n * prefix::tiles_of(x[k].tok1 - x[k].tok0);
+      items += x[k].n;
+    }
+  }
+  tiles = __reduce_add_sync(0xffffffffu, tiles);
+  items = __reduce_add_sync(0xffffffffu, items);
+  if (lane == 0) {
+    sums[0][warp] = tiles;
+    sums[1][warp] = items;
   }
   __syncthreads();
-  int tiles = 0, items = 0;
-  for (long long i0 = 0; i0 < 2LL * p.c.R; i0 += PLAN_THREADS) {
-    const long long i = i0 + tid;
-    const bool own = i >= p.c.R, live = i < 2LL * p.c.R;
-    const int r = live ? (int)(own ? i - p.c.R : i) : 0;
-    int nq = 0, n = 0, tok0 = 0, tok1 = 0;
-    if (live && own) {
-      tok0 = p.start[r];
-      tok1 = prefix::row_len(p, r);
-      nq = p.G;
-      n = tok1 > tok0 ? 1 : 0;
-    } else if (live) {
-      const int k = p.pre_item[r];
-      if (k > 0) {
-        tok1 = p.start[r];
-        nq = k * p.G;
-        n = (nq + p.qt - 1) / p.qt;
-      }
-    }
-    const int t = prefix::tiles_of(tok1 - tok0);
-    int all_t, all_n;
-    const int at_t = tiles + block_exclusive_scan(n * t, scan_sh, &all_t);
-    const int at_n = items + block_exclusive_scan(n, scan_sh, &all_n);
-    for (int k = 0; k < n; ++k) {
+  // (WARPS = 32: a lane for every warp's sum)
+  const int t = sums[0][lane], n = sums[1][lane];
+  int at_t = __reduce_add_sync(0xffffffffu, lane < warp ? t : 0), at_n = __reduce_add_sync(0xffffffffu, lane < warp ? n : 0);
+  tiles = __reduce_add_sync(0xffffffffu, t);
+  items = __reduce_add_sync(0xffffffffu, n);
+  const int active = min((tiles + 1) / 2, p.ctas);
+  if (threadIdx.x == 0) *p.head = prefix::Head{tiles, active, items, 0};
+  for (int i0 = begin; i0 < end; i0 += 32) {
+    const int i = i0 + lane;
+    const Place x = place(i);
+    const int each = prefix::tiles_of(x.tok1 - x.tok0);
+    const int t_in = warp_inclusive_scan(x.n * each), n_in = warp_inclusive_scan(x.n);
+    const int t0 = at_t + t_in - x.n * each, n0 = at_n + n_in - x.n;
+    const bool own = i >= R;
+    const int r = own ? i - R : i;
+    for (int k = 0; k < x.n; ++k) {
       Item it;
-      it.tile0 = at_t + k * t;
+      it.tile0 = t0 + k * each;
       it.row = r;
-      it.tok0 = tok0;
-      it.tok1 = tok1;
+      it.tok0 = x.tok0;
+      it.tok1 = x.tok1;
       it.q0 = k * p.qt;
-      it.nq = min(p.qt, nq - k * p.qt);
+      it.nq = min(p.qt, x.nq - k * p.qt);
       it.list = own ? -1 : (r % p.Hkv) * p.N + p.base[r / p.Hkv];
       it.pad = 0;
-      p.items[at_n + k] = it;
+      p.items[n0 + k] = it;
+      // the CTAs whose range begins in it
+      const int hi = paged::cta_of(it.tile0 + each - 1, tiles, active);
+      for (int c = it.tile0 == 0 ? 0 : paged::cta_of(it.tile0 - 1, tiles, active) + 1; c <= hi; ++c) p.cta_item[c] = n0 + k;
     }
-    if (live) (own ? p.own_item : p.pre_item)[r] = n > 0 ? at_n : -1;
-    tiles += all_t;
-    items += all_n;
-  }
-  __syncthreads();
-  const int active = min((tiles + 1) / 2, p.ctas);
-  if (tid == 0) *p.head = prefix::Head{tiles, active, items, 0};
-  for (int c = tid; c < active; c += PLAN_THREADS) {
-    const int x = paged::cta_begin(c, tiles, active);
-    int lo = 0, hi = items - 1;                // the last item that begins at or before x
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (p.items[mid].tile0 <= x) lo = mid;
-      else hi = mid - 1;
-    }
-    p.cta_item[c] = lo;
+    __syncwarp();
+    if (i < end) (own ? p.own_item : p.pre_item)[r] = x.n > 0 ? n0 : -1;
+    at_t += __shfl_sync(0xffffffffu, t_in, 31);
+    at_n += __shfl_sync(0xffffffffu, n_in, 31);
   }
 }
 
@@ -366,7 +394,7 @@ __global__ void __launch_bounds__(F_THREADS) prefix_f32_kernel(const Params p) {
       if (oq + i >= a.it.nq) break;
       int g;
       const int r = prefix::query_row(p, a.it, oq + i, g);
-      const size_t at = a.u0 == 0 ? prefix::first_slot(p, own, r, g, 0) : prefix::cont_slot(p, cta, oq + i);
+      const size_t at = a.u0 == 0 ? prefix::first_slot(p, own, r, g) : prefix::cont_slot(p, cta, oq + i);
       float* to = (a.u0 == 0 ? p.first_o : p.cont_o) + at * D + od;
 #pragma unroll
       for (int j = 0; j < W; ++j) to[j] = o[i][j];
@@ -378,75 +406,67 @@ __global__ void __launch_bounds__(F_THREADS) prefix_f32_kernel(const Params p) {
 // ------------------------------------------------------------------ join
 constexpr int JOIN_THREADS = 256;
 
-// Results of the queries from their parts: `warps` warps a query share its parts, a lane has four outputs.
+// Results of the queries from their parts: `warps` warps of a block have a query, a lane four of its outputs.
 template <typename T, int D>
 __global__ void __launch_bounds__(JOIN_THREADS) prefix_join_kernel(const Params p, int warps) {
   constexpr int LANES = D / 4;                 // of a part
-  constexpr int HALF = 32 / LANES;             // parts a warp reads at once
-  __shared__ float red_m[JOIN_THREADS / 32], red_l[JOIN_THREADS / 32];
-  __shared__ float4 red_o[JOIN_THREADS / 32][LANES];
+  constexpr int AT_ONCE = 32 / LANES;          // parts a warp reads at once
+  __shared__ float4 sum_sh[JOIN_THREADS / 32][LANES];
   wait_prior_grid();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % warps;
   const long long query = (long long)blockIdx.x * (JOIN_THREADS / 32 / warps) + warp / warps;
   const bool live = query < (long long)p.c.R * p.G;
-  const int r = live ? (int)(query / p.G) : 0, g = (int)(query % p.G);
+  const int r = live ? (int)(query / p.G) : 0, g = live ? (int)(query % p.G) : 0;
   const int l = r / p.Hkv, h = r % p.Hkv;
   const prefix::Head head = *p.head;
-  // the parts: [0, n0) of the prefix, then [0, n1) of the row's own tokens
-  int n[2] = {0, 0}, lo[2] = {0, 0}, parts[2] = {1, 1}, local[2] = {0, g};
+  // the parts: [0, n0) of the prefix, then [0, n1) of the row's own tokens, from CTA lo on
+  int n0 = 0, n1 = 0, lo0 = 0, lo1 = 0, local = 0;
   if (live) {
-#pragma unroll
-    for (int kind = 0; kind < 2; ++kind) {
-      int item = -1;
-      if (kind == 1) {
-        item = p.own_item[r];
-      } else if (p.place[r] >= 0) {
-        const int x = p.place[r] * p.G + g;
-        item = p.pre_item[p.root[l] * p.Hkv + h] + x / p.qt;
-        local[0] = x % p.qt;
-      }
-      if (item < 0) continue;
-      const Item it = p.items[item];
-      lo[kind] = paged::cta_of(it.tile0, head.total, head.active);
-      const int hi = paged::cta_of(it.tile0 + prefix::tiles_of(it.tok1 - it.tok0) - 1, head.total, head.active);
-      parts[kind] = prefix::parts_of(p, it.nq);
-      n[kind] = (hi - lo[kind] + 1) * parts[kind];
+    const int place = p.place[r], root = p.root[l], own = p.own_item[r];
+    int pre = -1;
+    if (place >= 0) {
+      const int x = place * p.G + g;
+      pre = p.pre_item[root * p.Hkv + h] + x / p.qt;
+      local = x % p.qt;
     }
+    const auto span = [&](int item, int& lo) {
+      const Item it = p.items[item];
+      lo = paged::cta_of(it.tile0, head.total, head.active);
+      return paged::cta_of(it.tile0 + prefix::tiles_of(it.tok1 - it.tok0) - 1, head.total, head.active) - lo + 1;
+    };
+    if (pre >= 0) n0 = span(pre, lo0);
+    if (own >= 0) n1 = span(own, lo1);
   }
-  const int all = n[0] + n[1];
-  // where part i lies
+  const int all = n0 + n1;
+  // where part i lies: in the pieces that begin an item, or in those that go on
   const auto at = [&](int i, bool& first) {
-    const int kind = i >= n[0], x = kind ? i - n[0] : i, c = x / parts[kind], part = x - c * parts[kind];
+    const bool own = i >= n0;
+    const int c = own ? i - n0 : i;
     first = c == 0;
-    return first ? prefix::first_slot(p, kind, r, g, part)
-                 : prefix::cont_slot(p, lo[kind] + c, local[kind] + part * (p.qt / 2));
+    return first ? prefix::first_slot(p, own, r, g) : prefix::cont_slot(p, (own ? lo1 : lo0) + c, own ? g : local);
   };
   const auto ml_of = [&](int i) {
+    if (i >= all) return make_float2(-INFINITY, 0.f);
     bool first;
     const size_t x = at(i, first);
     return (first ? p.first_ml : p.cont_ml)[x];
   };
-  // this warp's maximum and sum, and the weighted outputs relative to its maximum
-  float M = -INFINITY, L = 0.f;
+  // every warp finds the maximum and the sum of all parts, and adds up its share of the outputs
+  float2 ml = ml_of(lane);
+  float M = ml.x;
+  for (int i = lane + 32; i < all; i += 32) M = fmaxf(M, ml_of(i).x);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  float L = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   const int hl = lane / LANES, d = lane % LANES;
-  for (int i0 = sub * 32; i0 < all; i0 += warps * 32) {
-    const int i = i0 + lane;
-    const float2 ml = i < all ? ml_of(i) : make_float2(-INFINITY, 0.f);
-    float top = ml.x;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    top = fmaxf(top, M);
-    const float f = paged::weight(M, top), w = paged::weight(ml.x, top);
-    float s = ml.y * w;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    L = fmaf(L, f, s);
-    M = top;
-    o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+  for (int i0 = 0; i0 < all; i0 += 32) {
+    if (i0 > 0) ml = ml_of(i0 + lane);
+    const float w = paged::weight(ml.x, M);
+    L = fmaf(ml.y, w, L);
     const int m = min(32, all - i0);
 #pragma unroll 4
-    for (int k = 0; k < m; k += HALF) {
+    for (int k = sub * AT_ONCE; k < m; k += warps * AT_ONCE) {
       const int j = k + hl;
       const float wj = __shfl_sync(0xffffffffu, w, j & 31), mj = __shfl_sync(0xffffffffu, ml.x, j & 31);
       if (j < m && mj != -INFINITY) {
@@ -461,6 +481,8 @@ __global__ void __launch_bounds__(JOIN_THREADS) prefix_join_kernel(const Params 
     }
   }
 #pragma unroll
+  for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+#pragma unroll
   for (int off = LANES; off < 32; off <<= 1) {
     o.x += __shfl_xor_sync(0xffffffffu, o.x, off);
     o.y += __shfl_xor_sync(0xffffffffu, o.y, off);
@@ -468,28 +490,13 @@ __global__ void __launch_bounds__(JOIN_THREADS) prefix_join_kernel(const Params 
     o.w += __shfl_xor_sync(0xffffffffu, o.w, off);
   }
   if (warps > 1) {
-    if (lane == 0) {
-      red_m[warp] = M;
-      red_l[warp] = L;
-    }
-    if (lane < LANES) red_o[warp][lane] = o;
+    if (lane < LANES) sum_sh[warp][lane] = o;
     __syncthreads();
     if (sub != 0) return;
-    float top = M;
-    for (int k = 1; k < warps; ++k) top = fmaxf(top, red_m[warp + k]);
-    const float f = paged::weight(M, top);
-    L *= f;
-    o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
     for (int k = 1; k < warps; ++k) {
-      const float w = paged::weight(red_m[warp + k], top);
-      const float4 y = red_o[warp + k][d];
-      L = fmaf(red_l[warp + k], w, L);
-      o.x = fmaf(y.x, w, o.x);
-      o.y = fmaf(y.y, w, o.y);
-      o.z = fmaf(y.z, w, o.z);
-      o.w = fmaf(y.w, w, o.w);
+      const float4 y = sum_sh[warp + k][d];
+      o = make_float4(o.x + y.x, o.y + y.y, o.z + y.z, o.w + y.w);
     }
-    M = top;
   }
   if (!live) return;
   const size_t q = (size_t)l * p.Hq + (size_t)h * p.G + g;
@@ -528,8 +535,7 @@ size_t layout(const PagedView& c, int G, int h_kv, Params* p, void* ws) {
   const size_t R = c.R, N = c.R / h_kv, D = c.D;
   const int sms = sm_count();
   p->N = (int)N;
-  p->two = c.dtype != KVP_F32;
-  p->qt = c.dtype == KVP_F32 ? F_QT : 256;
+  p->qt = c.dtype == KVP_F32 ? F_QT : 256 / G * G;
   p->ctas = c.dtype == KVP_F32 ? 2 * sms : sms;
   const size_t items = 2 * R + R * G / p->qt + 1;
   p->root = (int*)take(N * 4);
@@ -545,8 +551,8 @@ size_t layout(const PagedView& c, int G, int h_kv, Params* p, void* ws) {
   p->items = (Item*)take(items * sizeof(Item));
   p->head = (prefix::Head*)take(sizeof(prefix::Head));
   p->cta_item = (int*)take(p->ctas * 4);
-  p->first_ml = (float2*)take(4 * R * G * sizeof(float2));
-  p->first_o = (float*)take(4 * R * G * D * 4);
+  p->first_ml = (float2*)take(2 * R * G * sizeof(float2));
+  p->first_o = (float*)take(2 * R * G * D * 4);
   p->cont_ml = (float2*)take((size_t)p->ctas * p->qt * sizeof(float2));
   p->cont_o = (float*)take((size_t)p->ctas * p->qt * D * 4);
   return at;
@@ -565,6 +571,10 @@ template <typename T, int D>
 cudaError_t run(const Params& p, cudaStream_t st) {
   count_launches(1);
   cudaError_t e = launch_with_pdl(prefix_look_kernel, dim3((unsigned)p.c.R), dim3(LOOK_THREADS), 0, st, p);
+  if (e != cudaSuccess) return e;
+  count_launches(1);
+  constexpr int PER = CHOOSE_THREADS / 32;
+  e = launch_with_pdl(prefix_choose_kernel, dim3((unsigned)((p.c.R + PER - 1) / PER)), dim3(CHOOSE_THREADS), 0, st, p);
   if (e != cudaSuccess) return e;
   count_launches(1);
   e = launch_with_pdl(prefix_plan_kernel, dim3(1), dim3(PLAN_THREADS), 0, st, p);

@@ -42,8 +42,7 @@ struct Params {
   int flip;              // scale < 0: the queries' signs change
   int zero;              // scale = 0: c2 is 1, and the queries count as 0 (-inf stays the logit of no token)
   int ctas;              // launched
-  int qt;                // queries of an item
-  int two;               // an item of up to qt / 2 queries leaves two parts per query (a half of the tiles each)
+  int qt;                // queries of an item: whole sequences'
   // the plan
   int* root;             // [N] sequence a sequence follows (itself)
   int* order;            // [N] sequences by family
@@ -59,7 +58,7 @@ struct Params {
   Head* head;
   int* cta_item;         // [ctas] item that a CTA's range begins in
   // partial results
-  float2* first_ml;      // [2 kinds][R * G][parts]
+  float2* first_ml;      // [2 kinds][R * G]
   float* first_o;        // [...][D]
   float2* cont_ml;       // [ctas][qt]
   float* cont_o;
@@ -73,7 +72,6 @@ __device__ __forceinline__ int row_len(const Params& p, int r) {
   const int n = p.c.lens[r];
   return n < 0 ? 0 : (n > p.c.cap ? p.c.cap : n);
 }
-__device__ __forceinline__ int parts_of(const Params& p, int nq) { return p.two && 2 * nq <= p.qt ? 2 : 1; }
 
 // One piece: tiles [u0, u1) of an item.
 struct Piece {
@@ -121,9 +119,10 @@ __device__ __forceinline__ int query_row(const Params& p, const Item& it, int i,
   return p.list[it.list + k] * p.Hkv + it.row % p.Hkv;
 }
 
-// Where a piece's partial result of a query goes: part `part` of `parts`, at [local].
-__device__ __forceinline__ size_t first_slot(const Params& p, bool own, int row, int g, int part) {
-  return (((size_t)own * p.c.R + row) * p.G + g) * 2 + part;
+// Where a piece's partial result of a query goes: of a piece that begins an item, and of one that goes on
+// (the item's query `local`).
+__device__ __forceinline__ size_t first_slot(const Params& p, bool own, int row, int g) {
+  return ((size_t)own * p.c.R + row) * p.G + g;
 }
 __device__ __forceinline__ size_t cont_slot(const Params& p, int cta, int local) { return (size_t)cta * p.qt + local; }
 

@@ -5,13 +5,18 @@
 // 4 D flop per query and key against 4 D bytes per key: with few queries bound by HBM, with 256 about as
 // long on the tensor cores (QK^T and two parts of P V: 3072 cycles a tile of D 128) as in HBM (2790).
 //
-//  * One CTA per SM.  Warp 0 copies: per tile K and V as a unit each of a ring, one TMA box per page (or 128
-//    tokens of one) and 64-column half.  Warp 1 issues the products.  Two groups of four warps have a
-//    128-row block of queries each, a thread a row: scores come from TMEM, the weights go back there as
-//    the first operand of P V, and the outputs stay in TMEM until the piece ends.
+//  * One CTA per SM.  Warp 0 copies keys and values: K and V of a tile are a unit each of a ring, one TMA
+//    box per page (or 128 tokens of one) and 64-column half, in the order in which the products use them.
+//    Warp 1 issues the products, as a whole warp up to the elected thread's instructions: with one thread
+//    walking alone, its descriptors were not known to be uniform and an instruction took 90 cycles to
+//    issue, as long as it ran.  Warp 2 clears the slots behind an item's last token, warp 3 copies the
+//    next piece's queries.  Sixteen warps have the softmax.
+//  * Queries 0..127 and 128..255 are two groups of eight warps.  A thread has a query (a TMEM lane) and 64
+//    of a tile's keys: scores come from TMEM once, and the weights go back in their place as the first
+//    operand of P V.  Outputs stay in TMEM until the piece ends.
 //  * More than 128 queries: each group has its own, and both take every tile.  Up to 128: both have the
-//    same, and take the tiles in turn (a part each for the join).  Either way one group's softmax runs
-//    beside the other's products.
+//    same, take the tiles in turn, and put their results together when the piece ends.  Either way one
+//    group's softmax runs beside the other's products.
 //  * V lies [key][dim] in memory, so it is the second operand in its MN-major form; nothing is transposed.
 //  * P enters the product as the sum of two 16-bit parts: 16 (bf16) or 22 (f16) bits of every weight, so
 //    that an output is off by its own rounding only; with one part bf16 outputs would be 1.4 times as far
@@ -34,7 +39,7 @@ using prefix::Params;
 using prefix::Piece;
 using prefix::TILE;
 
-constexpr int X_THREADS = 384;
+constexpr int X_THREADS = 640;
 constexpr int ROWS = 128;                // queries of a group
 constexpr float LAG = 8.f;               // log2 of how far the maximum may lag
 
@@ -42,12 +47,14 @@ template <int D>
 struct Px {
   static constexpr int HALVES = D / 64;
   static constexpr int HALF_BYTES = TILE * 128;            // 64 columns of 128 tokens
-  static constexpr int UNIT = HALVES * HALF_BYTES;         // K or V of a tile, or the queries of a group
+  static constexpr int UNIT = HALVES * HALF_BYTES;         // K or V of a tile
   static constexpr int UNITS = D == 128 ? 5 : 10;
-  static constexpr int OFF_RING = 2 * UNIT;
-  static constexpr int OFF_BAR = OFF_RING + UNITS * UNIT;
-  static constexpr int OFF_FLAG = OFF_BAR + 8 * (2 * UNITS + 8);
-  static constexpr int SMEM = OFF_FLAG + 16 + 1024;        // + alignment slack
+  static constexpr int Q_HALF = 2 * ROWS * 128;            // 64 columns of 256 queries
+  static constexpr int OFF_RING = HALVES * Q_HALF;
+  static constexpr int OFF_X = OFF_RING + UNITS * UNIT;    // float2 [2 groups][ROWS]
+  static constexpr int OFF_BAR = OFF_X + 2 * ROWS * 8;
+  static constexpr int OFF_FLAG = OFF_BAR + 8 * (3 * UNITS + 10);
+  static constexpr int SMEM = OFF_FLAG + 16;
   static_assert(SMEM <= 227 * 1024, "shared memory of a CTA");
 };
 
@@ -84,10 +91,18 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
 // Uses of r stay behind the wait for its loads.
-__device__ __forceinline__ void loaded(uint32_t (&r)[32]) {
+template <int N>
+__device__ __forceinline__ void loaded(uint32_t (&r)[N]) {
 #pragma unroll
-  for (int i = 0; i < 32; i += 8)
+  for (int i = 0; i < N; i += 8)
     asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
                       "+r"(r[i + 6]), "+r"(r[i + 7]));
 }
@@ -111,62 +126,131 @@ __device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
+__device__ __forceinline__ uint64_t fsub2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 
-// A pair of weights as 16-bit values, and what that leaves of them.
-__device__ __forceinline__ uint32_t pack_rest(__nv_bfloat16, float& a, float& b) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  const uint32_t u = *reinterpret_cast<const uint32_t*>(&h);
-  a -= __uint_as_float(u << 16);
-  b -= __uint_as_float(u & 0xffff0000u);
-  return u;
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
 }
-__device__ __forceinline__ uint32_t pack_rest(__half, float& a, float& b) {
+// Lane 0's value, known to the compiler as the same in the whole warp.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ void bar_sync(int id, int count) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+__device__ __forceinline__ void store32(float* p, const float (&x)[8]) {
+  asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]),
+               "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+               : "memory");
+}
+
+// A query's 16 outputs of a piece.
+__device__ __forceinline__ void store_part(float* p, const uint32_t (&x)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; i += 8) {
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(x[i + j]);
+    store32(p + i, f);
+  }
+}
+
+// A pair of weights as 16-bit values, and what those leave of it.
+__device__ __forceinline__ void split(__nv_bfloat16, uint64_t w, uint32_t& hi, uint32_t& lo) {
+  float a, b;
+  unpack2(w, a, b);
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  unpack2(fsub2(w, pack2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u))), a, b);
+  const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
+  lo = *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ void split(__half, uint64_t w, uint32_t& hi, uint32_t& lo) {
+  float a, b;
+  unpack2(w, a, b);
   const __half2 h = __floats2half2_rn(a, b);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
   const float2 f = __half22float2(h);
-  a -= f.x;
-  b -= f.y;
-  return *reinterpret_cast<const uint32_t*>(&h);
+  unpack2(fsub2(w, pack2(f.x, f.y)), a, b);
+  const __half2 r = __floats2half2_rn(a, b);
+  lo = *reinterpret_cast<const uint32_t*>(&r);
 }
-__device__ __forceinline__ uint32_t pack(__nv_bfloat16, float a, float b) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ uint32_t pack(__half, float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
+
+// The ring's units in the order in which warp 1 uses them: before a group's scores of its next tile come
+// the outputs of its last one, so V of a tile follows K of the next tile or two.  next(info, both) gives
+// the tiles, emit(is_v, info) takes the units; either ends the walk with false.
+template <typename Info, typename Next, typename Emit>
+__device__ __forceinline__ void for_units(Next&& next, Emit&& emit) {
+  Info cur, held[2] = {};
+  int tile[2] = {-1, -1};                // whose outputs a group has still to bring
+  bool v[2] = {};                        // V of that tile has still to come
+  bool both;
+  for (int li = 0; next(cur, both); ++li) {
+    bool k = true;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      if (!both && (li & 1) != g) continue;
+      if (v[g]) {
+        if (!emit(true, held[g])) return;
+        if (tile[g ^ 1] == tile[g]) v[g ^ 1] = false;
+      }
+      held[g] = cur;
+      tile[g] = li;
+      v[g] = true;
+      if (k && !emit(false, cur)) return;
+      k = false;
+    }
+  }
+  const bool a_first = tile[0] <= tile[1];
+  if (!a_first && v[1] && !emit(true, held[1])) return;
+  if (v[0]) {
+    if (!emit(true, held[0])) return;
+    if (tile[1] == tile[0]) v[1] = false;
+  }
+  if (a_first && v[1]) emit(true, held[1]);
 }
 
 template <typename T, int D>
 __global__ void __launch_bounds__(X_THREADS, 1)
-    paged_prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Params p) {
+    paged_prefix_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                           const __grid_constant__ CUtensorMap tmV, const Params p) {
   using C = Px<D>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = ptx::smem_u32(smem);
   const uint32_t ring = sbase + C::OFF_RING;
-  const uint32_t bar_full = sbase + C::OFF_BAR, bar_empty = bar_full + 8 * C::UNITS;
-  const uint32_t bar_q = bar_empty + 8 * C::UNITS, bar_s = bar_q + 16, bar_p = bar_s + 16, bar_o = bar_p + 16;
+  // a unit's copies have landed; it has been read; its slots behind the last token are clear
+  const uint32_t bar_full = sbase + C::OFF_BAR, bar_empty = bar_full + 8 * C::UNITS, bar_clean = bar_empty + 8 * C::UNITS;
+  // queries have landed, have been read; scores, weights, outputs of a group
+  const uint32_t bar_q = bar_clean + 8 * C::UNITS, bar_qe = bar_q + 16;
+  const uint32_t bar_s = bar_qe + 16, bar_p = bar_s + 16, bar_o = bar_p + 16;
   volatile int* flags = reinterpret_cast<volatile int*>(smem + C::OFF_FLAG);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31, cta = blockIdx.x;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::UNITS; ++s) {
       ptx::mbar_init(bar_full + 8 * s, 1);
-      ptx::mbar_init(bar_empty + 8 * s, 1);
+      ptx::mbar_init(bar_empty + 8 * s, 2);
+      ptx::mbar_init(bar_clean + 8 * s, 1);
     }
     for (int g = 0; g < 2; ++g) {
-      ptx::mbar_init(bar_q + 8 * g, 4);
+      ptx::mbar_init(bar_q + 8 * g, 1);
+      ptx::mbar_init(bar_qe + 8 * g, 1);
       ptx::mbar_init(bar_s + 8 * g, 1);
-      ptx::mbar_init(bar_p + 8 * g, 4);
+      ptx::mbar_init(bar_p + 8 * g, 8);
       ptx::mbar_init(bar_o + 8 * g, 1);
     }
     flags[0] = 0;
     ptx::fence_mbar_init();
+    ptx::prefetch_tmap(&tmQ);
     ptx::prefetch_tmap(&tmK);
     ptx::prefetch_tmap(&tmV);
   }
@@ -177,308 +261,404 @@ __global__ void __launch_bounds__(X_THREADS, 1)
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  const uint32_t tmem = flags[1];
+  const uint32_t tmem = uniform(flags[1]);
   wait_prior_grid();
 
-  // 128 x 80 + 256 x 208 registers, of the 384 x 168 that the block starts with
-  if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-  else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+  // a warp goes on, or gives up, as a whole
+  const auto wait = [&](uint32_t bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, flags, p.status)) != 0;
+  };
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ copies
+  // 128 x 64 + 512 x 104 registers, all of the 640 x 96 that the block starts with.  (Each in its own
+  // branch: behind a join the compiler keeps to the smaller one.)
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     prefix::Walk walk(p, cta);
     Piece a;
-    const int box = min(p.c.ps, TILE);
-    int u = 0;
-    a.u1 = 0;
-    // the next tile: its tokens, and a page id in each lane
-    int tok = 0, n = 0, page = 0;
-    const auto look = [&]() {
-      if (u >= a.u1) {
-        if (!walk.step(a)) return false;
-        u = a.u0;
-      }
-      tok = a.it.tok0 + u * TILE;
-      n = min(TILE, a.it.tok1 - tok);
-      ++u;
-      page = 0;
-      if (lane * box < n) {
-        page = p.c.table[(size_t)a.it.row * p.c.max_pages + (tok >> p.c.shift) + lane];
-        if (page < 0 || page >= p.c.n_pages) {
-          raise_status(p.status, KVP_ERR_DEVICE_CHECK);
-          page = p.c.n_pages;            // outside the tensor map: zeros
+    if (warp == 0) {
+      // ------------------------------------------------------------ keys and values
+      struct Pages {
+        int page, boxes, y;                // a page id in each lane
+      } next{};
+      const int box = min(p.c.ps, TILE);
+      int u = 0;
+      a.u1 = 0;
+      bool next_both = false;
+      // the page ids are fetched a tile ahead
+      const auto look = [&]() {
+        if (u >= a.u1) {
+          if (!walk.step(a)) return false;
+          u = a.u0;
+          next_both = a.it.nq > ROWS;
         }
-      }
-      return true;
-    };
-    int li = 0;                          // units
-    bool ok = true, more = look();
-    while (more && ok) {
-      const int boxes = (n + box - 1) / box, y = tok & (p.c.ps - 1), held = page;
-      more = look();
+        const int tok = a.it.tok0 + u * TILE, n = min(TILE, a.it.tok1 - tok);
+        ++u;
+        next.boxes = (n + box - 1) / box;
+        next.y = tok & (p.c.ps - 1);
+        next.page = 0;
+        if (lane * box < n) {
+          next.page = p.c.table[(size_t)a.it.row * p.c.max_pages + (tok >> p.c.shift) + lane];
+          if (next.page < 0 || next.page >= p.c.n_pages) {
+            raise_status(p.status, KVP_ERR_DEVICE_CHECK);
+            next.page = p.c.n_pages;       // outside the tensor map: zeros
+          }
+        }
+        return true;
+      };
       const int k = lane / C::HALVES, hf = lane % C::HALVES;
-      const int pg = __shfl_sync(0xffffffffu, held, k);
-#pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        const int s = li % C::UNITS, use = li / C::UNITS;
-        if (use > 0) ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_empty + 8 * s, (use - 1) & 1, flags, p.status));
-        if (!ok) break;
-        if (lane == 0) ptx::mbar_arrive_expect_tx(bar_full + 8 * s, boxes * box * 128 * C::HALVES);
-        __syncwarp();
-        if (k < boxes)
-          ptx::tma_load_3d(ring + s * C::UNIT + hf * C::HALF_BYTES + k * box * 128, v ? &tmV : &tmK, bar_full + 8 * s,
-                           64 * hf, y, pg);
-        __syncwarp();
-        ++li;
-      }
-    }
-    // every copy must land before the CTA can exit
-    for (int j = max(0, li - C::UNITS); j < li; ++j)
-      ptx::mbar_wait_drain(bar_full + 8 * (j % C::UNITS), (j / C::UNITS) & 1, p.status);
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ products
-    if (lane == 0) {
+      int unit = 0;
+      bool more = look();
+      for_units<Pages>(
+          [&](Pages& x, bool& both) {
+            if (!more) return false;
+            x = next;
+            both = next_both;
+            more = look();
+            return true;
+          },
+          [&](bool is_v, const Pages& x) {
+            const int s = unit % C::UNITS, use = unit / C::UNITS;
+            if (use > 0 && !wait(bar_empty + 8 * s, (use - 1) & 1)) return false;
+            const int page = __shfl_sync(0xffffffffu, x.page, k);
+            if (lane == 0) ptx::mbar_arrive_expect_tx(bar_full + 8 * s, x.boxes * box * 128 * C::HALVES);
+            __syncwarp();
+            if (k < x.boxes)
+              ptx::tma_load_3d(ring + s * C::UNIT + hf * C::HALF_BYTES + k * box * 128, is_v ? &tmV : &tmK, bar_full + 8 * s,
+                               64 * hf, x.y, page);
+            __syncwarp();
+            ++unit;
+            return true;
+          });
+      // every copy must land before the CTA can exit
+      for (int j = max(0, unit - C::UNITS); j < unit; ++j)
+        ptx::mbar_wait_drain(bar_full + 8 * (j % C::UNITS), (j / C::UNITS) & 1, p.status);
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ products
       constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
       constexpr uint32_t id_s = ptx::idesc_f16(BF, ROWS, TILE);
       constexpr uint32_t id_o = ptx::idesc_f16(BF, ROWS, D) | 1u << 16;      // B (V) is MN-major
-      prefix::Walk walk(p, cta);
-      Piece a;
-      int li = 0;                        // tiles
-      // of either group: the tile whose weights it has still to bring, and whether that is the first or
-      // the last of its piece; the weights and queries it has brought
+      int li = 0, unit = 0;                // tiles, units of the ring
+      // of either group: the tile whose outputs it has still to bring, V's unit once that is known, whether
+      // it is the first or the last of its piece; the weights it has brought
       struct Group {
-        int pend = -1;
+        int pend = -1, v = -1;
         bool first = false, last = false;
-        int uses_q = 0, uses_p = 0;
+        int uses = 0;
       } ga, gb;
       bool ok = true;
-      const auto outputs = [&](auto which, Group& me, const Group& other) {
+      const auto outputs = [&](auto which, Group& me, Group& other) {
         constexpr int g = decltype(which)::value;
-        const int unit = 2 * me.pend + 1, s = unit % C::UNITS;
-        ok = ok && ptx::mbar_wait(bar_p + 8 * g, me.uses_p++ & 1, flags, p.status) &&
-             ptx::mbar_wait(bar_full + 8 * s, (unit / C::UNITS) & 1, flags, p.status);
-        if (!ok) return;
-        ptx::tc_fence_after();
-        const uint32_t v = ring + s * C::UNIT, o = tmem + TM_O + 128 * g, w = tmem + TM_S + 128 * g;
-#pragma unroll
-        for (int part = 1; part >= 0; --part)
-#pragma unroll
-          for (int k = 0; k < TILE / 16; ++k)
-            mma_f16_ts(o, w + 32 * (k >> 1) + 16 * part + 8 * (k & 1), desc_mn_sw128(v + 2048 * k, C::HALF_BYTES), id_o,
-                       !(me.first && part == 1 && k == 0));
-        if (me.last) ptx::mma_commit(bar_o + 8 * g);
-        if (other.pend != me.pend) ptx::mma_commit(bar_empty + 8 * s);
-        me.pend = -1;
-      };
-      const auto scores = [&](auto which, Group& me, bool both) {
-        constexpr int g = decltype(which)::value;
-        const int unit = 2 * li, s = unit % C::UNITS;
-        if (me.first) ok = ok && ptx::mbar_wait(bar_q + 8 * g, me.uses_q++ & 1, flags, p.status);
-        ok = ok && ptx::mbar_wait(bar_full + 8 * s, (unit / C::UNITS) & 1, flags, p.status);
-        if (!ok) return;
-        ptx::tc_fence_after();
-        const uint32_t q = sbase + g * C::UNIT, k = ring + s * C::UNIT;
-#pragma unroll
-        for (int x = 0; x < D / 16; ++x) {
-          const uint32_t at = (x >> 2) * C::HALF_BYTES + (x & 3) * 32;
-          ptx::mma_f16_ss(tmem + TM_S + 128 * g, ptx::desc_sw128(q + at), ptx::desc_sw128(k + at), id_s, x > 0);
+        if (me.v < 0) {
+          me.v = unit++;
+          if (other.pend == me.pend) other.v = me.v;
         }
-        ptx::mma_commit(bar_s + 8 * g);
-        if (!both || g == 1) ptx::mma_commit(bar_empty + 8 * s);
+        const int s = me.v % C::UNITS;
+        ok = ok && wait(bar_clean + 8 * s, (me.v / C::UNITS) & 1) && wait(bar_p + 8 * g, me.uses++ & 1);
+        if (!ok) return;
+        ptx::tc_fence_after();
+        const uint32_t o = tmem + TM_O + 128 * g, w = tmem + TM_S + 128 * g;
+        const uint64_t v = desc_mn_sw128(ring + s * C::UNIT, C::HALF_BYTES);
+        const bool free = other.pend != me.pend;
+        if (elect_one()) {
+#pragma unroll
+          for (int part = 1; part >= 0; --part)
+#pragma unroll
+            for (int k = 0; k < TILE / 16; ++k)
+              mma_f16_ts(o, w + 32 * (k >> 1) + 16 * part + 8 * (k & 1), v + 128 * k, id_o,
+                         !(me.first && part == 1 && k == 0));
+          if (me.last) ptx::mma_commit(bar_o + 8 * g);
+          if (free) ptx::mma_commit(bar_empty + 8 * s);
+        }
+        __syncwarp();
+        me.pend = me.v = -1;
+      };
+      int kunit = 0, qslot = 0, turn = 0, uses_q0 = 0, uses_q1 = 0;
+      const auto scores = [&](auto which, Group& me, bool both, bool begin, bool end) {
+        constexpr int g = decltype(which)::value;
+        const int s = kunit % C::UNITS;
+        if (begin && !(both && g == 1)) ok = ok && wait(bar_q + 8 * qslot, (qslot ? uses_q1++ : uses_q0++) & 1);
+        if (!(both && g == 1)) ok = ok && wait(bar_full + 8 * s, (kunit / C::UNITS) & 1);
+        if (!ok) return;
+        ptx::tc_fence_after();
+        const uint64_t q = ptx::desc_sw128(sbase + (both ? g : qslot) * (ROWS * 128));
+        const uint64_t k = ptx::desc_sw128(ring + s * C::UNIT);
+        if (elect_one()) {
+#pragma unroll
+          for (int x = 0; x < D / 16; ++x)
+            ptx::mma_f16_ss(tmem + TM_S + 128 * g, q + (((x >> 2) * C::Q_HALF + (x & 3) * 32) >> 4),
+                            k + (((x >> 2) * C::HALF_BYTES + (x & 3) * 32) >> 4), id_s, x > 0);
+          ptx::mma_commit(bar_s + 8 * g);
+          if (!both || g == 1) {
+            ptx::mma_commit(bar_empty + 8 * s);
+            if (end) ptx::mma_commit(bar_qe + 8 * qslot);
+            if (end && both) ptx::mma_commit(bar_qe + 8);
+          }
+        }
+        __syncwarp();
         me.pend = li;
       };
       const std::integral_constant<int, 0> A{};
       const std::integral_constant<int, 1> B{};
       while (ok && walk.step(a)) {
-        const bool both = a.it.nq > ROWS;
-        const int step = both ? 1 : 2;
-        for (int u = a.u0; ok && u < a.u1; ++u, ++li) {
-          const bool first = u - a.u0 < step, last = a.u1 - 1 - u < step;
+        const bool both = uniform(a.it.nq) > ROWS;
+        const int u0 = uniform(a.u0), u1 = uniform(a.u1), step = both ? 1 : 2;
+        qslot = both ? 0 : turn;
+        turn ^= !both;
+        for (int u = u0; ok && u < u1; ++u, ++li) {
+          const bool first = u - u0 < step, last = u1 - 1 - u < step;
+          const bool begin = u == u0, end = u == u1 - 1;
           if (both || !(li & 1)) {
             if (ga.pend >= 0) outputs(A, ga, gb);
             ga.first = first;
             ga.last = last;
-            if (ok) scores(A, ga, both);
+            kunit = unit++;
+            if (ok) scores(A, ga, both, begin, end);
           }
           if (ok && (both || (li & 1))) {
             if (gb.pend >= 0) outputs(B, gb, ga);
             gb.first = first;
             gb.last = last;
-            if (ok) scores(B, gb, both);
+            if (!both) kunit = unit++;
+            if (ok) scores(B, gb, both, begin, end);
           }
         }
       }
       // the older one first
-      const bool second = ga.pend >= 0 && (gb.pend < 0 || ga.pend <= gb.pend);
-      if (!second && ok && gb.pend >= 0) outputs(B, gb, ga);
+      const bool a_first = ga.pend <= gb.pend;
+      if (!a_first && ok && gb.pend >= 0) outputs(B, gb, ga);
       if (ok && ga.pend >= 0) outputs(A, ga, gb);
-      if (second && ok && gb.pend >= 0) outputs(B, gb, ga);
+      if (a_first && ok && gb.pend >= 0) outputs(B, gb, ga);
+    } else if (warp == 2) {
+      // ------------------------------------------------------------ slots behind the last token
+      int u = 0, unit = 0;
+      a.u1 = 0;
+      for_units<int>(
+          [&](int& valid, bool& both) {
+            if (u >= a.u1) {
+              if (!walk.step(a)) return false;
+              u = a.u0;
+            }
+            valid = a.it.tok1 - a.it.tok0 - u * TILE;
+            both = a.it.nq > ROWS;
+            ++u;
+            return true;
+          },
+          [&](bool is_v, int valid) {
+            const int s = unit % C::UNITS;
+            if (!wait(bar_full + 8 * s, (unit / C::UNITS) & 1)) return false;
+            if (is_v && valid < TILE) {
+              for (int e = valid * 8 + lane; e < TILE * 8; e += 32)
+#pragma unroll
+                for (int hf = 0; hf < C::HALVES; ++hf)
+                  *reinterpret_cast<uint4*>(smem + C::OFF_RING + s * C::UNIT + hf * C::HALF_BYTES + e * 16) =
+                      make_uint4(0, 0, 0, 0);
+              ptx::fence_proxy_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) {
+              ptx::mbar_arrive(bar_clean + 8 * s);
+              ptx::mbar_arrive(bar_empty + 8 * s);
+            }
+            __syncwarp();
+            ++unit;
+            return true;
+          });
+    } else {
+      // ------------------------------------------------------------ queries: a box per sequence and 64-column half
+      int turn = 0, fills[2] = {0, 0}, uses[2] = {0, 0};
+      bool ok = true;
+      while (ok && walk.step(a)) {
+        const bool both = a.it.nq > ROWS;
+        const int slot = both ? 0 : turn;
+        turn ^= !both;
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+          if (both || s == slot) {
+            if (fills[s] > 0) ok = ok && wait(bar_qe + 8 * s, (fills[s] - 1) & 1);
+            ++fills[s];
+          }
+        if (!ok) break;
+        const uint32_t bar = bar_q + 8 * slot;
+        const int boxes = a.it.nq / p.G * C::HALVES, h = a.it.row % p.Hkv;
+        if (lane == 0) ptx::mbar_arrive_expect_tx(bar, a.it.nq * 128 * C::HALVES);
+        __syncwarp();
+        for (int e = lane; e < boxes; e += 32) {
+          const int k = e / C::HALVES, hf = e % C::HALVES;
+          const int n = a.it.list < 0 ? a.it.row / p.Hkv : p.list[a.it.list + a.it.q0 / p.G + k];
+          ptx::tma_load_3d(sbase + hf * C::Q_HALF + (slot * ROWS + k * p.G) * 128, &tmQ, bar, 64 * hf, h * p.G, n);
+        }
+        __syncwarp();
+        uses[0] += slot == 0;
+        uses[1] += slot == 1;
+      }
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        if (uses[s] > 0) ptx::mbar_wait_drain(bar_q + 8 * s, (uses[s] - 1) & 1, p.status);
     }
-    __syncwarp();
-  } else if (warp >= 4) {
+  } else {
     // ------------------------------------------------------------ softmax
-    const int g = (warp - 4) >> 2, quad = warp & 3, tid = (warp & 3) * 32 + lane;
-    const uint32_t lanes = (uint32_t)quad << 21;          // this warp's TMEM lanes
-    const uint32_t ts = tmem + TM_S + 128 * g + lanes, to = tmem + TM_O + 128 * g + lanes;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     prefix::Walk walk(p, cta);
     Piece a;
-    int li0 = 0, uses_s = 0, uses_o = 0;
-    bool ok = true;
-    const auto wait = [&](uint32_t bar, uint32_t parity) {   // a warp goes on, or gives up, as a whole
-      return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, flags, p.status)) != 0;
-    };
+    const int w = (warp - 4) >> 2, g = w >> 1, c = w & 1, quad = warp & 3, tid = quad * 32 + lane;
+    const uint32_t lanes = (uint32_t)quad << 21;          // this warp's TMEM lanes
+    const uint32_t ts = tmem + TM_S + 128 * g + 64 * c + lanes, to = tmem + TM_O + lanes;
+    const int pair = 1 + g * 4 + quad;                    // barrier of the two warps that share queries
+    float2* row = reinterpret_cast<float2*>(smem + C::OFF_X) + tid;   // [g * ROWS]: what they tell each other
+    constexpr int ALL = 9;                                // barrier of all sixteen
+    const float mul = p.zero ? 0.f : -1.f;
+    int li0 = 0, uses_s = 0, uses_oa = 0, uses_ob = 0;
+    bool ok = true;                                       // (once a wait ran out no other is begun; barriers are met)
     while (walk.step(a)) {
       const bool own = a.it.list < 0, both = a.it.nq > ROWS;
       const int step = both ? 1 : 2, tiles = a.u1 - a.u0;
       const int u0 = both ? a.u0 : a.u0 + ((li0 ^ g) & 1);
+      const bool has_a = both || a.u0 + (li0 & 1) < a.u1, has_b = both || a.u0 + (~li0 & 1) < a.u1;
       const int q0 = both ? g * ROWS : 0, nq = min(ROWS, a.it.nq - q0);
-      const bool busy = quad * 32 < nq;                   // (the same in a warp)
-      const int li_piece = li0;
+      const bool busy = quad * 32 < nq;                   // (the same in both warps)
       li0 += tiles;
       // this thread's query, and where its part goes
       size_t slot = 0;
       if (tid < nq) {
         int qg;
         const int r = prefix::query_row(p, a.it, q0 + tid, qg);
-        slot = a.u0 == 0 ? prefix::first_slot(p, own, r, qg, both ? 0 : g)
-                         : prefix::cont_slot(p, cta, g * ROWS + tid);
-      }
-      float2* ml = (a.u0 == 0 ? p.first_ml : p.cont_ml) + slot;
-      if (u0 >= a.u1) {                                   // the other group has the piece's only tile
-        if (tid < nq) *ml = make_float2(-INFINITY, 0.f);
-        continue;
-      }
-      // the queries, a lane per 16 bytes of a row
-      {
-        constexpr int CH = D / 8;
-        const uint32_t keep = p.zero ? 0u : 0xffffffffu, sign = p.flip ? 0x80008000u : 0u;
-        for (int e = tid; e < nq * CH; e += ROWS) {
-          const int i = e / CH, ch = e % CH;
-          int qg;
-          const int r = prefix::query_row(p, a.it, q0 + i, qg);
-          uint4 x = *reinterpret_cast<const uint4*>((const T*)p.q + (r / p.Hkv) * p.q_stride +
-                                                    (size_t)((r % p.Hkv) * p.G + qg) * D + ch * 8);
-          x.x = (x.x & keep) ^ sign;
-          x.y = (x.y & keep) ^ sign;
-          x.z = (x.z & keep) ^ sign;
-          x.w = (x.w & keep) ^ sign;
-          *reinterpret_cast<uint4*>(smem + g * C::UNIT + (ch >> 3) * C::HALF_BYTES + i * 128 +
-                                    (((ch & 7) ^ (i & 7)) << 4)) = x;
-        }
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar_q + 8 * g);
+        slot = a.u0 == 0 ? prefix::first_slot(p, own, r, qg) : prefix::cont_slot(p, cta, q0 + tid);
       }
       float m = -INFINITY, l = 0.f;
-      for (int u = u0; ok && u < a.u1; u += step) {
-        ok = wait(bar_s + 8 * g, uses_s++ & 1);
-        if (!ok) break;
-        const int valid = a.it.tok1 - a.it.tok0 - u * TILE;
+      for (int u = u0; u < a.u1; u += step) {
+        ok = ok && wait(bar_s + 8 * g, uses_s & 1);
+        ++uses_s;
+        const int valid = a.it.tok1 - a.it.tok0 - u * TILE - 64 * c;
         if (busy) {
           ptx::tc_fence_after();
-          // the largest score, then the weights chunk by chunk: 32 scores make way for 16 + 16 columns of weights
-          float top = -INFINITY;
+          uint32_t s[2][32];
+          ptx::tmem_ld32(ts, s[0]);
+          ptx::tmem_ld32(ts + 32, s[1]);
+          ptx::tmem_ld_wait();
+          loaded(s[0]);
+          loaded(s[1]);
+          if (p.flip || p.zero) {
 #pragma unroll
-          for (int k = 0; k < TILE; k += 32) {
-            uint32_t s[32];
-            ptx::tmem_ld32(ts + k, s);
-            ptx::tmem_ld_wait();
-            loaded(s);
-            if (valid < TILE) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (k + i >= valid) s[i] = 0xff800000u;
-            }
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) top = max3(top, __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+            for (int i = 0; i < 64; ++i) s[i >> 5][i & 31] = __float_as_uint(__uint_as_float(s[i >> 5][i & 31]) * mul);
           }
-          const float x = top * p.c2;
-          if (u == u0) {
-            m = x;
-          } else if (__any_sync(0xffffffffu, x > m + LAG)) {
-            const float up = fmaxf(m, x), f = paged::weight(m, up);
-            m = up;
-            l *= f;
-            // the tile before has been added up: the scores' barrier follows its products
-#pragma unroll 1
-            for (int k = 0; k < D; k += 32) {
-              uint32_t o[32], w[2][16];
-              ptx::tmem_ld32(to + k, o);
-              ptx::tmem_ld_wait();
-              loaded(o);
+          if (valid < 64) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) w[i >> 4][i & 15] = __float_as_uint(__uint_as_float(o[i]) * f);
-              tmem_st16(to + k, w[0]);
-              tmem_st16(to + k + 16, w[1]);
+            for (int i = 0; i < 64; ++i)
+              if (i >= valid) s[i >> 5][i & 31] = 0xff800000u;
+          }
+          float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            top[0] = max3(top[0], __uint_as_float(s[0][i]), __uint_as_float(s[0][i + 1]));
+            top[1] = max3(top[1], __uint_as_float(s[1][i]), __uint_as_float(s[1][i + 1]));
+          }
+          const float x = fmaxf(top[0], top[1]) * p.c2;
+          if (ptx::bar_red_or(u == u0 || x > m + LAG, pair, 64)) {
+            (c ? row[g * ROWS].y : row[g * ROWS].x) = x;
+            bar_sync(pair, 64);
+            const float up = max3(m, x, c ? row[g * ROWS].x : row[g * ROWS].y);
+            if (u != u0) {
+              const float f = paged::weight(m, up);
+              l *= f;
+              // the tile before has been added up: the scores' barrier follows its products
+#pragma unroll 1
+              for (int k = c * (D / 2); k < (c + 1) * (D / 2); k += 16) {
+                uint32_t o[16];
+                tmem_ld16(to + 128 * g + k, o);
+                ptx::tmem_ld_wait();
+                loaded(o);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_st16(to + 128 * g + k, o);
+              }
             }
+            m = up;
           }
           const float off = m == -INFINITY ? 0.f : -m;     // nothing but -inf so far: weights of 0
           const uint64_t c2 = pack2(p.c2, p.c2), off2 = pack2(off, off);
           uint64_t sum[2] = {0, 0};
 #pragma unroll
-          for (int k = 0; k < TILE; k += 32) {
-            uint32_t s[32], hi[16], lo[16];
-            ptx::tmem_ld32(ts + k, s);
-            ptx::tmem_ld_wait();
-            loaded(s);
-            if (valid < TILE) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (k + i >= valid) s[i] = 0xff800000u;
-            }
+          for (int k = 0; k < 2; ++k) {
+            // 32 scores make way for 16 + 16 columns of weights
+            uint32_t hi[16], lo[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               float w0, w1;
-              unpack2(ffma2(pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c2, off2), w0, w1);
-              w0 = fast_exp2(w0);
-              w1 = fast_exp2(w1);
-              sum[i & 1] = fadd2(sum[i & 1], pack2(w0, w1));
-              hi[i] = pack_rest(T(), w0, w1);
-              lo[i] = pack(T(), w0, w1);
+              unpack2(ffma2(pack2(__uint_as_float(s[k][2 * i]), __uint_as_float(s[k][2 * i + 1])), c2, off2), w0, w1);
+              const uint64_t w = pack2(fast_exp2(w0), fast_exp2(w1));
+              sum[i & 1] = fadd2(sum[i & 1], w);
+              split(T(), w, hi[i], lo[i]);
             }
-            tmem_st16(ts + k, hi);
-            tmem_st16(ts + k + 16, lo);
+            tmem_st16(ts + 32 * k, hi);
+            tmem_st16(ts + 32 * k + 16, lo);
           }
-          float a0, a1, b0, b1;
-          unpack2(sum[0], a0, a1);
-          unpack2(sum[1], b0, b1);
-          l += (a0 + a1) + (b0 + b1);
+          float a0, a1;
+          unpack2(fadd2(sum[0], sum[1]), a0, a1);
+          l += a0 + a1;
           tmem_st_wait();
           ptx::tc_fence_before();
-        }
-        if (valid < TILE) {
-          const int unit = 2 * (li_piece + u - a.u0) + 1, sl = unit % C::UNITS;
-          ok = wait(bar_full + 8 * sl, (unit / C::UNITS) & 1);
-          for (int e = valid * 8 + tid; e < TILE * 8; e += ROWS)
-#pragma unroll
-            for (int hf = 0; hf < C::HALVES; ++hf)
-              *reinterpret_cast<uint4*>(smem + C::OFF_RING + sl * C::UNIT + hf * C::HALF_BYTES + e * 16) = make_uint4(0, 0, 0, 0);
-          ptx::fence_proxy_async_smem();
         }
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar_p + 8 * g);
       }
-      if (!ok) break;
-      ok = wait(bar_o + 8 * g, uses_o++ & 1);
-      if (!ok) break;
-      if (busy) {
-        ptx::tc_fence_after();
-        float* out = (a.u0 == 0 ? p.first_o : p.cont_o) + slot * D;
+      // the piece's outputs
+      float* out = (a.u0 == 0 ? p.first_o : p.cont_o) + slot * D;
+      float2* ml = (a.u0 == 0 ? p.first_ml : p.cont_ml) + slot;
+      if (g ? has_b : has_a) ok = ok && wait(bar_o + 8 * g, (g ? uses_ob : uses_oa) & 1);
+      if (both) {
+        if (busy) {
+          ptx::tc_fence_after();
+          (c ? row[g * ROWS].y : row[g * ROWS].x) = l;
+          bar_sync(pair, 64);
+          l += c ? row[g * ROWS].x : row[g * ROWS].y;
 #pragma unroll
-        for (int k = 0; k < D; k += 32) {
-          uint32_t o[32];
-          ptx::tmem_ld32(to + k, o);
-          ptx::tmem_ld_wait();
-          loaded(o);
-          if (tid < nq) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<uint4*>(out + k + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          for (int k = c * (D / 2); k < (c + 1) * (D / 2); k += 16) {
+            uint32_t o[16];
+            tmem_ld16(to + 128 * g + k, o);
+            ptx::tmem_ld_wait();
+            loaded(o);
+            if (tid < nq) store_part(out + k, o);
           }
+          if (tid < nq && c == 0) *ml = make_float2(m, l);
+          ptx::tc_fence_before();
+          bar_sync(pair, 64);
+        }
+        ok = ok && wait(bar_o + 8 * (g ^ 1), (g ? uses_oa : uses_ob) & 1);
+      } else {
+        if (g ? has_a : has_b) ok = ok && wait(bar_o + 8 * (g ^ 1), (g ? uses_oa : uses_ob) & 1);
+        ptx::tc_fence_after();
+        if (busy) {
+          if (c) row[g * ROWS].y = l;
+          bar_sync(pair, 64);
+          if (!c) row[g * ROWS] = make_float2(m, l + row[g * ROWS].y);
+        }
+        bar_sync(ALL, 512);
+        if (busy) {
+          const float2 A = row[0], B = row[ROWS];
+          const float M = fmaxf(A.x, B.x), fa = paged::weight(A.x, M), fb = paged::weight(B.x, M);
+#pragma unroll
+          for (int k = w * (D / 4); k < (w + 1) * (D / 4); k += 16) {
+            uint32_t o[16], y[16];
+            tmem_ld16(to + k, o);
+            tmem_ld16(to + 128 + k, y);
+            ptx::tmem_ld_wait();
+            loaded(o);
+            loaded(y);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              // (a group without a tile has left what was there before)
+              const float va = has_a ? __uint_as_float(o[i]) * fa : 0.f;
+              o[i] = __float_as_uint(has_b ? fmaf(__uint_as_float(y[i]), fb, va) : va);
+            }
+            if (tid < nq) store_part(out + k, o);
+          }
+          if (tid < nq && w == 0) *ml = make_float2(M, fmaf(A.y, fa, B.y * fb));
         }
         ptx::tc_fence_before();
-        if (tid < nq) *ml = make_float2(m, l);
+        bar_sync(ALL, 512);                               // both outputs have been read
       }
+      uses_oa += has_a;
+      uses_ob += has_b;
     }
   }
   ptx::tc_fence_before();
@@ -503,14 +683,15 @@ EncodeTiledFn encoder() {
   return fn;
 }
 
-bool pool_map(CUtensorMap* m, const PagedView& c, const void* base) {
+// [z][y][D] values, the axes `z_stride` and `y_stride` elements apart; boxes of 64 values by `rows`.
+bool map_of(CUtensorMap* m, int dtype, const void* base, int D, int y, int z, int64_t y_stride, int64_t z_stride, int rows) {
   const EncodeTiledFn fn = encoder();
   if (!fn) return false;
-  const cuuint64_t dims[3] = {(cuuint64_t)c.D, (cuuint64_t)c.ps, (cuuint64_t)c.n_pages};
-  const cuuint64_t strides[2] = {(cuuint64_t)c.token_stride * 2, (cuuint64_t)c.page_stride * 2};
-  const cuuint32_t box[3] = {64, (cuuint32_t)(c.ps < TILE ? c.ps : TILE), 1};
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)y, (cuuint64_t)z};
+  const cuuint64_t strides[2] = {(cuuint64_t)y_stride * 2, (cuuint64_t)z_stride * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)rows, 1};
   const cuuint32_t estr[3] = {1, 1, 1};
-  return fn(m, c.dtype == KVP_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+  return fn(m, dtype == KVP_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -518,13 +699,17 @@ bool pool_map(CUtensorMap* m, const PagedView& c, const void* base) {
 
 template <typename T, int D>
 cudaError_t run(const Params& p, cudaStream_t st) {
-  CUtensorMap tk, tv;
-  if (!pool_map(&tk, p.c, p.c.k) || !pool_map(&tv, p.c, p.c.v)) return cudaErrorInvalidValue;
+  CUtensorMap tq, tk, tv;
+  const int box = p.c.ps < TILE ? p.c.ps : TILE;
+  if (!map_of(&tq, p.c.dtype, p.q, D, p.Hq, p.N, D, p.q_stride, p.G) ||
+      !map_of(&tk, p.c.dtype, p.c.k, D, p.c.ps, p.c.n_pages, p.c.token_stride, p.c.page_stride, box) ||
+      !map_of(&tv, p.c.dtype, p.c.v, D, p.c.ps, p.c.n_pages, p.c.token_stride, p.c.page_stride, box))
+    return cudaErrorInvalidValue;
   const auto kern = paged_prefix_tc_kernel<T, D>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Px<D>::SMEM);
   if (e != cudaSuccess) return e;
   count_launches(1);
-  return launch_with_pdl(kern, dim3((unsigned)p.ctas), dim3(X_THREADS), Px<D>::SMEM, st, tk, tv, p);
+  return launch_with_pdl(kern, dim3((unsigned)p.ctas), dim3(X_THREADS), Px<D>::SMEM, st, tq, tk, tv, p);
 }
 
 }  // namespace
