@@ -18,6 +18,7 @@ namespace {
 using prefix::Item;
 using prefix::Params;
 using prefix::Piece;
+using prefix::GAP;
 using prefix::TILE;
 
 constexpr int LOOK_THREADS = 256;
@@ -175,16 +176,18 @@ __global__ void __launch_bounds__(CHOOSE_THREADS) prefix_choose_kernel(const Par
 // once the block has added up the warps'.
 __global__ void __launch_bounds__(PLAN_THREADS) prefix_plan_kernel(const Params p) {
   constexpr int WARPS = PLAN_THREADS / 32, AHEAD = 4;
-  __shared__ int sums[2][WARPS];
+  __shared__ long long places_sh[WARPS];
+  __shared__ int items_sh[WARPS];
   wait_prior_grid();
   allow_next_grid();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, R = p.c.R;
   const int run = (2 * R + 32 * WARPS - 1) / (32 * WARPS) * 32, begin = min(warp * run, 2 * R), end = min(begin + run, 2 * R);
   struct Place {
     int tok0, tok1, nq, n;               // tokens, queries, items
+    int width, each;                     // places of a tile, of an item
   };
   const auto place = [&](int i) {
-    Place x{0, 0, 0, 0};
+    Place x{0, 0, 0, 0, 2, GAP};
     if (i >= end) return x;
     if (i >= R) {
       x.tok0 = p.start[i - R];
@@ -197,59 +200,76 @@ __global__ void __launch_bounds__(PLAN_THREADS) prefix_plan_kernel(const Params 
       x.nq = k * p.G;
       x.n = (x.nq + p.qt - 1) / p.qt;
     }
+    x.width = prefix::width_of(min(x.nq, p.qt));
+    x.each = prefix::tiles_of(x.tok1 - x.tok0) * x.width + GAP;
     return x;
   };
-  int tiles = 0, items = 0;
+  long long sum = 0;
+  int items = 0;
   for (int i0 = begin; i0 < end; i0 += 32 * AHEAD) {
     Place x[AHEAD];
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k) x[k] = place(i0 + 32 * k + lane);
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k) {
-      tiles += x[k].n * prefix::tiles_of(x[k].tok1 - x[k].tok0);
+      sum += (long long)x[k].n * x[k].each;
       items += x[k].n;
     }
   }
-  tiles = __reduce_add_sync(0xffffffffu, tiles);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
   items = __reduce_add_sync(0xffffffffu, items);
   if (lane == 0) {
-    sums[0][warp] = tiles;
-    sums[1][warp] = items;
+    places_sh[warp] = sum;
+    items_sh[warp] = items;
   }
   __syncthreads();
   // (WARPS = 32: a lane for every warp's sum)
-  const int t = sums[0][lane], n = sums[1][lane];
-  int at_t = __reduce_add_sync(0xffffffffu, lane < warp ? t : 0), at_n = __reduce_add_sync(0xffffffffu, lane < warp ? n : 0);
-  tiles = __reduce_add_sync(0xffffffffu, t);
+  const long long t = places_sh[lane];
+  const int n = items_sh[lane];
+  long long before = lane < warp ? t : 0;
+  sum = t;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, off);
+    sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  }
+  // places are counted in 32 bits: 2^29 are 30 s of work
+  const bool fits = sum < 1LL << 29;
+  if (!fits && threadIdx.x == 0) raise_status(p.status, KVP_ERR_DEVICE_CHECK);
+  int at = fits ? (int)before : 0, at_n = __reduce_add_sync(0xffffffffu, lane < warp ? n : 0);
+  const int total = fits ? (int)sum : 0;
   items = __reduce_add_sync(0xffffffffu, n);
-  const int active = min((tiles + 1) / 2, p.ctas);
-  if (threadIdx.x == 0) *p.head = prefix::Head{tiles, active, items, 0};
+  // a CTA has at least four places: a tile or more wherever it lies in an item
+  const int active = min(total / 4, p.ctas);
+  if (threadIdx.x == 0) *p.head = prefix::Head{total, active, total > 0 ? items : 0, 0};
   for (int i0 = begin; i0 < end; i0 += 32) {
     const int i = i0 + lane;
-    const Place x = place(i);
-    const int each = prefix::tiles_of(x.tok1 - x.tok0);
-    const int t_in = warp_inclusive_scan(x.n * each), n_in = warp_inclusive_scan(x.n);
-    const int t0 = at_t + t_in - x.n * each, n0 = at_n + n_in - x.n;
+    Place x = place(i);
+    if (!fits) x.n = 0;
+    const int at_in = warp_inclusive_scan(x.n * x.each), n_in = warp_inclusive_scan(x.n);
+    const int at0 = at + at_in - x.n * x.each, n0 = at_n + n_in - x.n;
     const bool own = i >= R;
     const int r = own ? i - R : i;
     for (int k = 0; k < x.n; ++k) {
       Item it;
-      it.tile0 = t0 + k * each;
+      const int gap0 = at0 + k * x.each;
+      it.tile0 = gap0 + GAP;
       it.row = r;
       it.tok0 = x.tok0;
       it.tok1 = x.tok1;
       it.q0 = k * p.qt;
       it.nq = min(p.qt, x.nq - k * p.qt);
       it.list = own ? -1 : (r % p.Hkv) * p.N + p.base[r / p.Hkv];
-      it.pad = 0;
+      it.width = x.width;
       p.items[n0 + k] = it;
-      // the CTAs whose range begins in it
-      const int hi = paged::cta_of(it.tile0 + each - 1, tiles, active);
-      for (int c = it.tile0 == 0 ? 0 : paged::cta_of(it.tile0 - 1, tiles, active) + 1; c <= hi; ++c) p.cta_item[c] = n0 + k;
+      // the CTAs whose range begins in it or its gap
+      const int hi = paged::cta_of(gap0 + x.each - 1, total, active);
+      for (int c = gap0 == 0 ? 0 : paged::cta_of(gap0 - 1, total, active) + 1; c <= hi; ++c) p.cta_item[c] = n0 + k;
     }
     __syncwarp();
     if (i < end) (own ? p.own_item : p.pre_item)[r] = x.n > 0 ? n0 : -1;
-    at_t += __shfl_sync(0xffffffffu, t_in, 31);
+    at += __shfl_sync(0xffffffffu, at_in, 31);
     at_n += __shfl_sync(0xffffffffu, n_in, 31);
   }
 }
@@ -280,9 +300,9 @@ __global__ void __launch_bounds__(F_THREADS) prefix_f32_kernel(const Params p) {
   float *ms = sm + C::OFF_M, *ls = ms + F_QT, *fs = ls + F_QT;
   const int tid = threadIdx.x, cta = blockIdx.x;
   wait_prior_grid();
-  prefix::Walk walk(p, cta);
+  prefix::Walk<true> walk(p, cta);
   Piece a;
-  while (walk.step(a)) {
+  while (walk.step(p, a)) {
     const bool own = a.it.list < 0;
     __syncthreads();
     for (int e = tid; e < F_QT * D / 4; e += F_THREADS) {
@@ -431,8 +451,9 @@ __global__ void __launch_bounds__(JOIN_THREADS) prefix_join_kernel(const Params 
     }
     const auto span = [&](int item, int& lo) {
       const Item it = p.items[item];
+      const int last = it.tile0 + (prefix::tiles_of(it.tok1 - it.tok0) - 1) * it.width;
       lo = paged::cta_of(it.tile0, head.total, head.active);
-      return paged::cta_of(it.tile0 + prefix::tiles_of(it.tok1 - it.tok0) - 1, head.total, head.active) - lo + 1;
+      return paged::cta_of(last, head.total, head.active) - lo + 1;
     };
     if (pre >= 0) n0 = span(pre, lo0);
     if (own >= 0) n1 = span(own, lo1);
@@ -582,9 +603,12 @@ cudaError_t run(const Params& p, cudaStream_t st) {
   if constexpr (sizeof(T) == 2) e = launch_paged_prefix_tc(p, st);
   else e = run_f32<D>(p, st);
   if (e != cudaSuccess) return e;
-  // A query can have a part or two from every CTA: few queries take a block each, many a warp.
+  // A query can have a part or two from every CTA: as many warps for each as let the blocks (eight an SM) run
+  // at once, up to eight.
   const long long queries = (long long)p.c.R * p.G;
-  const int warps = queries <= 2048 ? JOIN_THREADS / 32 : 1, per = JOIN_THREADS / 32 / warps;
+  int warps = JOIN_THREADS / 32;
+  while (warps > 1 && queries * warps > 64LL * sm_count()) warps >>= 1;
+  const int per = JOIN_THREADS / 32 / warps;
   count_launches(1);
   return launch_with_pdl(prefix_join_kernel<T, D>, dim3((unsigned)((queries + per - 1) / per)), dim3(JOIN_THREADS), 0,
                          st, p, warps);

@@ -4,7 +4,9 @@
 // Work comes in items: the shared prefix of a family and KV head with up to `qt` of the family's queries,
 // or one row's own tokens (behind the prefix it takes part in) with its G queries.  The tiles of TILE keys
 // of all items form one sequence, of which every CTA takes an equal range; a CTA's share of an item is a
-// piece.  A piece that begins an item leaves its partial results (maximum, sum, unnormalised output) at the
+// piece.  The sequence has two places for a tile, three for one that meets more than 128 queries (bound by
+// the tensor cores), and before every item GAP places, about what it costs to begin and end one: without
+// those, the CTAs that had the short items at the end took 1.4 times as long as the rest.  A piece that begins an item leaves its partial results (maximum, sum, unnormalised output) at the
 // queries' own places, one that goes on from the CTA before at the CTA's, and the join adds a query's parts
 // in the order of the tiles, so results do not depend on timing.
 #pragma once
@@ -17,19 +19,20 @@ namespace kvp {
 namespace prefix {
 
 constexpr int TILE = 128;                // keys
+constexpr int GAP = 4;
 
 // A prefix with some of its queries, or a row's own tokens.
 struct __align__(16) Item {
-  int tile0;             // first tile in the sequence of all items
+  int tile0;             // place of its first tile
   int row;               // row whose pages hold the tokens
   int tok0, tok1;        // tokens
   int q0, nq;            // queries, counted in the family's list (own tokens: 0, G)
   int list;              // prefix: where the head's list of participants begins; own tokens: -1
-  int pad;
+  int width;             // places of a tile
 };
 
-struct Head {
-  int total, active, n_items, pad;
+struct __align__(16) Head {
+  int total, active, n_items, pad;       // places, CTAs that have any
 };
 
 struct Params {
@@ -56,7 +59,7 @@ struct Params {
   int* own_item;         // [R]
   Item* items;
   Head* head;
-  int* cta_item;         // [ctas] item that a CTA's range begins in
+  int* cta_item;         // [ctas] first item with a tile in a CTA's range
   // partial results
   float2* first_ml;      // [2 kinds][R * G]
   float* first_o;        // [...][D]
@@ -68,6 +71,7 @@ struct Params {
 };
 
 __device__ __forceinline__ int tiles_of(int n) { return (n + TILE - 1) / TILE; }
+__device__ __forceinline__ int width_of(int nq) { return nq > 128 ? 3 : 2; }
 __device__ __forceinline__ int row_len(const Params& p, int r) {
   const int n = p.c.lens[r];
   return n < 0 ? 0 : (n > p.c.cap ? p.c.cap : n);
@@ -79,32 +83,36 @@ struct Piece {
   int u0, u1;
 };
 
-// Walks over a CTA's pieces; the next item's record is fetched one ahead.
+// Walks over a CTA's pieces; with AHEAD the next item's record is fetched one ahead.
+template <bool AHEAD>
 struct Walk {
-  const Item* items;
-  int item, x, end;
+  int item, n_items, x, end;
   Item next;
+  __device__ __forceinline__ Walk() {}
   __device__ __forceinline__ Walk(const Params& p, int cta) {
     const Head h = *p.head;
-    items = p.items;
+    const int first = p.cta_item[cta];
+    n_items = h.n_items;
     x = end = 0;
     if (cta >= h.active) return;
     x = paged::cta_begin(cta, h.total, h.active);
     end = paged::cta_begin(cta + 1, h.total, h.active);
-    item = p.cta_item[cta];
-    next = items[item];
+    item = first;
+    if (AHEAD) next = p.items[item];
   }
-  __device__ __forceinline__ bool step(Piece& a) {
-    if (x >= end) return false;
-    a.it = next;
-    a.u0 = x - a.it.tile0;
-    const int n = tiles_of(a.it.tok1 - a.it.tok0);
-    if (a.u0 < 0 || n <= a.u0) return false;   // no such plan
-    a.u1 = n < a.u0 + (end - x) ? n : a.u0 + (end - x);
-    x += a.u1 - a.u0;
-    ++item;
-    if (x < end) next = items[item];
-    return true;
+  __device__ __forceinline__ bool step(const Params& p, Piece& a) {
+    while (x < end) {
+      a.it = AHEAD ? next : p.items[item];
+      if (a.it.tile0 >= end) break;
+      const int w = a.it.width, past = max(0, x - a.it.tile0);
+      a.u0 = (past + w - 1) / w;
+      a.u1 = min(tiles_of(a.it.tok1 - a.it.tok0), (end - a.it.tile0 + w - 1) / w);
+      x = a.it.tile0 + a.u1 * w;
+      if (++item >= n_items) x = end;
+      else if (AHEAD && x < end) next = p.items[item];
+      if (a.u0 < a.u1) return true;
+    }
+    return false;
   }
 };
 

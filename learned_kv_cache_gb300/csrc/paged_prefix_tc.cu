@@ -35,12 +35,14 @@
 namespace kvp {
 namespace {
 
+using prefix::Item;
 using prefix::Params;
 using prefix::Piece;
 using prefix::TILE;
 
 constexpr int X_THREADS = 640;
 constexpr int ROWS = 128;                // queries of a group
+constexpr int RUN = 8;                   // sequences whose queries are copied at once
 constexpr float LAG = 8.f;               // log2 of how far the maximum may lag
 
 template <int D>
@@ -90,6 +92,16 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
@@ -97,6 +109,16 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 // Uses of r stay behind the wait for its loads.
 template <int N>
@@ -221,8 +243,8 @@ __device__ __forceinline__ void for_units(Next&& next, Emit&& emit) {
 
 template <typename T, int D>
 __global__ void __launch_bounds__(X_THREADS, 1)
-    paged_prefix_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                           const __grid_constant__ CUtensorMap tmV, const Params p) {
+    paged_prefix_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmQs,
+                           const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Params p) {
   using C = Px<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = ptx::smem_u32(smem);
@@ -251,6 +273,7 @@ __global__ void __launch_bounds__(X_THREADS, 1)
     flags[0] = 0;
     ptx::fence_mbar_init();
     ptx::prefetch_tmap(&tmQ);
+    ptx::prefetch_tmap(&tmQs);
     ptx::prefetch_tmap(&tmK);
     ptx::prefetch_tmap(&tmV);
   }
@@ -262,7 +285,7 @@ __global__ void __launch_bounds__(X_THREADS, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = uniform(flags[1]);
-  wait_prior_grid();
+  allow_next_grid();                     // (the join's blocks come as SMs fall free)
 
   // a warp goes on, or gives up, as a whole
   const auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -273,7 +296,8 @@ __global__ void __launch_bounds__(X_THREADS, 1)
   // branch: behind a join the compiler keeps to the smaller one.)
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    prefix::Walk walk(p, cta);
+    wait_prior_grid();
+    prefix::Walk<true> walk(p, cta);
     Piece a;
     if (warp == 0) {
       // ------------------------------------------------------------ keys and values
@@ -287,7 +311,7 @@ __global__ void __launch_bounds__(X_THREADS, 1)
       // the page ids are fetched a tile ahead
       const auto look = [&]() {
         if (u >= a.u1) {
-          if (!walk.step(a)) return false;
+          if (!walk.step(p, a)) return false;
           u = a.u0;
           next_both = a.it.nq > ROWS;
         }
@@ -343,9 +367,9 @@ __global__ void __launch_bounds__(X_THREADS, 1)
       struct Group {
         int pend = -1, v = -1;
         bool first = false, last = false;
-        int uses = 0;
+        int uses = 1;                      // (the first are no tile's: see the softmax)
       } ga, gb;
-      bool ok = true;
+      bool ok = wait(bar_p, 0) && wait(bar_p + 8, 0);
       const auto outputs = [&](auto which, Group& me, Group& other) {
         constexpr int g = decltype(which)::value;
         if (me.v < 0) {
@@ -364,7 +388,7 @@ __global__ void __launch_bounds__(X_THREADS, 1)
           for (int part = 1; part >= 0; --part)
 #pragma unroll
             for (int k = 0; k < TILE / 16; ++k)
-              mma_f16_ts(o, w + 32 * (k >> 1) + 16 * part + 8 * (k & 1), v + 128 * k, id_o,
+              mma_f16_ts(o, w + 16 * k + 8 * part, v + 128 * k, id_o,
                          !(me.first && part == 1 && k == 0));
           if (me.last) ptx::mma_commit(bar_o + 8 * g);
           if (free) ptx::mma_commit(bar_empty + 8 * s);
@@ -399,7 +423,7 @@ __global__ void __launch_bounds__(X_THREADS, 1)
       };
       const std::integral_constant<int, 0> A{};
       const std::integral_constant<int, 1> B{};
-      while (ok && walk.step(a)) {
+      while (ok && walk.step(p, a)) {
         const bool both = uniform(a.it.nq) > ROWS;
         const int u0 = uniform(a.u0), u1 = uniform(a.u1), step = both ? 1 : 2;
         qslot = both ? 0 : turn;
@@ -431,11 +455,11 @@ __global__ void __launch_bounds__(X_THREADS, 1)
     } else if (warp == 2) {
       // ------------------------------------------------------------ slots behind the last token
       int u = 0, unit = 0;
-      a.u1 = 0;
+      a.u0 = a.u1 = 0;
       for_units<int>(
           [&](int& valid, bool& both) {
             if (u >= a.u1) {
-              if (!walk.step(a)) return false;
+              if (!walk.step(p, a)) return false;
               u = a.u0;
             }
             valid = a.it.tok1 - a.it.tok0 - u * TILE;
@@ -464,93 +488,107 @@ __global__ void __launch_bounds__(X_THREADS, 1)
             return true;
           });
     } else {
-      // ------------------------------------------------------------ queries: a box per sequence and 64-column half
-      int turn = 0, fills[2] = {0, 0}, uses[2] = {0, 0};
+      // ------------------------------------------------------------ queries, ahead of their piece
+      // A box per sequence and 64-column half (some 75 cycles each, however small), or per RUN sequences
+      // that follow each other.
+      int turn = 0, fills0 = 0, fills1 = 0, uses0 = 0, uses1 = 0;
       bool ok = true;
-      while (ok && walk.step(a)) {
+      while (walk.step(p, a)) {
         const bool both = a.it.nq > ROWS;
         const int slot = both ? 0 : turn;
         turn ^= !both;
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-          if (both || s == slot) {
-            if (fills[s] > 0) ok = ok && wait(bar_qe + 8 * s, (fills[s] - 1) & 1);
-            ++fills[s];
-          }
+        if (slot == 0 && fills0++ > 0) ok = ok && wait(bar_qe, fills0 & 1);
+        if ((both || slot == 1) && fills1++ > 0) ok = ok && wait(bar_qe + 8, fills1 & 1);
         if (!ok) break;
-        const uint32_t bar = bar_q + 8 * slot;
-        const int boxes = a.it.nq / p.G * C::HALVES, h = a.it.row % p.Hkv;
+        const uint32_t bar = bar_q + 8 * slot, to = sbase + slot * ROWS * 128;
+        const int seqs = a.it.nq / p.G, h = a.it.row % p.Hkv * p.G;
+        const int* list = p.list + a.it.list + a.it.q0 / p.G;
         if (lane == 0) ptx::mbar_arrive_expect_tx(bar, a.it.nq * 128 * C::HALVES);
         __syncwarp();
-        for (int e = lane; e < boxes; e += 32) {
-          const int k = e / C::HALVES, hf = e % C::HALVES;
-          const int n = a.it.list < 0 ? a.it.row / p.Hkv : p.list[a.it.list + a.it.q0 / p.G + k];
-          ptx::tma_load_3d(sbase + hf * C::Q_HALF + (slot * ROWS + k * p.G) * 128, &tmQ, bar, 64 * hf, h * p.G, n);
+        const int hf = lane % C::HALVES;
+        if (a.it.list < 0) {
+          if (lane < C::HALVES) ptx::tma_load_3d(to + hf * C::Q_HALF, &tmQ, bar, 64 * hf, h, a.it.row / p.Hkv);
+        } else {
+          for (int k0 = lane / C::HALVES * RUN; k0 < seqs; k0 += 32 / C::HALVES * RUN) {
+            int n[RUN];
+            bool run = true;
+#pragma unroll
+            for (int k = 0; k < RUN; ++k) {
+              n[k] = k0 + k < seqs ? list[k0 + k] : -1;
+              run = run && n[k] == n[0] + k;
+            }
+            const uint32_t at = to + hf * C::Q_HALF + k0 * p.G * 128;
+            if (run) {
+              ptx::tma_load_3d(at, &tmQs, bar, 64 * hf, h, n[0]);
+            } else {
+#pragma unroll
+              for (int k = 0; k < RUN; ++k)
+                if (k0 + k < seqs) ptx::tma_load_3d(at + k * p.G * 128, &tmQ, bar, 64 * hf, h, n[k]);
+            }
+          }
         }
         __syncwarp();
-        uses[0] += slot == 0;
-        uses[1] += slot == 1;
+        uses0 += slot == 0;
+        uses1 += slot == 1;
       }
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-        if (uses[s] > 0) ptx::mbar_wait_drain(bar_q + 8 * s, (uses[s] - 1) & 1, p.status);
+      // every copy must land before the CTA can exit
+      if (uses0 > 0) ptx::mbar_wait_drain(bar_q, (uses0 - 1) & 1, p.status);
+      if (uses1 > 0) ptx::mbar_wait_drain(bar_q + 8, (uses1 - 1) & 1, p.status);
     }
   } else {
     // ------------------------------------------------------------ softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
-    prefix::Walk walk(p, cta);
-    Piece a;
+    prefix::Walk<false> walk;            // (registers: the item's record is read again when the piece ends)
     const int w = (warp - 4) >> 2, g = w >> 1, c = w & 1, quad = warp & 3, tid = quad * 32 + lane;
     const uint32_t lanes = (uint32_t)quad << 21;          // this warp's TMEM lanes
     const uint32_t ts = tmem + TM_S + 128 * g + 64 * c + lanes, to = tmem + TM_O + lanes;
     const int pair = 1 + g * 4 + quad;                    // barrier of the two warps that share queries
     float2* row = reinterpret_cast<float2*>(smem + C::OFF_X) + tid;   // [g * ROWS]: what they tell each other
     constexpr int ALL = 9;                                // barrier of all sixteen
-    const float mul = p.zero ? 0.f : -1.f;
     int li0 = 0, uses_s = 0, uses_oa = 0, uses_ob = 0;
     bool ok = true;                                       // (once a wait ran out no other is begun; barriers are met)
-    while (walk.step(a)) {
-      const bool own = a.it.list < 0, both = a.it.nq > ROWS;
+    // The first piece is none: while the plan is still being made, a tile of whatever lies in TMEM brings
+    // the instructions in (a first tile took 8000 cycles, any other 2000).
+    bool dry = true;
+    Piece a{Item{0, 0, 0, TILE, 0, 2 * ROWS, 0, 0}, 0, 1};
+    for (; dry || walk.step(p, a);) {
+      const bool both = a.it.nq > ROWS;
       const int step = both ? 1 : 2, tiles = a.u1 - a.u0;
       const int u0 = both ? a.u0 : a.u0 + ((li0 ^ g) & 1);
       const bool has_a = both || a.u0 + (li0 & 1) < a.u1, has_b = both || a.u0 + (~li0 & 1) < a.u1;
-      const int q0 = both ? g * ROWS : 0, nq = min(ROWS, a.it.nq - q0);
+      const int q0 = both ? g * ROWS : 0, nq = min(ROWS, a.it.nq - q0), tokens = a.it.tok1 - a.it.tok0 - 64 * c;
       const bool busy = quad * 32 < nq;                   // (the same in both warps)
-      li0 += tiles;
-      // this thread's query, and where its part goes
-      size_t slot = 0;
-      if (tid < nq) {
-        int qg;
-        const int r = prefix::query_row(p, a.it, q0 + tid, qg);
-        slot = a.u0 == 0 ? prefix::first_slot(p, own, r, qg) : prefix::cont_slot(p, cta, q0 + tid);
-      }
+      if (!dry) li0 += tiles;
       float m = -INFINITY, l = 0.f;
       for (int u = u0; u < a.u1; u += step) {
-        ok = ok && wait(bar_s + 8 * g, uses_s & 1);
-        ++uses_s;
-        const int valid = a.it.tok1 - a.it.tok0 - u * TILE - 64 * c;
+        if (!dry) ok = ok && wait(bar_s + 8 * g, uses_s++ & 1);
+        const int valid = tokens - u * TILE;
         if (busy) {
           ptx::tc_fence_after();
-          uint32_t s[2][32];
-          ptx::tmem_ld32(ts, s[0]);
-          ptx::tmem_ld32(ts + 32, s[1]);
-          ptx::tmem_ld_wait();
-          loaded(s[0]);
-          loaded(s[1]);
-          if (p.flip || p.zero) {
-#pragma unroll
-            for (int i = 0; i < 64; ++i) s[i >> 5][i & 31] = __float_as_uint(__uint_as_float(s[i >> 5][i & 31]) * mul);
-          }
-          if (valid < 64) {
-#pragma unroll
-            for (int i = 0; i < 64; ++i)
-              if (i >= valid) s[i >> 5][i & 31] = 0xff800000u;
-          }
+          uint32_t s[32];
           float top[2] = {-INFINITY, -INFINITY};
+          {
+            uint32_t y[32];
+            ptx::tmem_ld32(ts, s);
+            ptx::tmem_ld32(ts + 32, y);
+            ptx::tmem_ld_wait();
+            loaded(s);
+            loaded(y);
+            if (p.flip || p.zero || valid < 64) {
+              const float mul = p.zero ? 0.f : p.flip ? -1.f : 1.f;
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            top[0] = max3(top[0], __uint_as_float(s[0][i]), __uint_as_float(s[0][i + 1]));
-            top[1] = max3(top[1], __uint_as_float(s[1][i]), __uint_as_float(s[1][i + 1]));
+              for (int i = 0; i < 32; ++i) {
+                s[i] = i < valid ? __float_as_uint(__uint_as_float(s[i]) * mul) : 0xff800000u;
+                y[i] = i + 32 < valid ? __float_as_uint(__uint_as_float(y[i]) * mul) : 0xff800000u;
+              }
+              tmem_st32(ts + 32, y);
+              tmem_st_wait();
+            }
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              top[0] = max3(top[0], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+              top[1] = max3(top[1], __uint_as_float(y[i]), __uint_as_float(y[i + 1]));
+            }
           }
           const float x = fmaxf(top[0], top[1]) * p.c2;
           if (ptx::bar_red_or(u == u0 || x > m + LAG, pair, 64)) {
@@ -562,14 +600,14 @@ __global__ void __launch_bounds__(X_THREADS, 1)
               l *= f;
               // the tile before has been added up: the scores' barrier follows its products
 #pragma unroll 1
-              for (int k = c * (D / 2); k < (c + 1) * (D / 2); k += 16) {
-                uint32_t o[16];
-                tmem_ld16(to + 128 * g + k, o);
+              for (int k = c * (D / 2); k < (c + 1) * (D / 2); k += 8) {
+                uint32_t o[8];
+                tmem_ld8(to + 128 * g + k, o);
                 ptx::tmem_ld_wait();
                 loaded(o);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                tmem_st16(to + 128 * g + k, o);
+                for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_st8(to + 128 * g + k, o);
               }
             }
             m = up;
@@ -577,21 +615,31 @@ __global__ void __launch_bounds__(X_THREADS, 1)
           const float off = m == -INFINITY ? 0.f : -m;     // nothing but -inf so far: weights of 0
           const uint64_t c2 = pack2(p.c2, p.c2), off2 = pack2(off, off);
           uint64_t sum[2] = {0, 0};
+          // 16 scores make way for 8 + 8 columns of weights; the second 32 are read again, 16 ahead (all 64 in
+          // registers would spill)
+          const auto weigh = [&](const uint32_t* x, int k) {
+            uint32_t parts[16];
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            // 32 scores make way for 16 + 16 columns of weights
-            uint32_t hi[16], lo[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
+            for (int i = 0; i < 8; ++i) {
               float w0, w1;
-              unpack2(ffma2(pack2(__uint_as_float(s[k][2 * i]), __uint_as_float(s[k][2 * i + 1])), c2, off2), w0, w1);
+              unpack2(ffma2(pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), c2, off2), w0, w1);
               const uint64_t w = pack2(fast_exp2(w0), fast_exp2(w1));
               sum[i & 1] = fadd2(sum[i & 1], w);
-              split(T(), w, hi[i], lo[i]);
+              split(T(), w, parts[i], parts[8 + i]);
             }
-            tmem_st16(ts + 32 * k, hi);
-            tmem_st16(ts + 32 * k + 16, lo);
-          }
+            tmem_st16(ts + k, parts);
+          };
+          uint32_t y[2][16];
+          weigh(s, 0);
+          tmem_ld16(ts + 32, y[0]);
+          weigh(s + 16, 16);
+          ptx::tmem_ld_wait();
+          loaded(y[0]);
+          tmem_ld16(ts + 48, y[1]);
+          weigh(y[0], 32);
+          ptx::tmem_ld_wait();
+          loaded(y[1]);
+          weigh(y[1], 48);
           float a0, a1;
           unpack2(fadd2(sum[0], sum[1]), a0, a1);
           l += a0 + a1;
@@ -601,7 +649,20 @@ __global__ void __launch_bounds__(X_THREADS, 1)
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar_p + 8 * g);
       }
+      if (dry) {
+        dry = false;
+        wait_prior_grid();
+        walk = prefix::Walk<false>(p, cta);
+        continue;
+      }
       // the piece's outputs
+      size_t slot = 0;
+      if (tid < nq) {
+        int qg;
+        const Item it = p.items[walk.item - 1];
+        const int r = prefix::query_row(p, it, q0 + tid, qg);
+        slot = a.u0 == 0 ? prefix::first_slot(p, it.list < 0, r, qg) : prefix::cont_slot(p, cta, q0 + tid);
+      }
       float* out = (a.u0 == 0 ? p.first_o : p.cont_o) + slot * D;
       float2* ml = (a.u0 == 0 ? p.first_ml : p.cont_ml) + slot;
       if (g ? has_b : has_a) ok = ok && wait(bar_o + 8 * g, (g ? uses_ob : uses_oa) & 1);
@@ -683,13 +744,14 @@ EncodeTiledFn encoder() {
   return fn;
 }
 
-// [z][y][D] values, the axes `z_stride` and `y_stride` elements apart; boxes of 64 values by `rows`.
-bool map_of(CUtensorMap* m, int dtype, const void* base, int D, int y, int z, int64_t y_stride, int64_t z_stride, int rows) {
+// [z][y][D] values, the axes `z_stride` and `y_stride` elements apart; boxes of 64 values by `rows` by `runs`.
+bool map_of(CUtensorMap* m, int dtype, const void* base, int D, int y, int z, int64_t y_stride, int64_t z_stride, int rows,
+            int runs) {
   const EncodeTiledFn fn = encoder();
   if (!fn) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)y, (cuuint64_t)z};
   const cuuint64_t strides[2] = {(cuuint64_t)y_stride * 2, (cuuint64_t)z_stride * 2};
-  const cuuint32_t box[3] = {64, (cuuint32_t)rows, 1};
+  const cuuint32_t box[3] = {64, (cuuint32_t)rows, (cuuint32_t)runs};
   const cuuint32_t estr[3] = {1, 1, 1};
   return fn(m, dtype == KVP_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -699,17 +761,18 @@ bool map_of(CUtensorMap* m, int dtype, const void* base, int D, int y, int z, in
 
 template <typename T, int D>
 cudaError_t run(const Params& p, cudaStream_t st) {
-  CUtensorMap tq, tk, tv;
+  CUtensorMap tq, tqs, tk, tv;
   const int box = p.c.ps < TILE ? p.c.ps : TILE;
-  if (!map_of(&tq, p.c.dtype, p.q, D, p.Hq, p.N, D, p.q_stride, p.G) ||
-      !map_of(&tk, p.c.dtype, p.c.k, D, p.c.ps, p.c.n_pages, p.c.token_stride, p.c.page_stride, box) ||
-      !map_of(&tv, p.c.dtype, p.c.v, D, p.c.ps, p.c.n_pages, p.c.token_stride, p.c.page_stride, box))
+  if (!map_of(&tq, p.c.dtype, p.q, D, p.Hq, p.N, D, p.q_stride, p.G, 1) ||
+      !map_of(&tqs, p.c.dtype, p.q, D, p.Hq, p.N, D, p.q_stride, p.G, RUN) ||
+      !map_of(&tk, p.c.dtype, p.c.k, D, p.c.ps, p.c.n_pages, p.c.token_stride, p.c.page_stride, box, 1) ||
+      !map_of(&tv, p.c.dtype, p.c.v, D, p.c.ps, p.c.n_pages, p.c.token_stride, p.c.page_stride, box, 1))
     return cudaErrorInvalidValue;
   const auto kern = paged_prefix_tc_kernel<T, D>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Px<D>::SMEM);
   if (e != cudaSuccess) return e;
   count_launches(1);
-  return launch_with_pdl(kern, dim3((unsigned)p.ctas), dim3(X_THREADS), Px<D>::SMEM, st, tq, tk, tv, p);
+  return launch_with_pdl(kern, dim3((unsigned)p.ctas), dim3(X_THREADS), Px<D>::SMEM, st, tq, tqs, tk, tv, p);
 }
 
 }  // namespace
