@@ -835,6 +835,7 @@ size_t kvp_qk_norm_rope_backward_workspace_size(int dtype, int n_batch, int h_q,
   kvp::RopeArgs a{};
   if (rope_args("rope", dtype, n_batch, seq_len, head_dim, nullptr, nullptr, 0, 0, &a) != KVP_OK || h_q < 1 || h_kv < 1)
     return 0;
+  a.n_tensors = 2;
   a.t[0].heads = h_q;
   a.t[1].heads = h_kv;
   return kvp::norm_rope_backward_workspace(a, head_dim);

@@ -12,12 +12,13 @@
 //    frequency in turns as a fraction of 2^64, so that the angle is one 64-bit product whose overflow drops
 //    the whole turns: exact up to 2^-64 of a turn per position, for every 32-bit position.  Its upper 32
 //    bits, less the nearest quarter turn, are exact to 2^-25 of an eighth of a turn as a float.
-//  * A block takes TOK tokens and all their heads; its threads compute the tokens' cosines and sines once
-//    (64 pairs x 4 tokens: one each), and a group of D / 16 lanes then walks over heads of one token with
-//    its 8 pairs' values in registers.
+//  * The unit of work is a token with some of a tensor's heads, and D / 16 lanes have one: they compute its
+//    cosines and sines (8 pairs a lane, while the first rows are on their way) and walk over the heads, the
+//    next rows' loads always ahead of the arithmetic.  Nothing is shared, so no warp waits for another (with
+//    the angles in shared memory and a few tokens a block, 8192 tokens of 32 + 8 heads took 52 us).
 //  * A lane owns 8 pairs of a row: two vectors of 8 values that lie rotary_dim / 2 apart (halves) or side
 //    by side (interleaved), so pairs never cross lanes and sums over a row are 2 or 3 shuffles.
-//  * Rows are taken a few at a time, all their loads before the first is used.
+//  * Lane groups side by side have tokens side by side: in a tensor laid out by heads their rows touch.
 #include <cmath>
 
 #include "kvp_common.cuh"
@@ -28,7 +29,7 @@ namespace {
 
 constexpr int THREADS = 256;
 constexpr int MAX_PAIRS = 64;
-constexpr int MAX_TOK = 32;
+constexpr int FORWARD_BLOCKS = 2, BACK_BLOCKS = 1;          // per SM
 
 struct Freqs {
   uint64_t step[MAX_PAIRS];   // turns per position, times 2^64
@@ -79,24 +80,6 @@ __device__ __forceinline__ float2 turn_of(int pos, uint64_t step) {
   }
 }
 
-// Fills cs[tok][pair] for tokens [t0, t0 + TOK) of the n_tokens.
-__device__ __forceinline__ void block_turns(const RopeArgs& a, const Freqs& f, long long t0, int tok, long long n_tokens,
-                                            float2* cs, int pairs_stride) {
-  const int pairs = a.rotary_dim >> 1;
-  for (int i = threadIdx.x; i < tok * pairs; i += THREADS) {
-    const int x = i / pairs, pair = i - x * pairs;
-    const long long t = t0 + x;
-    if (t >= n_tokens) break;
-    const int b = (int)(t / a.seq_len), s = (int)(t - (long long)b * a.seq_len);
-    const int pos = a.positions ? a.positions[b * a.position_stride + s] : a.start + s;
-    float2 v = turn_of(pos, f.step[pair]);
-    v.x *= a.gain;
-    v.y *= a.gain;
-    if (a.inverse) v.y = -v.y;
-    cs[x * pairs_stride + pair] = v;
-  }
-}
-
 // The lane's place in a row.
 template <int D, bool INTERLEAVED>
 struct Lane {
@@ -131,58 +114,97 @@ __device__ __forceinline__ void turn(float (&x)[2][8], const float2 (&cs)[8], fl
   }
 }
 
-// This lane's weights (1 without any).
-template <typename T>
-__device__ __forceinline__ void load_weights(const void* w, int f32, int at0, int at1, float (&out)[2][8]) {
+// Units of a tensor: token by token for the first `chunk` heads, then for the next.
+struct Split {
+  uint32_t n_tokens;
+  int chunk;
+  uint32_t units[2];     // of either tensor
+};
+// A unit: rows [h0, h0 + n) of a tensor's heads at a token (none: n = 0).
+struct Unit {
+  int b, s, h0, n;
+  __device__ __forceinline__ Unit(const RopeArgs& a, const Split& split, int heads, uint32_t u, bool live) {
+    const uint32_t part = live ? u / split.n_tokens : 0, t = live ? u - part * split.n_tokens : 0;
+    b = (int)(t / (uint32_t)a.seq_len);
+    s = (int)(t - (uint32_t)b * a.seq_len);
+    h0 = part * split.chunk;
+    n = live ? min(split.chunk, heads - h0) : 0;
+  }
+};
+
+// What every block has in shared memory.
+template <int D>
+struct Tables {
+  uint64_t step[MAX_PAIRS];
+  float w[2][D];         // weights (1 without any)
+};
+template <typename T, int D, bool NORM>
+__device__ __forceinline__ void fill_tables(Tables<D>& sh, const RopeArgs& a, const Freqs& f) {
+  if (threadIdx.x < MAX_PAIRS) sh.step[threadIdx.x] = f.step[threadIdx.x];
+  wait_prior_grid();
+  allow_next_grid();
+  if (NORM && threadIdx.x < 2 * D) {
+    const int j = threadIdx.x / D, i = threadIdx.x % D;
+    const void* w = j ? a.t[1].w : a.t[0].w;
+    sh.w[j][i] = !w ? 1.f : a.w_f32 ? ((const float*)w)[i] : to_f32<T>(((const T*)w)[i]);
+  }
+  __syncthreads();
+}
+__device__ __forceinline__ int position(const RopeArgs& a, const Unit& u) {
+  return a.positions ? a.positions[u.b * a.position_stride + u.s] : a.start + u.s;
+}
+// Cosines and sines (times gain) of the lane's pairs.
+__device__ __forceinline__ void turns(const RopeArgs& a, const uint64_t* step, int pos, bool rotates, float2 (&cs)[8]) {
 #pragma unroll
-  for (int k = 0; k < 2; ++k)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int at = (k ? at1 : at0) + i;
-      out[k][i] = !w ? 1.f : f32 ? ((const float*)w)[at] : to_f32<T>(((const T*)w)[at]);
+  for (int i = 0; i < 8; ++i) {
+    float2 v = make_float2(1.f, 0.f);
+    if (rotates) {
+      v = turn_of(pos, step[i]);
+      v.x *= a.gain;
+      v.y *= a.inverse ? -a.gain : a.gain;
     }
+    cs[i] = v;
+  }
+}
+__device__ __forceinline__ void load_w(const float* w, int at0, int at1, float (&out)[2][8]) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 4) {
+    *reinterpret_cast<float4*>(&out[0][i]) = *reinterpret_cast<const float4*>(w + at0 + i);
+    *reinterpret_cast<float4*>(&out[1][i]) = *reinterpret_cast<const float4*>(w + at1 + i);
+  }
 }
 
 template <typename T, int D, bool NORM, bool INTERLEAVED>
-__global__ void __launch_bounds__(THREADS, 2)
-    rope_kernel(const RopeArgs a, const __grid_constant__ Freqs f, int tok, long long n_tokens) {
+__global__ void __launch_bounds__(THREADS, FORWARD_BLOCKS)
+    rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ Freqs f, const Split split) {
   using L = Lane<D, INTERLEAVED>;
-  constexpr int U = sizeof(T) == 2 ? 4 : 2;               // rows at a time
-  __shared__ float2 cs_sh[MAX_TOK * (D / 2)];
+  // rows at a time: twice these in registers (four with norms spill: 457 us for 434)
+  constexpr int U = sizeof(T) == 4 ? 2 : NORM ? 3 : 4;
+  __shared__ __align__(16) Tables<D> sh;
   const L lane(a.rotary_dim);
-  wait_prior_grid();
-  allow_next_grid();
-  const long long t0 = (long long)blockIdx.x * tok;
-  block_turns(a, f, t0, tok, n_tokens, cs_sh, D / 2);
-  __syncthreads();
-  const int group = threadIdx.x / L::PER_ROW, x = group % tok, stride = L::GROUPS / tok;
-  const long long t = t0 + x;
-  const bool live = t < n_tokens;                         // the lanes of a row agree
-  const int b = live ? (int)(t / a.seq_len) : 0, s = live ? (int)(t - (long long)b * a.seq_len) : 0;
-  float2 cs[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) cs[i] = lane.turns && live ? cs_sh[x * (D / 2) + 8 * lane.u + i] : make_float2(1.f, 0.f);
-#pragma unroll 1
-  for (int j = 0; j < a.n_tensors; ++j) {
-    const RopeTensor& z = a.t[j];
-    const T* in = (const T*)z.x + b * z.xs[0] + s * z.xs[2];
-    T* out = (T*)z.y + b * z.ys[0] + s * z.ys[2];
-    float w[2][8];
-    if (NORM) load_weights<T>(z.w, a.w_f32, lane.at0, lane.at1, w);
-    // the same number of steps for every lane of a warp: the sums are warp-wide shuffles
-    for (int h0 = 0; h0 < z.heads; h0 += U * stride) {
-      const int h = h0 + group / tok;
-      Raw<T> raw[U][2];
+  fill_tables<T, D, NORM>(sh, a, f);
+  const uint32_t all = split.units[0] + split.units[1];
+  const uint32_t first = blockIdx.x * L::GROUPS + threadIdx.x / 32 * (32 / L::PER_ROW);   // the warp's
+  for (uint32_t u0 = first; u0 < all; u0 += gridDim.x * L::GROUPS) {
+    const uint32_t id = u0 + (threadIdx.x & 31) / L::PER_ROW;
+    const bool second = id >= split.units[0];
+    const RopeTensor& z = second ? a.t[1] : a.t[0];
+    const Unit u(a, split, z.heads, second ? id - split.units[0] : id, id < all);
+    const int64_t xs = z.xs[1], ys = z.ys[1];
+    const T* in = (const T*)z.x + u.b * z.xs[0] + u.s * z.xs[2] + u.h0 * xs;
+    T* out = (T*)z.y + u.b * z.ys[0] + u.s * z.ys[2] + u.h0 * ys;
+    const auto load = [&](Raw<T> (&raw)[U][2], int h) {
 #pragma unroll
       for (int k = 0; k < U; ++k)
-        if (live && h + k * stride < z.heads) {
-          raw[k][0].load(in + (h + k * stride) * z.xs[1] + lane.at0);
-          raw[k][1].load(in + (h + k * stride) * z.xs[1] + lane.at1);
+        if (h + k < u.n) {
+          raw[k][0].load(in + (h + k) * xs + lane.at0);
+          raw[k][1].load(in + (h + k) * xs + lane.at1);
         }
+    };
+    float2 cs[8];
+    const auto rows = [&](const Raw<T> (&raw)[U][2], int h) {
 #pragma unroll
       for (int k = 0; k < U; ++k) {
-        if (h0 + k * stride >= z.heads) break;            // none of the block's
-        const bool mine = live && h + k * stride < z.heads;
         float v[2][8];
         raw[k][0].get(v[0]);
         raw[k][1].get(v[1]);
@@ -191,6 +213,8 @@ __global__ void __launch_bounds__(THREADS, 2)
 #pragma unroll
           for (int i = 0; i < 8; ++i) ss = fmaf(v[0][i], v[0][i], fmaf(v[1][i], v[1][i], ss));
           const float r = __frsqrt_rn(row_sum<L::PER_ROW>(ss) * (1.f / D) + a.eps);
+          float w[2][8];
+          load_w(sh.w[second], lane.at0, lane.at1, w);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             v[0][i] = v[0][i] * r * w[0][i];
@@ -198,71 +222,77 @@ __global__ void __launch_bounds__(THREADS, 2)
           }
         }
         if (lane.turns) turn<INTERLEAVED>(v, cs, 1.f);
-        if (mine) {
-          store8(out + (h + k * stride) * z.ys[1] + lane.at0, v[0]);
-          store8(out + (h + k * stride) * z.ys[1] + lane.at1, v[1]);
+        if (h + k < u.n) {
+          store8(out + (h + k) * ys + lane.at0, v[0]);
+          store8(out + (h + k) * ys + lane.at1, v[1]);
         }
       }
+    };
+    // every lane of the warp takes as many steps as any: sums over a row are the whole warp's shuffles
+    const int most = __reduce_max_sync(0xffffffffu, u.n);
+    Raw<T> even[U][2], odd[U][2];
+    const int pos = position(a, u);
+    load(even, 0);
+    turns(a, sh.step + 8 * lane.u, pos, lane.turns, cs);
+    for (int h = 0; h < most; h += 2 * U) {
+      load(odd, h + U);
+      rows(even, h);
+      if (h + U >= most) break;
+      load(even, h + 2 * U);
+      rows(odd, h + U);
     }
   }
 }
 
-// Gradients of one tensor: blocks [first, first + blocks) walk over its tokens.  A lane sums its 16 values'
-// weight gradients over all its rows in registers; the block's groups are added at the end, and the blocks'
-// sums by rope_weight_kernel in a fixed order.
+// Gradients: blocks [0, split_at) have the first tensor's units, the rest the second's.  A lane sums its 16
+// values' weight gradients over all its rows in registers; the block's groups are added at the end, and the
+// blocks' sums by rope_weight_kernel in a fixed order.
 template <typename T, int D, bool INTERLEAVED>
-__global__ void __launch_bounds__(THREADS, 2)
-    norm_rope_backward_kernel(const RopeArgs a, const __grid_constant__ Freqs f, long long n_tokens, int split,
-                              int tok0, int tok1, float* __restrict__ part) {
+__global__ void __launch_bounds__(THREADS, BACK_BLOCKS)
+    norm_rope_backward_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ Freqs f, const Split split,
+                              int split_at, float* __restrict__ part) {
   using L = Lane<D, INTERLEAVED>;
   constexpr int U = sizeof(T) == 2 ? 2 : 1;
-  __shared__ float2 cs_sh[MAX_TOK * (D / 2)];
+  __shared__ __align__(16) Tables<D> sh;
   __shared__ float sum_sh[THREADS / 32][D];
   const L lane(a.rotary_dim);
-  const int j = (int)blockIdx.x < split ? 0 : 1, tok = j == 0 ? tok0 : tok1;
-  const int block = j == 0 ? blockIdx.x : blockIdx.x - split, blocks = j == 0 ? split : gridDim.x - split;
-  const RopeTensor& z = a.t[j];
-  wait_prior_grid();
-  allow_next_grid();
-  const int group = threadIdx.x / L::PER_ROW, x = group % tok, stride = L::GROUPS / tok;
-  float w[2][8], dw[2][8];
-  load_weights<T>(z.w, a.w_f32, lane.at0, lane.at1, w);
+  fill_tables<T, D, true>(sh, a, f);
+  const bool second = (int)blockIdx.x >= split_at;
+  const uint32_t block = second ? blockIdx.x - split_at : blockIdx.x, blocks = second ? gridDim.x - split_at : split_at;
+  const RopeTensor& z = second ? a.t[1] : a.t[0];
+  const uint32_t all = split.units[second];
+  float dw[2][8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) dw[0][i] = dw[1][i] = 0.f;
-  for (long long t0 = (long long)block * tok; t0 < n_tokens; t0 += (long long)blocks * tok) {
-    __syncthreads();                                      // the last tokens' values are read
-    block_turns(a, f, t0, tok, n_tokens, cs_sh, D / 2);
-    __syncthreads();
-    const long long t = t0 + x;
-    const bool live = t < n_tokens;
-    const int b = live ? (int)(t / a.seq_len) : 0, s = live ? (int)(t - (long long)b * a.seq_len) : 0;
-    const T* in = (const T*)z.x + b * z.xs[0] + s * z.xs[2];
-    const T* dy = (const T*)z.dy + b * z.dys[0] + s * z.dys[2];
-    T* out = (T*)z.y + b * z.ys[0] + s * z.ys[2];
-    float2 cs[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) cs[i] = lane.turns && live ? cs_sh[x * (D / 2) + 8 * lane.u + i] : make_float2(1.f, 0.f);
-    for (int h0 = 0; h0 < z.heads; h0 += U * stride) {
-      const int h = h0 + group / tok;
-      Raw<T> raw[U][2], back[U][2];
+  const uint32_t first = block * L::GROUPS + threadIdx.x / 32 * (32 / L::PER_ROW);
+  for (uint32_t u0 = first; u0 < all; u0 += blocks * L::GROUPS) {
+    const uint32_t id = u0 + (threadIdx.x & 31) / L::PER_ROW;
+    const Unit u(a, split, z.heads, id, id < all);
+    const int64_t xs = z.xs[1], ds = z.dys[1], ys = z.ys[1];
+    const T* in = (const T*)z.x + u.b * z.xs[0] + u.s * z.xs[2] + u.h0 * xs;
+    const T* dy = (const T*)z.dy + u.b * z.dys[0] + u.s * z.dys[2] + u.h0 * ds;
+    T* out = (T*)z.y + u.b * z.ys[0] + u.s * z.ys[2] + u.h0 * ys;
+    const auto load = [&](Raw<T> (&raw)[U][4], int h) {
 #pragma unroll
       for (int k = 0; k < U; ++k)
-        if (live && h + k * stride < z.heads) {
-          raw[k][0].load(in + (h + k * stride) * z.xs[1] + lane.at0);
-          raw[k][1].load(in + (h + k * stride) * z.xs[1] + lane.at1);
-          back[k][0].load(dy + (h + k * stride) * z.dys[1] + lane.at0);
-          back[k][1].load(dy + (h + k * stride) * z.dys[1] + lane.at1);
+        if (h + k < u.n) {
+          raw[k][0].load(in + (h + k) * xs + lane.at0);
+          raw[k][1].load(in + (h + k) * xs + lane.at1);
+          raw[k][2].load(dy + (h + k) * ds + lane.at0);
+          raw[k][3].load(dy + (h + k) * ds + lane.at1);
         }
+    };
+    float2 cs[8];
+    const auto rows = [&](const Raw<T> (&raw)[U][4], int h) {
 #pragma unroll
       for (int k = 0; k < U; ++k) {
-        if (h0 + k * stride >= z.heads) break;
-        const bool mine = live && h + k * stride < z.heads;
-        float v[2][8], g[2][8];
+        float v[2][8], g[2][8], w[2][8];
         raw[k][0].get(v[0]);
         raw[k][1].get(v[1]);
-        back[k][0].get(g[0]);
-        back[k][1].get(g[1]);
+        raw[k][2].get(g[0]);
+        raw[k][3].get(g[1]);
         if (lane.turns) turn<INTERLEAVED>(g, cs, -1.f);
+        load_w(sh.w[second], lane.at0, lane.at1, w);
         float ss = 0.f, dot = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -271,7 +301,7 @@ __global__ void __launch_bounds__(THREADS, 2)
         }
         const float r = __frsqrt_rn(row_sum<L::PER_ROW>(ss) * (1.f / D) + a.eps);
         const float mean = row_sum<L::PER_ROW>(dot) * r * (1.f / D);
-        if (mine) {
+        if (h + k < u.n) {
 #pragma unroll
           for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -280,10 +310,22 @@ __global__ void __launch_bounds__(THREADS, 2)
               dw[m][i] = fmaf(g[m][i], n, dw[m][i]);
               v[m][i] = r * (g[m][i] * w[m][i] - n * mean);
             }
-          store8(out + (h + k * stride) * z.ys[1] + lane.at0, v[0]);
-          store8(out + (h + k * stride) * z.ys[1] + lane.at1, v[1]);
+          store8(out + (h + k) * ys + lane.at0, v[0]);
+          store8(out + (h + k) * ys + lane.at1, v[1]);
         }
       }
+    };
+    const int most = __reduce_max_sync(0xffffffffu, u.n);
+    Raw<T> even[U][4], odd[U][4];
+    const int pos = position(a, u);
+    load(even, 0);
+    turns(a, sh.step + 8 * lane.u, pos, lane.turns, cs);
+    for (int h = 0; h < most; h += 2 * U) {
+      load(odd, h + U);
+      rows(even, h);
+      if (h + U >= most) break;
+      load(even, h + 2 * U);
+      rows(odd, h + U);
     }
   }
   // the groups of a warp, then the warps
@@ -346,50 +388,55 @@ Freqs freqs_of(const RopeArgs& a) {
   return f;
 }
 
-template <typename T, int D, bool NORM>
-cudaError_t run(const RopeArgs& a, cudaStream_t st) {
-  const long long n = (long long)a.n_batch * a.seq_len;
-  // Tokens of a block: as many as give every thread one cosine and sine (4 at 64 pairs), fewer while that
-  // leaves SMs without a block.
-  int tok = D == 128 ? 4 : 8;
-  const int sms = sm_count();
-  while (tok > 1 && (n + tok - 1) / tok < 2LL * sms) tok >>= 1;
-  const auto kern = a.interleaved ? rope_kernel<T, D, NORM, true> : rope_kernel<T, D, NORM, false>;
-  count_launches(1);
-  return launch_with_pdl(kern, dim3((unsigned)((n + tok - 1) / tok)), dim3(THREADS), 0, st, a, freqs_of(a), tok, n);
+// Heads of a unit, for `slots` lane groups at once: all of them when there are units enough to even out, else
+// fewer, down to the rows of two steps, as long as that gives every group more than one.
+Split split_of(const RopeArgs& a, int slots, int step) {
+  Split s{};
+  s.n_tokens = (uint32_t)a.n_batch * (uint32_t)a.seq_len;
+  const int most = a.n_tensors > 1 && a.t[1].heads > a.t[0].heads ? a.t[1].heads : a.t[0].heads;
+  int parts = 1;
+  while ((most + parts - 1) / parts > step && (unsigned long long)s.n_tokens * parts < 3ULL * slots) parts <<= 1;
+  s.chunk = (most + parts - 1) / parts;
+  for (int j = 0; j < a.n_tensors; ++j) s.units[j] = s.n_tokens * (uint32_t)((a.t[j].heads + s.chunk - 1) / s.chunk);
+  return s;
 }
 
-constexpr int BACK_BLOCKS = 2;                              // per SM
+template <typename T, int D, bool NORM>
+cudaError_t run(const RopeArgs& a, cudaStream_t st) {
+  const int groups = THREADS / (D / 16), most = FORWARD_BLOCKS * sm_count();
+  const Split split = split_of(a, most * groups, sizeof(T) == 2 ? 8 : 4);
+  const long long blocks = ((long long)split.units[0] + split.units[1] + groups - 1) / groups;
+  const auto kern = a.interleaved ? rope_kernel<T, D, NORM, true> : rope_kernel<T, D, NORM, false>;
+  count_launches(1);
+  return launch_with_pdl(kern, dim3((unsigned)(blocks < most ? blocks : most)), dim3(THREADS), 0, st, a, freqs_of(a), split);
+}
 
 // Blocks of the gradient kernel, and the first of the second tensor's: shared out by heads.
-void back_blocks(const RopeArgs& a, int D, int* blocks, int* split, int* tok) {
-  const long long n = (long long)a.n_batch * a.seq_len;
-  const int sms = sm_count(), groups = THREADS / (D / 16), all = a.t[0].heads + a.t[1].heads;
+Split back_split(const RopeArgs& a, int D, int* blocks, int* split_at) {
+  const int groups = THREADS / (D / 16), most = BACK_BLOCKS * sm_count();
+  const Split s = split_of(a, most * groups, 4);
   int b[2];
   for (int j = 0; j < 2; ++j) {
-    tok[j] = 1;
-    // tokens until every group has two rows
-    while (tok[j] < MAX_TOK && tok[j] < groups && tok[j] * a.t[j].heads < 2 * groups) tok[j] <<= 1;
-    const long long most = (n + tok[j] - 1) / tok[j];
-    b[j] = (int)(((long long)BACK_BLOCKS * sms * a.t[j].heads + all - 1) / all);
-    if (b[j] > most) b[j] = (int)most;
+    const long long need = ((long long)s.units[j] + groups - 1) / groups;
+    const long long share = ((long long)most * a.t[j].heads) / (a.t[0].heads + a.t[1].heads);
+    b[j] = (int)(need < share ? need : share > 0 ? share : 1);
   }
-  *split = b[0];
+  *split_at = b[0];
   *blocks = b[0] + b[1];
+  return s;
 }
 
 template <typename T, int D>
 cudaError_t run_backward(const RopeArgs& a, float* dw0, float* dw1, void* ws, cudaStream_t st) {
-  int blocks, split, tok[2];
-  back_blocks(a, D, &blocks, &split, tok);
+  int blocks, split_at;
+  const Split split = back_split(a, D, &blocks, &split_at);
   const auto kern = a.interleaved ? norm_rope_backward_kernel<T, D, true> : norm_rope_backward_kernel<T, D, false>;
-  const long long n = (long long)a.n_batch * a.seq_len;
   count_launches(1);
-  const cudaError_t e = launch_with_pdl(kern, dim3((unsigned)blocks), dim3(THREADS), 0, st, a, freqs_of(a), n, split,
-                                        tok[0], tok[1], (float*)ws);
+  const cudaError_t e = launch_with_pdl(kern, dim3((unsigned)blocks), dim3(THREADS), 0, st, a, freqs_of(a), split, split_at,
+                                        (float*)ws);
   if (e != cudaSuccess || (!dw0 && !dw1)) return e;
   count_launches(1);
-  return launch_with_pdl(rope_weight_kernel<D>, dim3(D / 8, 2), dim3(THREADS), 0, st, (const float*)ws, split, blocks,
+  return launch_with_pdl(rope_weight_kernel<D>, dim3(D / 8, 2), dim3(THREADS), 0, st, (const float*)ws, split_at, blocks,
                          dw0, dw1);
 }
 
@@ -411,8 +458,8 @@ cudaError_t launch_rope(const RopeArgs& a, int dtype, int head_dim, int norm, cu
 }
 
 size_t norm_rope_backward_workspace(const RopeArgs& a, int head_dim) {
-  int blocks, split, tok[2];
-  back_blocks(a, head_dim, &blocks, &split, tok);
+  int blocks, split_at;
+  back_split(a, head_dim, &blocks, &split_at);
   return (size_t)blocks * head_dim * sizeof(float);
 }
 

@@ -8,6 +8,7 @@ they are not recorded by autograd.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 import torch
@@ -112,30 +113,42 @@ def _there(device, stream):
     return torch.cuda.stream(stream)
 
 
+_Strides = ctypes.c_int64 * 3
+
+
 def _rows(t, name, like=None, heads=None):
     """[B, H, S, D] or [H, S, D] with a contiguous last axis: (the 4-dim view, strides or None)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() == 3:
+    n = t.dim()
+    if n == 3:
         t = t.unsqueeze(0)
-    if t.dim() != 4:
+    elif n != 4:
         raise ValueError(f"{name} must be [B, H, S, D] or [H, S, D]")
     if like is not None:
-        if t.device != like.device:
+        if t.get_device() != like.get_device():
             raise ValueError(f"{name} must be on {like.device}, got {t.device}")
         if t.dtype != like.dtype:
             raise ValueError(f"{name} must be {like.dtype}, got {t.dtype}")
-        shape = (like.shape[0], like.shape[1] if heads is None else heads, like.shape[2], like.shape[3])
+        shape = like.shape if heads is None else (like.shape[0], heads, like.shape[2], like.shape[3])
         if t.shape != shape:
-            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.is_contiguous():
         return t, None
-    s = t.stride()
-    if s[3] != 1:
+    b, h, s, d = t.stride()
+    if d != 1:
         raise ValueError(f"{name}: the head_dim axis must be contiguous")
-    return t, (ctypes.c_int64 * 3)(s[0], s[1], s[2])
+    return t, _Strides(b, h, s)
+
+
+def _result(out, name, x, x4, heads=None):
+    """The tensor to return and its rows: `out`, or a new dense tensor like x."""
+    if out is None:
+        return torch.empty(x.shape, dtype=x.dtype, device=x.device), None
+    out4, strides = _rows(out, name, x4, heads)
+    return out4, strides
 
 
 def _positions(positions, like):
@@ -144,8 +157,8 @@ def _positions(positions, like):
         return None, 0
     if not isinstance(positions, torch.Tensor):
         raise TypeError("positions must be a torch.Tensor")
-    B, S = like.shape[0], like.shape[2]
-    if positions.device != like.device:
+    B, _, S, _ = like.shape
+    if positions.get_device() != like.get_device():
         raise ValueError(f"positions must be on {like.device}, got {positions.device}")
     if positions.dtype != torch.int32:
         raise ValueError(f"positions must be torch.int32, got {positions.dtype}")
@@ -174,31 +187,34 @@ def kvp_rope(x, rope, positions=None, start=0, inverse=False, out=None, stream=N
             return kvp_rope(x, rope, positions, start, inverse, out)
     if rope is None:
         raise TypeError("rope must be a Rope")
-    if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    out4, os = _rows(out, "out", x4)
+    out4, os = _result(out, "out", x, x4)
     pos, ps = _positions(positions, x4)
     B, H, S, D = x4.shape
     rc = load().kvp_rope(x4.data_ptr(), out4.data_ptr(), _dtype(x4), B, H, S, D, xs, os, _rope_ref(rope), pos, ps,
-                         int(start), int(bool(inverse)), _raw_stream(x4.device.index))
-    _check("kvp_rope", rc)
-    return out
+                         int(start), int(bool(inverse)), _raw_stream(x4.get_device()))
+    if rc:
+        _check("kvp_rope", rc)
+    return out4 if out is None else out
+
+
+def _weight(w, name, q4):
+    if w is None:
+        return None
+    _need(w, name, None, q4.shape[3:])
+    if w.get_device() != q4.get_device():
+        raise ValueError(f"{name} must be on {q4.device}, got {w.device}")
+    if w.dtype != q4.dtype and w.dtype != torch.float32:
+        raise ValueError(f"{name} must be {q4.dtype} or torch.float32, got {w.dtype}")
+    return w.data_ptr()
 
 
 def _weights(q_weight, k_weight, q4):
-    D, dtype = q4.shape[3], q4.dtype
-    given = [(n, w) for n, w in (("q_weight", q_weight), ("k_weight", k_weight)) if w is not None]
-    for name, w in given:
-        _need(w, name, None, (D,))
-        if w.device != q4.device:
-            raise ValueError(f"{name} must be on {q4.device}, got {w.device}")
-        if w.dtype not in (q4.dtype, torch.float32):
-            raise ValueError(f"{name} must be {q4.dtype} or torch.float32, got {w.dtype}")
-        if w.dtype != given[0][1].dtype:
-            raise ValueError("q_weight and k_weight must have the same dtype")
-        dtype = w.dtype
-    return (None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(),
-            _DTYPE[dtype])
+    q, k = _weight(q_weight, "q_weight", q4), _weight(k_weight, "k_weight", q4)
+    if q is None:
+        return q, k, _DTYPE[q4.dtype if k is None else k_weight.dtype]
+    if k is not None and k_weight.dtype != q_weight.dtype:
+        raise ValueError("q_weight and k_weight must have the same dtype")
+    return q, k, _DTYPE[q_weight.dtype]
 
 
 def kvp_qk_norm_rope(q, k, q_weight=None, k_weight=None, eps=1e-6, rope=None, positions=None, start=0, q_out=None,
@@ -214,19 +230,22 @@ def kvp_qk_norm_rope(q, k, q_weight=None, k_weight=None, eps=1e-6, rope=None, po
     B, Hq, S, D = q4.shape
     Hkv = k.shape[-3] if isinstance(k, torch.Tensor) and k.dim() >= 3 else 0
     k4, ks = _rows(k, "k", q4, Hkv)
-    if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if k_out is None:
-        k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device)
-    qo4, qos = _rows(q_out, "q_out", q4)
-    ko4, kos = _rows(k_out, "k_out", k4)
+    qo4, qos = _result(q_out, "q_out", q, q4)
+    ko4, kos = _result(k_out, "k_out", k, k4)
     pos, ps = _positions(positions, q4)
     qw, kw, wd = _weights(q_weight, k_weight, q4)
     rc = load().kvp_qk_norm_rope(q4.data_ptr(), k4.data_ptr(), qo4.data_ptr(), ko4.data_ptr(), dtype, B, Hq, Hkv, S, D,
                                  qs, ks, qos, kos, qw, kw, wd, float(eps), _rope_ref(rope), pos, ps, int(start),
-                                 _raw_stream(q4.device.index))
-    _check("kvp_qk_norm_rope", rc)
-    return q_out, k_out
+                                 _raw_stream(q4.get_device()))
+    if rc:
+        _check("kvp_qk_norm_rope", rc)
+    return qo4 if q_out is None else q_out, ko4 if k_out is None else k_out
+
+
+@functools.lru_cache(maxsize=256)
+def _backward_bytes(device, *sizes):
+    """(The sizes alone decide, on a device: the current one.)"""
+    return int(load().kvp_qk_norm_rope_backward_workspace_size(*sizes))
 
 
 def kvp_qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight=None, k_weight=None, eps=1e-6, rope=None, positions=None,
@@ -245,26 +264,22 @@ def kvp_qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight=None, k_weight=None
     k4, ks = _rows(k, "k", q4, Hkv)
     gq4, gqs = _rows(dq_out, "dq_out", q4)
     gk4, gks = _rows(dk_out, "dk_out", k4)
-    if dq is None:
-        dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if dk is None:
-        dk = torch.empty(k.shape, dtype=q.dtype, device=q.device)
-    dq4, dqs = _rows(dq, "dq", q4)
-    dk4, dks = _rows(dk, "dk", k4)
+    dq4, dqs = _result(dq, "dq", q, q4)
+    dk4, dks = _result(dk, "dk", k, k4)
     pos, ps = _positions(positions, q4)
     qw, kw, wd = _weights(q_weight, k_weight, q4)
-    dw = torch.empty(2, D, dtype=torch.float32, device=q4.device)
+    dwq, dwk = torch.empty(2, D, dtype=torch.float32, device=q4.device).unbind()
     if workspace is None:
-        need = int(load().kvp_qk_norm_rope_backward_workspace_size(dtype, B, Hq, Hkv, S, D))
-        workspace = torch.empty(need, dtype=torch.uint8, device=q4.device)
+        workspace = torch.empty(_backward_bytes(q4.get_device(), dtype, B, Hq, Hkv, S, D), dtype=torch.uint8, device=q4.device)
     else:
         _need(workspace, "workspace", torch.uint8)
         if workspace.device != q4.device:
             raise ValueError(f"workspace must be on {q4.device}, got {workspace.device}")
     rc = load().kvp_qk_norm_rope_backward(gq4.data_ptr(), gk4.data_ptr(), q4.data_ptr(), k4.data_ptr(), dq4.data_ptr(),
-                                          dk4.data_ptr(), dw.data_ptr(), dw.data_ptr() + 4 * D, dtype, B, Hq, Hkv, S, D,
+                                          dk4.data_ptr(), dwq.data_ptr(), dwk.data_ptr(), dtype, B, Hq, Hkv, S, D,
                                           gqs, gks, qs, ks, dqs, dks, qw, kw, wd, float(eps), _rope_ref(rope), pos, ps,
                                           int(start), workspace.data_ptr(), workspace.numel(),
-                                          _raw_stream(q4.device.index))
-    _check("kvp_qk_norm_rope_backward", rc)
-    return dq, dk, dw[0], dw[1]
+                                          _raw_stream(q4.get_device()))
+    if rc:
+        _check("kvp_qk_norm_rope_backward", rc)
+    return dq4 if dq is None else dq, dk4 if dk is None else dk, dwq, dwk
