@@ -300,6 +300,7 @@ __global__ void __launch_bounds__(F_THREADS) prefix_f32_kernel(const Params p) {
   float *ms = sm + C::OFF_M, *ls = ms + F_QT, *fs = ls + F_QT;
   const int tid = threadIdx.x, cta = blockIdx.x;
   wait_prior_grid();
+  allow_next_grid();
   prefix::Walk<true> walk(p, cta);
   Piece a;
   while (walk.step(p, a)) {
@@ -432,32 +433,35 @@ __global__ void __launch_bounds__(JOIN_THREADS) prefix_join_kernel(const Params 
   constexpr int LANES = D / 4;                 // of a part
   constexpr int AT_ONCE = 32 / LANES;          // parts a warp reads at once
   __shared__ float4 sum_sh[JOIN_THREADS / 32][LANES];
-  wait_prior_grid();
+  // The plan may be read before the parts are there: the kernel before this one has let it go once the plan
+  // was made.
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % warps;
   const long long query = (long long)blockIdx.x * (JOIN_THREADS / 32 / warps) + warp / warps;
   const bool live = query < (long long)p.c.R * p.G;
   const int r = live ? (int)(query / p.G) : 0, g = live ? (int)(query % p.G) : 0;
   const int l = r / p.Hkv, h = r % p.Hkv;
-  const prefix::Head head = *p.head;
   // the parts: [0, n0) of the prefix, then [0, n1) of the row's own tokens, from CTA lo on
   int n0 = 0, n1 = 0, lo0 = 0, lo1 = 0, local = 0;
   if (live) {
-    const int place = p.place[r], root = p.root[l], own = p.own_item[r];
+    const int4 head = __ldcg((const int4*)p.head);
+    const int place = __ldcg(p.place + r), root = __ldcg(p.root + l), own = __ldcg(p.own_item + r);
     int pre = -1;
     if (place >= 0) {
       const int x = place * p.G + g;
-      pre = p.pre_item[root * p.Hkv + h] + x / p.qt;
+      pre = __ldcg(p.pre_item + root * p.Hkv + h) + x / p.qt;
       local = x % p.qt;
     }
     const auto span = [&](int item, int& lo) {
-      const Item it = p.items[item];
-      const int last = it.tile0 + (prefix::tiles_of(it.tok1 - it.tok0) - 1) * it.width;
-      lo = paged::cta_of(it.tile0, head.total, head.active);
-      return paged::cta_of(last, head.total, head.active) - lo + 1;
+      const int4 a = __ldcg((const int4*)(p.items + item)), b = __ldcg((const int4*)(p.items + item) + 1);
+      // (tile0, row, tok0, tok1), (q0, nq, list, width); (places, CTAs, ...)
+      const int last = a.x + (prefix::tiles_of(a.w - a.z) - 1) * b.w;
+      lo = paged::cta_of(a.x, head.x, head.y);
+      return paged::cta_of(last, head.x, head.y) - lo + 1;
     };
     if (pre >= 0) n0 = span(pre, lo0);
     if (own >= 0) n1 = span(own, lo1);
   }
+  wait_prior_grid();
   const int all = n0 + n1;
   // where part i lies: in the pieces that begin an item, or in those that go on
   const auto at = [&](int i, bool& first) {

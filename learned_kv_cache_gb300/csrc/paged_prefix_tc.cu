@@ -285,7 +285,6 @@ __global__ void __launch_bounds__(X_THREADS, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = uniform(flags[1]);
-  allow_next_grid();                     // (the join's blocks come as SMs fall free)
 
   // a warp goes on, or gives up, as a whole
   const auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -297,6 +296,7 @@ __global__ void __launch_bounds__(X_THREADS, 1)
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     wait_prior_grid();
+    allow_next_grid();                   // (the join comes as SMs fall free, and may read the plan: it is done)
     prefix::Walk<true> walk(p, cta);
     Piece a;
     if (warp == 0) {
