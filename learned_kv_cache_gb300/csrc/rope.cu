@@ -13,9 +13,12 @@
 //    the whole turns: exact up to 2^-64 of a turn per position, for every 32-bit position.  Its upper 32
 //    bits, less the nearest quarter turn, are exact to 2^-25 of an eighth of a turn as a float.
 //  * The unit of work is a token with some of a tensor's heads, and D / 16 lanes have one: they compute its
-//    cosines and sines (8 pairs a lane, while the first rows are on their way) and walk over the heads, the
-//    next rows' loads always ahead of the arithmetic.  Nothing is shared, so no warp waits for another (with
-//    the angles in shared memory and a few tokens a block, 8192 tokens of 32 + 8 heads took 52 us).
+//    cosines and sines (8 pairs a lane) and walk over the heads.  Nothing is shared between lanes but sums
+//    over a row, so no warp waits for another (with the angles in shared memory and a few tokens a block,
+//    8192 tokens of 32 + 8 heads took 52 us).
+//  * What keeps HBM busy is bytes on their way: every lane has a ring of its own in shared memory, into which
+//    it copies rows (cp.async) some steps before it uses them, beyond the end of a unit.  As many in
+//    registers would spill, or leave an SM too few warps (gradients of those tokens: 58 us).
 //  * A lane owns 8 pairs of a row: two vectors of 8 values that lie rotary_dim / 2 apart (halves) or side
 //    by side (interleaved), so pairs never cross lanes and sums over a row are 2 or 3 shuffles.
 //  * Lane groups side by side have tokens side by side: in a tensor laid out by heads their rows touch.
@@ -29,13 +32,27 @@ namespace {
 
 constexpr int THREADS = 256;
 constexpr int MAX_PAIRS = 64;
-constexpr int FORWARD_BLOCKS = 2, BACK_BLOCKS = 1;          // per SM
+constexpr int FORWARD_BLOCKS = 2, BACK_BLOCKS = 2;          // per SM
 
 struct Freqs {
   uint64_t step[MAX_PAIRS];   // turns per position, times 2^64
 };
 
-// Eight consecutive values as they lie in memory.
+// Eight values as four pairs, from memory and back.
+template <typename T>
+__device__ __forceinline__ void unpack8(const uint4 (&x)[sizeof(T) / 2], uint64_t* v) {
+  if constexpr (sizeof(T) == 4) {
+    v[0] = (uint64_t)x[0].y << 32 | x[0].x;
+    v[1] = (uint64_t)x[0].w << 32 | x[0].z;
+    v[2] = (uint64_t)x[1].y << 32 | x[1].x;
+    v[3] = (uint64_t)x[1].w << 32 | x[1].z;
+  } else {
+    float f[8];
+    Vec16<T>::unpack(x[0], f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = pack2(f[2 * i], f[2 * i + 1]);
+  }
+}
 template <typename T>
 struct Raw {
   uint4 v[sizeof(T) / 2];
@@ -43,41 +60,46 @@ struct Raw {
 #pragma unroll
     for (int i = 0; i < (int)(sizeof(T) / 2); ++i) v[i] = reinterpret_cast<const uint4*>(p)[i];
   }
-  __device__ __forceinline__ void get(float* f) const {
-#pragma unroll
-    for (int i = 0; i < (int)(sizeof(T) / 2); ++i) Vec16<T>::unpack(v[i], f + i * Vec16<T>::N);
-  }
+  __device__ __forceinline__ void get(uint64_t* f) const { unpack8<T>(v, f); }
 };
-__device__ __forceinline__ void store8(float* p, const float* f) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+__device__ __forceinline__ void store8(float* p, const uint64_t* v) {
+  reinterpret_cast<ulonglong2*>(p)[0] = make_ulonglong2(v[0], v[1]);
+  reinterpret_cast<ulonglong2*>(p)[1] = make_ulonglong2(v[2], v[3]);
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* f) {
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const uint64_t* v) {
   __nv_bfloat162 h[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    unpack2(v[i], a, b);
+    h[i] = __floats2bfloat162_rn(a, b);
+  }
   *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(h);
 }
-__device__ __forceinline__ void store8(__half* p, const float* f) {
+__device__ __forceinline__ void store8(__half* p, const uint64_t* v) {
   __half2 h[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    unpack2(v[i], a, b);
+    h[i] = __floats2half2_rn(a, b);
+  }
   *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(h);
 }
 
-// Cosine and sine of pos * step turns.
+// Cosine and sine of pos * step turns.  Within an eighth of a turn of the nearest quarter the Taylor series
+// up to t^10 leave 3e-10 (t^11 / 11! at pi / 4); no branches, as the quarters differ from lane to lane (the
+// library's function and a switch took 3 times the instructions, half of all).
 __device__ __forceinline__ float2 turn_of(int pos, uint64_t step) {
   const uint32_t t = (uint32_t)(((uint64_t)(int64_t)pos * step) >> 32);
   const uint32_t quarter = (t + 0x20000000u) >> 30;
-  const int rest = (int)(t - (quarter << 30));              // within an eighth of a turn of it
-  float s, c;
-  sincospif((float)rest * 0x1p-31f, &s, &c);
-  switch (quarter & 3) {
-    case 0: return make_float2(c, s);
-    case 1: return make_float2(-s, c);
-    case 2: return make_float2(-c, -s);
-    default: return make_float2(s, -c);
-  }
+  const float x = (float)(int)(t - (quarter << 30)) * (6.283185307179586f * 0x1p-32f), xx = x * x;
+  const float c = fmaf(xx, fmaf(xx, fmaf(xx, fmaf(xx, fmaf(xx, -1.f / 3628800.f, 1.f / 40320.f), -1.f / 720.f), 1.f / 24.f), -0.5f), 1.f);
+  const float s = fmaf(x * xx, fmaf(xx, fmaf(xx, fmaf(xx, 1.f / 362880.f, -1.f / 5040.f), 1.f / 120.f), -1.f / 6.f), x);
+  // a quarter turn on: (c, s) -> (-s, c)
+  const float a = quarter & 1 ? s : c, b = quarter & 1 ? c : s;
+  return make_float2(__uint_as_float(__float_as_uint(a) ^ ((quarter + 1) << 30 & 0x80000000u)),
+                     __uint_as_float(__float_as_uint(b) ^ (quarter << 30 & 0x80000000u)));
 }
 
 // The lane's place in a row.
@@ -101,16 +123,49 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
-// The pairs (a, b) of a lane turned by cs.  dir = 1: by the angle; -1: back.
-template <bool INTERLEAVED>
-__device__ __forceinline__ void turn(float (&x)[2][8], const float2 (&cs)[8], float dir) {
+// Cosines and sines (times gain) of the lane's eight pairs, two to a register pair.
+struct Turns {
+  uint64_t c[4], s[4], minus[4];         // (minus the sines: packed arithmetic has no signs)
+  template <bool INTERLEAVED>
+  __device__ __forceinline__ void fill(const RopeArgs& a, const uint64_t* step, int pos, bool rotates) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float& a = INTERLEAVED ? x[i >> 2][2 * (i & 3)] : x[0][i];
-    float& b = INTERLEAVED ? x[i >> 2][2 * (i & 3) + 1] : x[1][i];
-    const float c = cs[i].x, s = cs[i].y * dir, y = a * c - b * s;
-    b = b * c + a * s;
-    a = y;
+    for (int i = 0; i < 4; ++i) {
+      float2 x = make_float2(1.f, 0.f), y = x;
+      if (rotates) {
+        const float up = a.inverse ? -a.gain : a.gain;
+        x = turn_of(pos, step[2 * i]);
+        y = turn_of(pos, step[2 * i + 1]);
+        x.x *= a.gain;
+        y.x *= a.gain;
+        x.y *= up;
+        y.y *= up;
+      }
+      c[i] = pack2(x.x, y.x);
+      s[i] = pack2(x.y, y.y);
+      if (!INTERLEAVED) minus[i] = pack2(-x.y, -y.y);
+    }
+  }
+};
+// The pairs (a, b) of a lane turned, or turned back.
+template <bool INTERLEAVED>
+__device__ __forceinline__ void turn(uint64_t (&v)[8], const Turns& t, bool back) {
+  if constexpr (INTERLEAVED) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float c[2], s[2], a, b;
+      unpack2(t.c[i >> 1], c[0], c[1]);
+      unpack2(t.s[i >> 1], s[0], s[1]);
+      unpack2(v[i], a, b);
+      const float ci = c[i & 1], si = back ? -s[i & 1] : s[i & 1];
+      v[i] = pack2(a * ci - b * si, b * ci + a * si);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t a = v[i], b = v[4 + i], s = back ? t.minus[i] : t.s[i], minus = back ? t.s[i] : t.minus[i];
+      v[i] = ffma2(b, minus, fmul2(a, t.c[i]));
+      v[4 + i] = ffma2(a, s, fmul2(b, t.c[i]));
+    }
   }
 }
 
@@ -150,35 +205,111 @@ __device__ __forceinline__ void fill_tables(Tables<D>& sh, const RopeArgs& a, co
   }
   __syncthreads();
 }
-__device__ __forceinline__ int position(const RopeArgs& a, const Unit& u) {
-  return a.positions ? a.positions[u.b * a.position_stride + u.s] : a.start + u.s;
+__device__ __forceinline__ void copy16(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
 }
-// Cosines and sines (times gain) of the lane's pairs.
-__device__ __forceinline__ void turns(const RopeArgs& a, const uint64_t* step, int pos, bool rotates, float2 (&cs)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float2 v = make_float2(1.f, 0.f);
-    if (rotates) {
-      v = turn_of(pos, step[i]);
-      v.x *= a.gain;
-      v.y *= a.inverse ? -a.gain : a.gain;
+__device__ __forceinline__ void copy4(void* to, const void* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
+}
+
+// The rows of a warp's units, one step of every lane group after the other, copied STEPS - 1 steps ahead.
+// SOURCES: x, or x and dy.
+template <typename T, int D, int SOURCES>
+struct Rows {
+  static constexpr int PARTS = 16 * sizeof(T) / 16;        // 16-byte parts of a lane's 16 values
+  static constexpr int STEPS = (SOURCES == 1 ? 48 : 64) / (4 * PARTS * SOURCES) < 3 ? 3 : (SOURCES == 1 ? 48 : 64) / (4 * PARTS * SOURCES);
+  static constexpr int SMEM = STEPS * (PARTS * SOURCES * 16 + 4) * THREADS;
+  // [step][part][thread], then the tokens' positions
+  uint4* ring;
+  int* ring_pos;
+  const RopeArgs& a;
+  const Split& split;
+  int at0, at1;
+  uint32_t u0, stride, all, begin;   // the warp's first unit, from step to step, the last; the lane's within the warp
+  int tensor;                        // units of one tensor only, or -1
+  // the unit that is being copied
+  int h, most, n, slot;
+  const T* src[SOURCES];
+  int64_t hs[SOURCES];
+  const int32_t* pos;
+
+  __device__ __forceinline__ Rows(const RopeArgs& a_, const Split& split_, uint4* smem, int at0_, int at1_)
+      : a(a_), split(split_), at0(at0_), at1(at1_) {
+    ring = smem + threadIdx.x;
+    ring_pos = reinterpret_cast<int*>(smem + STEPS * PARTS * SOURCES * THREADS) + threadIdx.x;
+  }
+  // This lane's unit of the warp's step u, and the tensor's number.
+  __device__ __forceinline__ Unit unit(uint32_t u, int& j) const {
+    const uint32_t id = u + begin;
+    j = tensor >= 0 ? tensor : id >= split.units[0];
+    return Unit(a, split, j ? a.t[1].heads : a.t[0].heads, tensor < 0 && j ? id - split.units[0] : id, id < all);
+  }
+  __device__ __forceinline__ void enter() {
+    int j;
+    const Unit x = unit(u0, j);
+    const RopeTensor& z = j ? a.t[1] : a.t[0];
+    hs[0] = z.xs[1];
+    src[0] = (const T*)z.x + x.b * z.xs[0] + x.s * z.xs[2] + x.h0 * hs[0];
+    if (SOURCES == 2) {
+      hs[SOURCES - 1] = z.dys[1];
+      src[SOURCES - 1] = (const T*)z.dy + x.b * z.dys[0] + x.s * z.dys[2] + x.h0 * hs[SOURCES - 1];
     }
-    cs[i] = v;
+    pos = a.positions ? a.positions + x.b * a.position_stride + x.s : nullptr;
+    n = x.n;
+    most = __reduce_max_sync(0xffffffffu, n);
+    h = 0;
   }
-}
-__device__ __forceinline__ void load_w(const float* w, int at0, int at1, float (&out)[2][8]) {
+  // Copies the next step's rows.
+  __device__ __forceinline__ void copy() {
+    if (u0 < all) {
+      if (h < n) {
 #pragma unroll
-  for (int i = 0; i < 8; i += 4) {
-    *reinterpret_cast<float4*>(&out[0][i]) = *reinterpret_cast<const float4*>(w + at0 + i);
-    *reinterpret_cast<float4*>(&out[1][i]) = *reinterpret_cast<const float4*>(w + at1 + i);
+        for (int k = 0; k < SOURCES; ++k)
+#pragma unroll
+          for (int i = 0; i < PARTS; ++i)
+            copy16(ring + ((slot * SOURCES + k) * PARTS + i) * THREADS,
+                   src[k] + (i < PARTS / 2 ? at0 + i * (8 / (PARTS / 2)) : at1 + (i - PARTS / 2) * (8 / (PARTS / 2))));
+        if (h == 0 && pos) copy4(ring_pos + slot * THREADS, pos);
+#pragma unroll
+        for (int k = 0; k < SOURCES; ++k) src[k] += hs[k];
+      }
+      if (++h == most) {
+        u0 += stride;
+        if (u0 < all) enter();
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    slot = slot + 1 == STEPS ? 0 : slot + 1;
   }
-}
+  __device__ __forceinline__ void start(uint32_t first, uint32_t stride_, uint32_t all_, uint32_t begin_, int tensor_) {
+    u0 = first;
+    stride = stride_;
+    all = all_;
+    begin = begin_;
+    tensor = tensor_;
+    slot = 0;
+    if (u0 < all) enter();
+#pragma unroll 1
+    for (int i = 0; i < STEPS - 1; ++i) copy();
+  }
+  __device__ __forceinline__ void landed() { asm volatile("cp.async.wait_group %0;" ::"n"(STEPS - 2) : "memory"); }
+  // The 16 values of source k in the ring's place s.
+  __device__ __forceinline__ void get(int s, int k, uint64_t (&v)[8]) const {
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      uint4 x[PARTS / 2];
+#pragma unroll
+      for (int i = 0; i < PARTS / 2; ++i) x[i] = ring[((s * SOURCES + k) * PARTS + m * (PARTS / 2) + i) * THREADS];
+      unpack8<T>(x, v + 4 * m);
+    }
+  }
+};
 
 template <typename T, int D, bool NORM, bool INTERLEAVED>
 __global__ void __launch_bounds__(THREADS, FORWARD_BLOCKS)
-    rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ Freqs f, const Split split) {
+    rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ Freqs f, const __grid_constant__ Split split) {
   using L = Lane<D, INTERLEAVED>;
-  // rows at a time: twice these in registers (four with norms spill: 457 us for 434)
+  // rows at a time: twice these in registers (four with norms spill: 457 us of 131072 tokens for 434)
   constexpr int U = sizeof(T) == 4 ? 2 : NORM ? 3 : 4;
   __shared__ __align__(16) Tables<D> sh;
   const L lane(a.rotary_dim);
@@ -201,39 +332,40 @@ __global__ void __launch_bounds__(THREADS, FORWARD_BLOCKS)
           raw[k][1].load(in + (h + k) * xs + lane.at1);
         }
     };
-    float2 cs[8];
+    Turns t;
     const auto rows = [&](const Raw<T> (&raw)[U][2], int h) {
 #pragma unroll
       for (int k = 0; k < U; ++k) {
-        float v[2][8];
-        raw[k][0].get(v[0]);
-        raw[k][1].get(v[1]);
+        uint64_t v[8];
+        raw[k][0].get(v);
+        raw[k][1].get(v + 4);
         if (NORM) {
-          float ss = 0.f;
+          uint64_t ss[2] = {0, 0};
 #pragma unroll
-          for (int i = 0; i < 8; ++i) ss = fmaf(v[0][i], v[0][i], fmaf(v[1][i], v[1][i], ss));
-          const float r = __frsqrt_rn(row_sum<L::PER_ROW>(ss) * (1.f / D) + a.eps);
-          float w[2][8];
-          load_w(sh.w[second], lane.at0, lane.at1, w);
+          for (int i = 0; i < 8; ++i) ss[i & 1] = ffma2(v[i], v[i], ss[i & 1]);
+          const float r = __frsqrt_rn(row_sum<L::PER_ROW>(sum2(fadd2(ss[0], ss[1]))) * (1.f / D) + a.eps);
+          const uint64_t r2 = pack2(r, r);
+          const float* w = sh.w[second];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            v[0][i] = v[0][i] * r * w[0][i];
-            v[1][i] = v[1][i] * r * w[1][i];
+          for (int i = 0; i < 8; i += 2) {
+            const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(w + (i < 4 ? lane.at0 : lane.at1 - 8) + 2 * i);
+            v[i] = fmul2(fmul2(v[i], r2), x.x);
+            v[i + 1] = fmul2(fmul2(v[i + 1], r2), x.y);
           }
         }
-        if (lane.turns) turn<INTERLEAVED>(v, cs, 1.f);
+        if (lane.turns) turn<INTERLEAVED>(v, t, false);
         if (h + k < u.n) {
-          store8(out + (h + k) * ys + lane.at0, v[0]);
-          store8(out + (h + k) * ys + lane.at1, v[1]);
+          store8(out + (h + k) * ys + lane.at0, v);
+          store8(out + (h + k) * ys + lane.at1, v + 4);
         }
       }
     };
     // every lane of the warp takes as many steps as any: sums over a row are the whole warp's shuffles
     const int most = __reduce_max_sync(0xffffffffu, u.n);
     Raw<T> even[U][2], odd[U][2];
-    const int pos = position(a, u);
+    const int pos = a.positions ? a.positions[u.b * a.position_stride + u.s] : a.start + u.s;
     load(even, 0);
-    turns(a, sh.step + 8 * lane.u, pos, lane.turns, cs);
+    t.fill<INTERLEAVED>(a, sh.step + 8 * lane.u, pos, lane.turns);
     for (int h = 0; h < most; h += 2 * U) {
       load(odd, h + U);
       rows(even, h);
@@ -249,94 +381,82 @@ __global__ void __launch_bounds__(THREADS, FORWARD_BLOCKS)
 // blocks' sums by rope_weight_kernel in a fixed order.
 template <typename T, int D, bool INTERLEAVED>
 __global__ void __launch_bounds__(THREADS, BACK_BLOCKS)
-    norm_rope_backward_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ Freqs f, const Split split,
-                              int split_at, float* __restrict__ part) {
+    norm_rope_backward_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ Freqs f,
+                              const __grid_constant__ Split split, int split_at, float* __restrict__ part) {
   using L = Lane<D, INTERLEAVED>;
-  constexpr int U = sizeof(T) == 2 ? 2 : 1;
+  using R = Rows<T, D, 2>;
+  extern __shared__ uint4 ring[];
   __shared__ __align__(16) Tables<D> sh;
   __shared__ float sum_sh[THREADS / 32][D];
   const L lane(a.rotary_dim);
   fill_tables<T, D, true>(sh, a, f);
-  const bool second = (int)blockIdx.x >= split_at;
-  const uint32_t block = second ? blockIdx.x - split_at : blockIdx.x, blocks = second ? gridDim.x - split_at : split_at;
-  const RopeTensor& z = second ? a.t[1] : a.t[0];
-  const uint32_t all = split.units[second];
-  float dw[2][8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) dw[0][i] = dw[1][i] = 0.f;
-  const uint32_t first = block * L::GROUPS + threadIdx.x / 32 * (32 / L::PER_ROW);
-  for (uint32_t u0 = first; u0 < all; u0 += blocks * L::GROUPS) {
-    const uint32_t id = u0 + (threadIdx.x & 31) / L::PER_ROW;
-    const Unit u(a, split, z.heads, id, id < all);
-    const int64_t xs = z.xs[1], ds = z.dys[1], ys = z.ys[1];
-    const T* in = (const T*)z.x + u.b * z.xs[0] + u.s * z.xs[2] + u.h0 * xs;
-    const T* dy = (const T*)z.dy + u.b * z.dys[0] + u.s * z.dys[2] + u.h0 * ds;
+  const int j = (int)blockIdx.x >= split_at;
+  const uint32_t block = j ? blockIdx.x - split_at : blockIdx.x, blocks = j ? gridDim.x - split_at : split_at;
+  const RopeTensor& z = j ? a.t[1] : a.t[0];
+  const uint32_t all = split.units[j], stride = blocks * L::GROUPS;
+  R rows(a, split, ring, lane.at0, lane.at1);
+  uint32_t u0 = block * L::GROUPS + threadIdx.x / 32 * (32 / L::PER_ROW);
+  rows.start(u0, stride, all, (threadIdx.x & 31) / L::PER_ROW, j);
+  uint64_t dw[8] = {};
+  int slot = 0;
+  for (; u0 < all; u0 += stride) {
+    int same;
+    const Unit u = rows.unit(u0, same);
+    const int64_t ys = z.ys[1];
     T* out = (T*)z.y + u.b * z.ys[0] + u.s * z.ys[2] + u.h0 * ys;
-    const auto load = [&](Raw<T> (&raw)[U][4], int h) {
+    // every lane of the warp takes as many steps as any: sums over a row are the whole warp's shuffles
+    const int most = __reduce_max_sync(0xffffffffu, u.n);
+    Turns t;
+    for (int h = 0; h < most; ++h) {
+      rows.landed();
+      if (h == 0)
+        t.fill<INTERLEAVED>(a, sh.step + 8 * lane.u, a.positions ? rows.ring_pos[slot * THREADS] : a.start + u.s, lane.turns);
+      uint64_t v[8], g[8], gw[8];
+      rows.get(slot, 0, v);
+      rows.get(slot, 1, g);
+      rows.copy();                     // into the place before this one
+      slot = slot + 1 == R::STEPS ? 0 : slot + 1;
+      if (lane.turns) turn<INTERLEAVED>(g, t, true);
+      const float* w = sh.w[j];
+      uint64_t ss[2] = {0, 0}, dot[2] = {0, 0};
 #pragma unroll
-      for (int k = 0; k < U; ++k)
-        if (h + k < u.n) {
-          raw[k][0].load(in + (h + k) * xs + lane.at0);
-          raw[k][1].load(in + (h + k) * xs + lane.at1);
-          raw[k][2].load(dy + (h + k) * ds + lane.at0);
-          raw[k][3].load(dy + (h + k) * ds + lane.at1);
-        }
-    };
-    float2 cs[8];
-    const auto rows = [&](const Raw<T> (&raw)[U][4], int h) {
-#pragma unroll
-      for (int k = 0; k < U; ++k) {
-        float v[2][8], g[2][8], w[2][8];
-        raw[k][0].get(v[0]);
-        raw[k][1].get(v[1]);
-        raw[k][2].get(g[0]);
-        raw[k][3].get(g[1]);
-        if (lane.turns) turn<INTERLEAVED>(g, cs, -1.f);
-        load_w(sh.w[second], lane.at0, lane.at1, w);
-        float ss = 0.f, dot = 0.f;
+      for (int i = 0; i < 8; i += 2) {
+        const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(w + (i < 4 ? lane.at0 : lane.at1 - 8) + 2 * i);
+        gw[i] = fmul2(g[i], x.x);
+        gw[i + 1] = fmul2(g[i + 1], x.y);
+        ss[0] = ffma2(v[i], v[i], ss[0]);
+        ss[1] = ffma2(v[i + 1], v[i + 1], ss[1]);
+        dot[0] = ffma2(gw[i], v[i], dot[0]);
+        dot[1] = ffma2(gw[i + 1], v[i + 1], dot[1]);
+      }
+      const float r = __frsqrt_rn(row_sum<L::PER_ROW>(sum2(fadd2(ss[0], ss[1]))) * (1.f / D) + a.eps);
+      const float mean = row_sum<L::PER_ROW>(sum2(fadd2(dot[0], dot[1]))) * r * (1.f / D);
+      if (h < u.n) {
+        const uint64_t r2 = pack2(r, r), m2 = pack2(-mean, -mean);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          ss = fmaf(v[0][i], v[0][i], fmaf(v[1][i], v[1][i], ss));
-          dot = fmaf(g[0][i] * w[0][i], v[0][i], fmaf(g[1][i] * w[1][i], v[1][i], dot));
+          const uint64_t n = fmul2(v[i], r2);
+          dw[i] = ffma2(g[i], n, dw[i]);
+          v[i] = fmul2(r2, ffma2(n, m2, gw[i]));
         }
-        const float r = __frsqrt_rn(row_sum<L::PER_ROW>(ss) * (1.f / D) + a.eps);
-        const float mean = row_sum<L::PER_ROW>(dot) * r * (1.f / D);
-        if (h + k < u.n) {
-#pragma unroll
-          for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float n = v[m][i] * r;
-              dw[m][i] = fmaf(g[m][i], n, dw[m][i]);
-              v[m][i] = r * (g[m][i] * w[m][i] - n * mean);
-            }
-          store8(out + (h + k) * ys + lane.at0, v[0]);
-          store8(out + (h + k) * ys + lane.at1, v[1]);
-        }
+        store8(out + lane.at0, v);
+        store8(out + lane.at1, v + 4);
+        out += ys;
       }
-    };
-    const int most = __reduce_max_sync(0xffffffffu, u.n);
-    Raw<T> even[U][4], odd[U][4];
-    const int pos = position(a, u);
-    load(even, 0);
-    turns(a, sh.step + 8 * lane.u, pos, lane.turns, cs);
-    for (int h = 0; h < most; h += 2 * U) {
-      load(odd, h + U);
-      rows(even, h);
-      if (h + U >= most) break;
-      load(even, h + 2 * U);
-      rows(odd, h + U);
     }
   }
   // the groups of a warp, then the warps
 #pragma unroll
-  for (int m = 0; m < 2; ++m)
+  for (int i = 0; i < 8; ++i) {
+    float x[2];
+    unpack2(dw[i], x[0], x[1]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int k = 0; k < 2; ++k) {
 #pragma unroll
-      for (int o = L::PER_ROW; o < 32; o <<= 1) dw[m][i] += __shfl_xor_sync(0xffffffffu, dw[m][i], o);
-      if ((threadIdx.x & 31) < L::PER_ROW) sum_sh[threadIdx.x >> 5][(m ? lane.at1 : lane.at0) + i] = dw[m][i];
+      for (int o = L::PER_ROW; o < 32; o <<= 1) x[k] += __shfl_xor_sync(0xffffffffu, x[k], o);
+      if ((threadIdx.x & 31) < L::PER_ROW) sum_sh[threadIdx.x >> 5][(i < 4 ? lane.at0 : lane.at1 - 8) + 2 * i + k] = x[k];
     }
+  }
   __syncthreads();
   if (threadIdx.x < D) {
     float sum = 0.f;
@@ -431,9 +551,11 @@ cudaError_t run_backward(const RopeArgs& a, float* dw0, float* dw1, void* ws, cu
   int blocks, split_at;
   const Split split = back_split(a, D, &blocks, &split_at);
   const auto kern = a.interleaved ? norm_rope_backward_kernel<T, D, true> : norm_rope_backward_kernel<T, D, false>;
+  constexpr int SMEM = Rows<T, D, 2>::SMEM;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  if (e != cudaSuccess) return e;
   count_launches(1);
-  const cudaError_t e = launch_with_pdl(kern, dim3((unsigned)blocks), dim3(THREADS), 0, st, a, freqs_of(a), split, split_at,
-                                        (float*)ws);
+  e = launch_with_pdl(kern, dim3((unsigned)blocks), dim3(THREADS), SMEM, st, a, freqs_of(a), split, split_at, (float*)ws);
   if (e != cudaSuccess || (!dw0 && !dw1)) return e;
   count_launches(1);
   return launch_with_pdl(rope_weight_kernel<D>, dim3(D / 8, 2), dim3(THREADS), 0, st, (const float*)ws, split_at, blocks,
