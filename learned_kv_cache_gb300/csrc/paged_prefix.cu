@@ -31,6 +31,32 @@ __device__ __forceinline__ int root_of(const Params& p, int l) {
   return y < 0 || y == x ? x : l;
 }
 
+// This thread's first page, of those from `i0` on, at which rows r and rf differ (or that is no page); each of
+// the `n` threads looks at U of them.
+constexpr int LOOK_U = 8;
+__device__ __forceinline__ int differ(const Params& p, int r, int rf, int i0, int most, int t, int n) {
+  const int32_t* a = p.c.table + (size_t)r * p.c.max_pages;
+  const int32_t* b = p.c.table + (size_t)rf * p.c.max_pages;
+  int x[LOOK_U], y[LOOK_U];
+#pragma unroll
+  for (int k = 0; k < LOOK_U; ++k) {
+    const int i = i0 + k * n + t;
+    x[k] = i < most ? a[i] : 0;
+    y[k] = i < most ? b[i] : 0;
+  }
+  int at = 0x7fffffff;
+#pragma unroll
+  for (int k = LOOK_U - 1; k >= 0; --k) {
+    const int i = i0 + k * n + t;
+    if (i < most && (x[k] != y[k] || x[k] < 0 || x[k] >= p.c.n_pages)) at = i;
+  }
+  return at;
+}
+__device__ __forceinline__ void check_row(const Params& p, int r) {
+  const int n = p.c.lens[r];
+  if (n < 0 || n > p.c.cap || p.lead[r / p.Hkv] >= p.N) raise_status(p.status, KVP_ERR_DEVICE_CHECK);
+}
+
 // Block r: how many leading tokens row r has on pages of its root's row (whole pages, that both rows have
 // filled).  The blocks of head 0 put their sequence into the families' order, by counting.
 __global__ void __launch_bounds__(LOOK_THREADS) prefix_look_kernel(const Params p) {
@@ -42,8 +68,7 @@ __global__ void __launch_bounds__(LOOK_THREADS) prefix_look_kernel(const Params 
   const int f = root_of(p, l);
   if (tid == 0) {
     mismatch = 0x7fffffff;
-    const int n = p.c.lens[r];
-    if (n < 0 || n > p.c.cap || p.lead[l] >= p.N) raise_status(p.status, KVP_ERR_DEVICE_CHECK);
+    check_row(p, r);
   }
   if (h == 0) {
     int before = 0, rank = 0, mine = 0;        // sequences of earlier families; of this one before l; of l's own
@@ -82,24 +107,8 @@ __global__ void __launch_bounds__(LOOK_THREADS) prefix_look_kernel(const Params 
   }
   const int rf = f * p.Hkv + h;
   const int most = min(prefix::row_len(p, r), prefix::row_len(p, rf)) >> p.c.shift;
-  const int32_t* a = p.c.table + (size_t)r * p.c.max_pages;
-  const int32_t* b = p.c.table + (size_t)rf * p.c.max_pages;
-  constexpr int U = 8;
-  for (int i0 = 0; i0 < most; i0 += U * LOOK_THREADS) {
-    int x[U], y[U];
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const int i = i0 + k * LOOK_THREADS + tid;
-      x[k] = i < most ? a[i] : 0;
-      y[k] = i < most ? b[i] : 0;
-    }
-    int at = 0x7fffffff;
-#pragma unroll
-    for (int k = U - 1; k >= 0; --k) {
-      const int i = i0 + k * LOOK_THREADS + tid;
-      if (i < most && (x[k] != y[k] || x[k] < 0 || x[k] >= p.c.n_pages)) at = i;
-    }
-    at = __reduce_min_sync(0xffffffffu, at);
+  for (int i0 = 0; i0 < most; i0 += LOOK_U * LOOK_THREADS) {
+    const int at = __reduce_min_sync(0xffffffffu, differ(p, r, rf, i0, most, tid, LOOK_THREADS));
     if ((tid & 31) == 0 && at != 0x7fffffff) atomicMin(&mismatch, at);
     __syncthreads();
     if (mismatch != 0x7fffffff) break;
@@ -114,15 +123,11 @@ constexpr int CHOOSE_THREADS = 128;
 // Saved tokens below which a prefix is not worth an item of its own.
 constexpr int MIN_SAVED = 2 * TILE;
 
-// A warp for every row; those of a family's lead choose its prefix: of the members' shared lengths the one
-// that saves most when the members that share at least so much take part.  More than 32 members offer 32
-// of theirs.  (In the plan's one block, 8 heads' rows were one warp's: 25 us of 4 families' 35.)
-__global__ void __launch_bounds__(CHOOSE_THREADS) prefix_choose_kernel(const Params p) {
-  wait_prior_grid();
-  allow_next_grid();
-  const int r = blockIdx.x * (CHOOSE_THREADS / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (r >= p.c.R) return;
-  const int l = r / p.Hkv, h = r % p.Hkv;
+// Row r (a warp's); that of a family's lead chooses its prefix: of the members' shared lengths the one that
+// saves most when the members that share at least so much take part.  More than 32 members offer 32 of
+// theirs.
+__device__ __forceinline__ void choose(const Params& p, int r) {
+  const int lane = threadIdx.x & 31, l = r / p.Hkv, h = r % p.Hkv;
   const int root = p.root[l], base = p.base[l], count = p.count[l];
   if (root != l || count < 2) {
     if (lane == 0) {
@@ -170,16 +175,21 @@ __global__ void __launch_bounds__(CHOOSE_THREADS) prefix_choose_kernel(const Par
   }
   if (lane == 0) p.pre_item[r] = k;            // for now: participants
 }
+// (In the plan's one block, 8 heads' rows were one warp's: 25 us of 4 families' 35.)
+__global__ void __launch_bounds__(CHOOSE_THREADS) prefix_choose_kernel(const Params p) {
+  wait_prior_grid();
+  allow_next_grid();
+  const int r = blockIdx.x * (CHOOSE_THREADS / 32) + (threadIdx.x >> 5);
+  if (r < p.c.R) choose(p, r);
+}
 
 // One block: the items in order with their places in the tile sequence, the CTAs' first items.  A warp
 // has a run of the 2 R places (prefixes, then own tokens): it adds its tiles and items up, and writes them
 // once the block has added up the warps'.
-__global__ void __launch_bounds__(PLAN_THREADS) prefix_plan_kernel(const Params p) {
+__device__ void make_plan(const Params& p) {
   constexpr int WARPS = PLAN_THREADS / 32, AHEAD = 4;
   __shared__ long long places_sh[WARPS];
   __shared__ int items_sh[WARPS];
-  wait_prior_grid();
-  allow_next_grid();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, R = p.c.R;
   const int run = (2 * R + 32 * WARPS - 1) / (32 * WARPS) * 32, begin = min(warp * run, 2 * R), end = min(begin + run, 2 * R);
   struct Place {
@@ -274,6 +284,63 @@ __global__ void __launch_bounds__(PLAN_THREADS) prefix_plan_kernel(const Params 
   }
 }
 
+__global__ void __launch_bounds__(PLAN_THREADS) prefix_plan_kernel(const Params p) {
+  wait_prior_grid();
+  allow_next_grid();
+  make_plan(p);
+}
+
+// All three at once for few rows of few pages: a cluster whose warps take the rows, and whose first block
+// makes the plan.  It takes as long (7 us) as the three, and a host that makes small calls only 2 launches
+// less, some 5 us of 27; a warp a row is slower than a block for long tables (112 rows of 1875 pages: 16 us
+// for 9).
+constexpr int CLUSTER = 8;
+constexpr int FEW_ROWS = 128, FEW_SEQS = 128, FEW_PAGES = 256;
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(PLAN_THREADS) prefix_few_kernel(const Params p) {
+  __shared__ int roots[FEW_SEQS];
+  wait_prior_grid();
+  allow_next_grid();
+  const int lane = threadIdx.x & 31, warps = CLUSTER * PLAN_THREADS / 32;
+  const int warp = (threadIdx.x >> 5) * CLUSTER + blockIdx.x;    // neighbouring rows on different SMs
+  for (int x = threadIdx.x; x < p.N; x += PLAN_THREADS) roots[x] = root_of(p, x);
+  __syncthreads();
+  for (int l = warp; l < p.N; l += warps) {
+    const int f = roots[l];
+    int before = 0, rank = 0, mine = 0;
+    for (int x = lane; x < p.N; x += 32) {
+      const int y = roots[x];
+      before += y < f;
+      rank += y == f && x < l;
+      mine += y == f;
+    }
+    before = __reduce_add_sync(0xffffffffu, before);
+    rank = __reduce_add_sync(0xffffffffu, rank);
+    mine = __reduce_add_sync(0xffffffffu, mine);
+    if (lane == 0) {
+      p.root[l] = f;
+      p.order[before + rank] = l;
+      p.base[l] = before;
+      p.count[l] = mine;
+    }
+  }
+  for (int r = warp; r < p.c.R; r += warps) {
+    const int l = r / p.Hkv, f = roots[l], rf = f * p.Hkv + r % p.Hkv;
+    if (lane == 0) check_row(p, r);
+    const int most = f == l ? 0 : min(prefix::row_len(p, r), prefix::row_len(p, rf)) >> p.c.shift;
+    int at = most;
+    for (int i0 = 0; i0 < most && at == most; i0 += LOOK_U * 32)
+      at = min(at, __reduce_min_sync(0xffffffffu, differ(p, r, rf, i0, most, lane, 32)));
+    if (lane == 0) p.shared[r] = at << p.c.shift;
+  }
+  cluster_sync();
+  for (int r = warp; r < p.c.R; r += warps) choose(p, r);
+  cluster_sync();
+  if (blockIdx.x == 0) make_plan(p);
+}
+
 // ------------------------------------------------------------------ fp32 caches
 constexpr int F_THREADS = 256;
 constexpr int F_QT = 32;                 // queries of an item
@@ -290,6 +357,114 @@ struct Pf32 {
   static constexpr int SMEM = (OFF_M + 3 * F_QT) * 4;
 };
 
+constexpr int THIN = 16;                 // queries
+constexpr int THIN_Q = 4;                // at a time
+
+// A piece with few queries (a row's own tokens): warps take the keys, D / 4 lanes a key and its value, four
+// queries in registers.  Every lane group keeps a state of its own, joined in shared memory when the piece
+// ends.  (By the kernel below, with 32 queries' places, 1600 rows of 250 own tokens took 300 us.)
+template <int D>
+__device__ __forceinline__ void thin_piece(const Params& p, const Piece& a, float* sm, int cta) {
+  constexpr int LANES = D / 4, KEYS = 32 / LANES, STATES = F_THREADS / LANES, U = 4;
+  float* os = sm;                                          // [STATES][THIN_Q][D]
+  float2* mls = reinterpret_cast<float2*>(sm + STATES * THIN_Q * D);   // [STATES][THIN_Q]
+  const int tid = threadIdx.x, state = tid / LANES, d = tid % LANES * 4;
+  const int begin = a.it.tok0 + a.u0 * TILE, end = min(a.it.tok1, a.it.tok0 + a.u1 * TILE);
+  const int32_t* table = p.c.table + (size_t)a.it.row * p.c.max_pages;
+  const auto query = [&](int i) {
+    int g;
+    const int r = prefix::query_row(p, a.it, i, g);
+    return make_int2(r, g);
+  };
+  for (int c = 0; c < a.it.nq; c += THIN_Q) {
+    float4 q[THIN_Q], o[THIN_Q];
+    float m[THIN_Q], l[THIN_Q];
+#pragma unroll
+    for (int i = 0; i < THIN_Q; ++i) {
+      q[i] = o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+      if (c + i < a.it.nq && !p.zero) {
+        const int2 x = query(c + i);
+        q[i] = *reinterpret_cast<const float4*>((const float*)p.q + (x.x / p.Hkv) * p.q_stride +
+                                                (size_t)((x.x % p.Hkv) * p.G + x.y) * D + d);
+        if (p.flip) q[i] = make_float4(-q[i].x, -q[i].y, -q[i].z, -q[i].w);
+      }
+    }
+    // (the warp's first key, so that its lanes take the same steps: the sums are the whole warp's shuffles)
+    for (int t0 = begin + tid / 32 * KEYS * U; t0 < end; t0 += STATES * U) {
+      float4 k[U], v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int t = t0 + u * KEYS + tid % 32 / LANES;
+        k[u] = v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (t < end) {
+          const int page = table[t >> p.c.shift];
+          if (page >= 0 && page < p.c.n_pages) {
+            const int64_t at = page * p.c.page_stride + (t & (p.c.ps - 1)) * p.c.token_stride + d;
+            k[u] = *reinterpret_cast<const float4*>((const float*)p.c.k + at);
+            v[u] = *reinterpret_cast<const float4*>((const float*)p.c.v + at);
+          } else {
+            raise_status(p.status, KVP_ERR_DEVICE_CHECK);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < THIN_Q; ++i) {
+        if (c + i >= a.it.nq) break;
+        float s[U], top = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          s[u] = fmaf(q[i].x, k[u].x, fmaf(q[i].y, k[u].y, fmaf(q[i].z, k[u].z, q[i].w * k[u].w)));
+#pragma unroll
+          for (int off = 1; off < LANES; off <<= 1) s[u] += __shfl_xor_sync(0xffffffffu, s[u], off);
+          s[u] = t0 + u * KEYS + tid % 32 / LANES < end ? s[u] * p.c2 : -INFINITY;
+          top = fmaxf(top, s[u]);
+        }
+        const float up = fmaxf(m[i], top), f = paged::weight(m[i], up);
+        m[i] = up;
+        l[i] *= f;
+        o[i] = make_float4(o[i].x * f, o[i].y * f, o[i].z * f, o[i].w * f);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const float w = paged::weight(s[u], up);
+          l[i] += w;
+          o[i].x = fmaf(w, v[u].x, o[i].x);
+          o[i].y = fmaf(w, v[u].y, o[i].y);
+          o[i].z = fmaf(w, v[u].z, o[i].z);
+          o[i].w = fmaf(w, v[u].w, o[i].w);
+        }
+      }
+    }
+    __syncthreads();                                       // the states before have been read
+#pragma unroll
+    for (int i = 0; i < THIN_Q; ++i) {
+      *reinterpret_cast<float4*>(os + (state * THIN_Q + i) * D + d) = o[i];
+      if (d == 0) mls[state * THIN_Q + i] = make_float2(m[i], l[i]);
+    }
+    __syncthreads();
+    const int i = tid / LANES;
+    if (i < THIN_Q && c + i < a.it.nq) {
+      float M = -INFINITY, L = 0.f;
+      for (int k = 0; k < STATES; ++k) M = fmaxf(M, mls[k * THIN_Q + i].x);
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = 0; k < STATES; ++k) {
+        const float2 ml = mls[k * THIN_Q + i];
+        const float w = paged::weight(ml.x, M);
+        const float4 x = *reinterpret_cast<const float4*>(os + (k * THIN_Q + i) * D + d);
+        L = fmaf(ml.y, w, L);
+        y = make_float4(fmaf(x.x, w, y.x), fmaf(x.y, w, y.y), fmaf(x.z, w, y.z), fmaf(x.w, w, y.w));
+      }
+      const int2 x = query(c + i);
+      const bool first = a.u0 == 0;
+      const size_t at = first ? prefix::first_slot(p, a.it.list < 0, x.x, x.y) : prefix::cont_slot(p, cta, c + i);
+      *reinterpret_cast<float4*>((first ? p.first_o : p.cont_o) + at * D + d) = y;
+      if (d == 0) (first ? p.first_ml : p.cont_ml)[at] = make_float2(M, L);
+    }
+  }
+  __syncthreads();
+}
+
 // The items of an fp32 cache (the tensor cores have no fp32 products): 32 queries with 64 keys at a time,
 // logits and outputs by FFMA from shared memory.
 template <int D>
@@ -304,6 +479,11 @@ __global__ void __launch_bounds__(F_THREADS) prefix_f32_kernel(const Params p) {
   prefix::Walk<true> walk(p, cta);
   Piece a;
   while (walk.step(p, a)) {
+    if (a.it.nq <= THIN) {
+      __syncthreads();
+      thin_piece<D>(p, a, sm, cta);
+      continue;
+    }
     const bool own = a.it.list < 0;
     __syncthreads();
     for (int e = tid; e < F_QT * D / 4; e += F_THREADS) {
@@ -594,15 +774,20 @@ cudaError_t run_f32(const Params& p, cudaStream_t st) {
 
 template <typename T, int D>
 cudaError_t run(const Params& p, cudaStream_t st) {
-  count_launches(1);
-  cudaError_t e = launch_with_pdl(prefix_look_kernel, dim3((unsigned)p.c.R), dim3(LOOK_THREADS), 0, st, p);
-  if (e != cudaSuccess) return e;
-  count_launches(1);
-  constexpr int PER = CHOOSE_THREADS / 32;
-  e = launch_with_pdl(prefix_choose_kernel, dim3((unsigned)((p.c.R + PER - 1) / PER)), dim3(CHOOSE_THREADS), 0, st, p);
-  if (e != cudaSuccess) return e;
-  count_launches(1);
-  e = launch_with_pdl(prefix_plan_kernel, dim3(1), dim3(PLAN_THREADS), 0, st, p);
+  cudaError_t e;
+  const int pages = p.c.max_pages < p.c.n_pages ? p.c.max_pages : p.c.n_pages;
+  if (p.c.R <= FEW_ROWS && p.N <= FEW_SEQS && pages <= FEW_PAGES) {
+    count_launches(1);
+    e = launch_with_pdl(prefix_few_kernel, dim3(CLUSTER), dim3(PLAN_THREADS), 0, st, p);
+  } else {
+    count_launches(3);
+    constexpr int PER = CHOOSE_THREADS / 32;
+    e = launch_with_pdl(prefix_look_kernel, dim3((unsigned)p.c.R), dim3(LOOK_THREADS), 0, st, p);
+    if (e != cudaSuccess) return e;
+    e = launch_with_pdl(prefix_choose_kernel, dim3((unsigned)((p.c.R + PER - 1) / PER)), dim3(CHOOSE_THREADS), 0, st, p);
+    if (e != cudaSuccess) return e;
+    e = launch_with_pdl(prefix_plan_kernel, dim3(1), dim3(PLAN_THREADS), 0, st, p);
+  }
   if (e != cudaSuccess) return e;
   if constexpr (sizeof(T) == 2) e = launch_paged_prefix_tc(p, st);
   else e = run_f32<D>(p, st);
