@@ -15,8 +15,9 @@
 //    of a tile's keys: scores come from TMEM once, and the weights go back in their place as the first
 //    operand of P V.  Outputs stay in TMEM until the piece ends.
 //  * More than 128 queries: each group has its own, and both take every tile.  Up to 128: both have the
-//    same, take the tiles in turn, and put their results together when the piece ends.  Either way one
-//    group's softmax runs beside the other's products.
+//    same, take the tiles in turn, and put their results together when the piece ends; a piece of one tile
+//    is one group's, and the other goes on with the next.  Either way one group's softmax runs beside the
+//    other's products.
 //  * V lies [key][dim] in memory, so it is the second operand in its MN-major form; nothing is transposed.
 //  * P enters the product as the sum of two 16-bit parts: 16 (bf16) or 22 (f16) bits of every weight, so
 //    that an output is off by its own rounding only; with one part bf16 outputs would be 1.4 times as far
@@ -525,10 +526,15 @@ __global__ void __launch_bounds__(X_THREADS, 1)
       const bool both = a.it.nq > ROWS;
       const int step = both ? 1 : 2, tiles = a.u1 - a.u0;
       const int u0 = both ? a.u0 : a.u0 + ((li0 ^ g) & 1);
-      const bool has_a = both || a.u0 + (li0 & 1) < a.u1, has_b = both || a.u0 + (~li0 & 1) < a.u1;
       const int q0 = both ? g * ROWS : 0, nq = min(ROWS, a.it.nq - q0), tokens = a.it.tok1 - a.it.tok0 - 64 * c;
       const bool busy = quad * 32 < nq;                   // (the same in both warps)
-      if (!dry) li0 += tiles;
+      const bool alone = both || tiles == 1;              // a group with its outputs
+      if (!dry) {
+        uses_oa += both || tiles > 1 || !(li0 & 1);
+        uses_ob += both || tiles > 1 || (li0 & 1);
+        li0 += tiles;
+      }
+      if (u0 >= a.u1) continue;                           // the other group has the piece's only tile
       float m = -INFINITY, l = 0.f;
       for (int u = u0; u < a.u1; u += step) {
         if (!dry) ok = ok && wait(bar_s + 8 * g, uses_s++ & 1);
@@ -635,10 +641,10 @@ __global__ void __launch_bounds__(X_THREADS, 1)
       }
       float* out = (a.u0 == 0 ? p.first_o : p.cont_o) + slot * D;
       float2* ml = (a.u0 == 0 ? p.first_ml : p.cont_ml) + slot;
-      if (g ? has_b : has_a) ok = ok && wait(bar_o + 8 * g, (g ? uses_ob : uses_oa) & 1);
-      if (both) {
+      ok = ok && wait(bar_o + 8 * g, ((g ? uses_ob : uses_oa) - 1) & 1);
+      ptx::tc_fence_after();
+      if (alone) {
         if (busy) {
-          ptx::tc_fence_after();
           (c ? row[g * ROWS].y : row[g * ROWS].x) = l;
           bar_sync(pair, 64);
           l += c ? row[g * ROWS].x : row[g * ROWS].y;
@@ -651,12 +657,13 @@ __global__ void __launch_bounds__(X_THREADS, 1)
             if (tid < nq) store_part(out + k, o);
           }
           if (tid < nq && c == 0) *ml = make_float2(m, l);
-          ptx::tc_fence_before();
           bar_sync(pair, 64);
         }
-        ok = ok && wait(bar_o + 8 * (g ^ 1), (g ? uses_oa : uses_ob) & 1);
+        ptx::tc_fence_before();
       } else {
-        if (g ? has_a : has_b) ok = ok && wait(bar_o + 8 * (g ^ 1), (g ? uses_oa : uses_ob) & 1);
+        // (of the other group's outputs none but these can be pending: its tiles before were added up before
+        // this group's last)
+        ok = ok && wait(bar_o + 8 * (g ^ 1), ((g ? uses_oa : uses_ob) - 1) & 1);
         ptx::tc_fence_after();
         if (busy) {
           if (c) row[g * ROWS].y = l;
@@ -676,11 +683,8 @@ __global__ void __launch_bounds__(X_THREADS, 1)
             loaded(o);
             loaded(y);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              // (a group without a tile has left what was there before)
-              const float va = has_a ? __uint_as_float(o[i]) * fa : 0.f;
-              o[i] = __float_as_uint(has_b ? fmaf(__uint_as_float(y[i]), fb, va) : va);
-            }
+            for (int i = 0; i < 16; ++i)
+              o[i] = __float_as_uint(fmaf(__uint_as_float(y[i]), fb, __uint_as_float(o[i]) * fa));
             if (tid < nq) store_part(out + k, o);
           }
           if (tid < nq && w == 0) *ml = make_float2(M, fmaf(A.y, fa, B.y * fb));
@@ -688,8 +692,6 @@ __global__ void __launch_bounds__(X_THREADS, 1)
         ptx::tc_fence_before();
         bar_sync(ALL, 512);                               // both outputs have been read
       }
-      uses_oa += has_a;
-      uses_ob += has_b;
     }
   }
   ptx::tc_fence_before();
