@@ -13,7 +13,7 @@ import math
 
 import torch
 
-from ._lib import _DTYPE, _check, _dtype, _need, load
+from ._lib import _DTYPE, _check, _need, load
 from .paged import _raw_stream
 
 
@@ -100,16 +100,16 @@ class Rope:
         return inv
 
 
-def _elsewhere(device, stream):
-    return stream is not None or torch.cuda.current_device() != device.index
+def _elsewhere(index, stream):
+    return stream is not None or torch.cuda.current_device() != index
 
 
-def _there(device, stream):
+def _there(index, stream):
     """The call's device and stream made the current ones, so that its temporaries belong to them."""
     if stream is None:
-        return torch.cuda.device(device)
-    if stream.device != device:
-        raise ValueError(f"stream must be on {device}, got {stream.device}")
+        return torch.cuda.device(index)
+    if stream.device != torch.device("cuda", index):
+        raise ValueError(f"stream must be on cuda:{index}, got {stream.device}")
     return torch.cuda.stream(stream)
 
 
@@ -117,38 +117,46 @@ _Strides = ctypes.c_int64 * 3
 
 
 def _rows(t, name, like=None, heads=None):
-    """[B, H, S, D] or [H, S, D] with a contiguous last axis: (the 4-dim view, strides or None)."""
+    """[B, H, S, D] or [H, S, D] with a contiguous last axis, of the same device, type and sizes as ``like`` (but for
+    ``heads``): (pointer, strides or None, (device index, dtype, B, H, S, D)).  A small call is its checks, so each
+    attribute is asked for once."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
+    index, dtype, shape = t.get_device(), t.dtype, t.shape
+    if index < 0 or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    n = t.dim()
-    if n == 3:
-        t = t.unsqueeze(0)
-    elif n != 4:
+    n = len(shape)
+    if n == 4:
+        B, H, S, D = shape
+    elif n == 3:
+        B = 1
+        H, S, D = shape
+    else:
         raise ValueError(f"{name} must be [B, H, S, D] or [H, S, D]")
+    this = (index, dtype, B, H, S, D)
     if like is not None:
-        if t.get_device() != like.get_device():
-            raise ValueError(f"{name} must be on {like.device}, got {t.device}")
-        if t.dtype != like.dtype:
-            raise ValueError(f"{name} must be {like.dtype}, got {t.dtype}")
-        shape = like.shape if heads is None else (like.shape[0], heads, like.shape[2], like.shape[3])
-        if t.shape != shape:
-            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        want = like if heads is None else like[:3] + (heads,) + like[4:]
+        if this != want:
+            if index != want[0]:
+                raise ValueError(f"{name} must be on cuda:{want[0]}, got {t.device}")
+            if dtype != want[1]:
+                raise ValueError(f"{name} must be {want[1]}, got {dtype}")
+            raise ValueError(f"{name} must have shape {want[2:]}, got {this[2:]}")
     if t.is_contiguous():
-        return t, None
-    b, h, s, d = t.stride()
-    if d != 1:
+        return t.data_ptr(), None, this
+    strides = t.stride()
+    if strides[-1] != 1:
         raise ValueError(f"{name}: the head_dim axis must be contiguous")
-    return t, _Strides(b, h, s)
+    return t.data_ptr(), _Strides(*strides[:3]) if n == 4 else _Strides(0, *strides[:2]), this
 
 
-def _result(out, name, x, x4, heads=None):
-    """The tensor to return and its rows: `out`, or a new dense tensor like x."""
+def _result(out, name, x, like):
+    """The tensor to return, like x: `out`, or a new dense one; (tensor, pointer, strides)."""
     if out is None:
-        return torch.empty(x.shape, dtype=x.dtype, device=x.device), None
-    out4, strides = _rows(out, name, x4, heads)
-    return out4, strides
+        out = torch.empty(x.shape, dtype=like[1], device=x.device)
+        return out, out.data_ptr(), None
+    ptr, strides, _ = _rows(out, name, like)
+    return out, ptr, strides
 
 
 def _positions(positions, like):
@@ -157,16 +165,18 @@ def _positions(positions, like):
         return None, 0
     if not isinstance(positions, torch.Tensor):
         raise TypeError("positions must be a torch.Tensor")
-    B, _, S, _ = like.shape
-    if positions.get_device() != like.get_device():
-        raise ValueError(f"positions must be on {like.device}, got {positions.device}")
+    B, S = like[2], like[4]
+    if positions.get_device() != like[0]:
+        raise ValueError(f"positions must be on cuda:{like[0]}, got {positions.device}")
     if positions.dtype != torch.int32:
         raise ValueError(f"positions must be torch.int32, got {positions.dtype}")
-    if positions.shape != (S,) and positions.shape != (B, S):
-        raise ValueError(f"positions must have shape ({S},) or ({B}, {S}), got {tuple(positions.shape)}")
-    if S > 1 and positions.stride(-1) != 1:
+    shape = positions.shape
+    if shape != (B, S) and shape != (S,):
+        raise ValueError(f"positions must have shape ({S},) or ({B}, {S}), got {tuple(shape)}")
+    strides = positions.stride()
+    if S > 1 and strides[-1] != 1:
         raise ValueError("positions must be contiguous along the tokens")
-    return positions.data_ptr(), positions.stride(0) if positions.dim() == 2 and B > 1 else 0
+    return positions.data_ptr(), strides[0] if len(strides) == 2 and B > 1 else 0
 
 
 def _rope_ref(rope):
@@ -177,44 +187,64 @@ def _rope_ref(rope):
     return rope._ref
 
 
+def _code(dtype):
+    code = _DTYPE.get(dtype)
+    if code is None:
+        raise ValueError(f"unsupported dtype {dtype}")
+    return code
+
+
 def kvp_rope(x, rope, positions=None, start=0, inverse=False, out=None, stream=None):
     """Rotate x [B, H, S, D] (or [H, S, D]; strided views are read in place) by the positions of its tokens:
     int32 [S] or [B, S], or start, start + 1, ...  ``inverse`` turns back (the rotation's gradient).  ``out`` may
     be x itself; by default a new dense tensor."""
-    x4, xs = _rows(x, "x")
-    if _elsewhere(x4.device, stream):
-        with _there(x4.device, stream):
+    x_ptr, xs, like = _rows(x, "x")
+    index, dtype, B, H, S, D = like
+    if _elsewhere(index, stream):
+        with _there(index, stream):
             return kvp_rope(x, rope, positions, start, inverse, out)
     if rope is None:
         raise TypeError("rope must be a Rope")
-    out4, os = _result(out, "out", x, x4)
-    pos, ps = _positions(positions, x4)
-    B, H, S, D = x4.shape
-    rc = load().kvp_rope(x4.data_ptr(), out4.data_ptr(), _dtype(x4), B, H, S, D, xs, os, _rope_ref(rope), pos, ps,
-                         int(start), int(bool(inverse)), _raw_stream(x4.get_device()))
+    dtype = _code(dtype)
+    out, out_ptr, os = _result(out, "out", x, like)
+    pos, ps = _positions(positions, like)
+    rc = load().kvp_rope(x_ptr, out_ptr, dtype, B, H, S, D, xs, os, _rope_ref(rope), pos, ps, int(start),
+                         int(bool(inverse)), _raw_stream(index))
     if rc:
         _check("kvp_rope", rc)
-    return out4 if out is None else out
+    return out
 
 
-def _weight(w, name, q4):
+def _weight(w, name, like):
+    """[D] of the tensors' type or float32: (pointer, dtype)."""
     if w is None:
-        return None
-    _need(w, name, None, q4.shape[3:])
-    if w.get_device() != q4.get_device():
-        raise ValueError(f"{name} must be on {q4.device}, got {w.device}")
-    if w.dtype != q4.dtype and w.dtype != torch.float32:
-        raise ValueError(f"{name} must be {q4.dtype} or torch.float32, got {w.dtype}")
-    return w.data_ptr()
+        return None, None
+    if not isinstance(w, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    index, dtype = w.get_device(), w.dtype
+    if index < 0 or not w.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if not w.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if w.shape != like[5:]:
+        raise ValueError(f"{name} must have shape {like[5:]}, got {tuple(w.shape)}")
+    if index != like[0]:
+        raise ValueError(f"{name} must be on cuda:{like[0]}, got {w.device}")
+    if dtype != like[1] and dtype != torch.float32:
+        raise ValueError(f"{name} must be {like[1]} or torch.float32, got {dtype}")
+    return w.data_ptr(), dtype
 
 
-def _weights(q_weight, k_weight, q4):
-    q, k = _weight(q_weight, "q_weight", q4), _weight(k_weight, "k_weight", q4)
-    if q is None:
-        return q, k, _DTYPE[q4.dtype if k is None else k_weight.dtype]
-    if k is not None and k_weight.dtype != q_weight.dtype:
+def _weights(q_weight, k_weight, like):
+    q, q_dtype = _weight(q_weight, "q_weight", like)
+    k, k_dtype = _weight(k_weight, "k_weight", like)
+    if q_dtype is not None and k_dtype is not None and q_dtype != k_dtype:
         raise ValueError("q_weight and k_weight must have the same dtype")
-    return q, k, _DTYPE[q_weight.dtype]
+    return q, k, _DTYPE[q_dtype or k_dtype or like[1]]
+
+
+def _heads(k):
+    return k.shape[-3] if isinstance(k, torch.Tensor) and k.dim() >= 3 else 0
 
 
 def kvp_qk_norm_rope(q, k, q_weight=None, k_weight=None, eps=1e-6, rope=None, positions=None, start=0, q_out=None,
@@ -222,28 +252,26 @@ def kvp_qk_norm_rope(q, k, q_weight=None, k_weight=None, eps=1e-6, rope=None, po
     """Norms of every head of q [B, H_q, S, D] and k [B, H_kv, S, D] (or without B; strided views are read in
     place) over its D values, times the weights [D] (of q's dtype or float32; None: ones), rotated as by
     :func:`kvp_rope` (rope None: not rotated) -> (q_out, k_out).  The outputs may be q and k themselves."""
-    q4, qs = _rows(q, "q")
-    if _elsewhere(q4.device, stream):
-        with _there(q4.device, stream):
+    q_ptr, qs, like = _rows(q, "q")
+    index, dtype, B, Hq, S, D = like
+    if _elsewhere(index, stream):
+        with _there(index, stream):
             return kvp_qk_norm_rope(q, k, q_weight, k_weight, eps, rope, positions, start, q_out, k_out)
-    dtype = _dtype(q4)
-    B, Hq, S, D = q4.shape
-    Hkv = k.shape[-3] if isinstance(k, torch.Tensor) and k.dim() >= 3 else 0
-    k4, ks = _rows(k, "k", q4, Hkv)
-    qo4, qos = _result(q_out, "q_out", q, q4)
-    ko4, kos = _result(k_out, "k_out", k, k4)
-    pos, ps = _positions(positions, q4)
-    qw, kw, wd = _weights(q_weight, k_weight, q4)
-    rc = load().kvp_qk_norm_rope(q4.data_ptr(), k4.data_ptr(), qo4.data_ptr(), ko4.data_ptr(), dtype, B, Hq, Hkv, S, D,
-                                 qs, ks, qos, kos, qw, kw, wd, float(eps), _rope_ref(rope), pos, ps, int(start),
-                                 _raw_stream(q4.get_device()))
+    dtype = _code(dtype)
+    k_ptr, ks, k_like = _rows(k, "k", like, _heads(k))
+    q_out, qo_ptr, qos = _result(q_out, "q_out", q, like)
+    k_out, ko_ptr, kos = _result(k_out, "k_out", k, k_like)
+    pos, ps = _positions(positions, like)
+    qw, kw, wd = _weights(q_weight, k_weight, like)
+    rc = load().kvp_qk_norm_rope(q_ptr, k_ptr, qo_ptr, ko_ptr, dtype, B, Hq, k_like[3], S, D, qs, ks, qos, kos, qw, kw, wd,
+                                 float(eps), _rope_ref(rope), pos, ps, int(start), _raw_stream(index))
     if rc:
         _check("kvp_qk_norm_rope", rc)
-    return qo4 if q_out is None else q_out, ko4 if k_out is None else k_out
+    return q_out, k_out
 
 
 @functools.lru_cache(maxsize=256)
-def _backward_bytes(device, *sizes):
+def _backward_bytes(index, *sizes):
     """(The sizes alone decide, on a device: the current one.)"""
     return int(load().kvp_qk_norm_rope_backward_workspace_size(*sizes))
 
@@ -253,33 +281,32 @@ def kvp_qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight=None, k_weight=None
     """Gradients of :func:`kvp_qk_norm_rope` from those of its outputs and its inputs ->
     (dq, dk, dq_weight, dk_weight), the last two float32 [D] (of weights that are None as of ones).
     dq may be dq_out or q itself, dk likewise."""
-    q4, qs = _rows(q, "q")
-    if _elsewhere(q4.device, stream):
-        with _there(q4.device, stream):
+    q_ptr, qs, like = _rows(q, "q")
+    index, dtype, B, Hq, S, D = like
+    if _elsewhere(index, stream):
+        with _there(index, stream):
             return kvp_qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, eps, rope, positions, start, dq,
                                              dk, workspace)
-    dtype = _dtype(q4)
-    B, Hq, S, D = q4.shape
-    Hkv = k.shape[-3] if isinstance(k, torch.Tensor) and k.dim() >= 3 else 0
-    k4, ks = _rows(k, "k", q4, Hkv)
-    gq4, gqs = _rows(dq_out, "dq_out", q4)
-    gk4, gks = _rows(dk_out, "dk_out", k4)
-    dq4, dqs = _result(dq, "dq", q, q4)
-    dk4, dks = _result(dk, "dk", k, k4)
-    pos, ps = _positions(positions, q4)
-    qw, kw, wd = _weights(q_weight, k_weight, q4)
-    dwq, dwk = torch.empty(2, D, dtype=torch.float32, device=q4.device).unbind()
+    dtype = _code(dtype)
+    k_ptr, ks, k_like = _rows(k, "k", like, _heads(k))
+    gq_ptr, gqs, _ = _rows(dq_out, "dq_out", like)
+    gk_ptr, gks, _ = _rows(dk_out, "dk_out", k_like)
+    dq, dq_ptr, dqs = _result(dq, "dq", q, like)
+    dk, dk_ptr, dks = _result(dk, "dk", k, k_like)
+    pos, ps = _positions(positions, like)
+    qw, kw, wd = _weights(q_weight, k_weight, like)
+    device = q.device
+    dwq, dwk = (torch.empty(D, dtype=torch.float32, device=device) for _ in range(2))
     if workspace is None:
-        workspace = torch.empty(_backward_bytes(q4.get_device(), dtype, B, Hq, Hkv, S, D), dtype=torch.uint8, device=q4.device)
+        workspace = torch.empty(_backward_bytes(index, dtype, B, Hq, k_like[3], S, D), dtype=torch.uint8, device=device)
     else:
         _need(workspace, "workspace", torch.uint8)
-        if workspace.device != q4.device:
-            raise ValueError(f"workspace must be on {q4.device}, got {workspace.device}")
-    rc = load().kvp_qk_norm_rope_backward(gq4.data_ptr(), gk4.data_ptr(), q4.data_ptr(), k4.data_ptr(), dq4.data_ptr(),
-                                          dk4.data_ptr(), dwq.data_ptr(), dwk.data_ptr(), dtype, B, Hq, Hkv, S, D,
-                                          gqs, gks, qs, ks, dqs, dks, qw, kw, wd, float(eps), _rope_ref(rope), pos, ps,
-                                          int(start), workspace.data_ptr(), workspace.numel(),
-                                          _raw_stream(q4.get_device()))
+        if workspace.device != device:
+            raise ValueError(f"workspace must be on {device}, got {workspace.device}")
+    rc = load().kvp_qk_norm_rope_backward(gq_ptr, gk_ptr, q_ptr, k_ptr, dq_ptr, dk_ptr, dwq.data_ptr(), dwk.data_ptr(), dtype,
+                                          B, Hq, k_like[3], S, D, gqs, gks, qs, ks, dqs, dks, qw, kw, wd, float(eps),
+                                          _rope_ref(rope), pos, ps, int(start), workspace.data_ptr(), workspace.numel(),
+                                          _raw_stream(index))
     if rc:
         _check("kvp_qk_norm_rope_backward", rc)
-    return dq4 if dq is None else dq, dk4 if dk is None else dk, dwq, dwk
+    return dq, dk, dwq, dwk
