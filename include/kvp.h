@@ -17,7 +17,8 @@
  * kvp_topk_cutoffs and kvp_sparse_lse_pass (KVpop's running top-k sparse
  * attention and its log-normalisers), and the paged cache, in which a row holds
  * only the pages its kept tokens need: kvp_paged_init, kvp_paged_append,
- * kvp_paged_fork, kvp_paged_compact, kvp_paged_free and kvp_paged_decode_attn.
+ * kvp_paged_fork, kvp_paged_compact, kvp_paged_free, kvp_paged_decode_attn and
+ * kvp_paged_prefix_decode_attn (rows that share a long prefix).
  *
  * What stands between a model's projections and those: kvp_rope (rotary
  * positions) and kvp_qk_norm_rope (norms of queries and keys with the rotation
@@ -676,8 +677,8 @@ int kvp_paged_decode_attn(const void* q, int64_t q_stride, const kvp_paged_cache
  * head_dim] of the cache's dtype.  G = h_q / h_kv <= 16; at most KVP_PREFIX_MAX_SEQS
  * sequences.  The plan of the work is made on the device: a captured call serves a
  * cache and families that change.  workspace:
- * kvp_paged_prefix_decode_attn_workspace_size() bytes, 256-byte aligned (some 4
- * outputs of float32 per query, and 20 or 40 MB). */
+ * kvp_paged_prefix_decode_attn_workspace_size() bytes, 256-byte aligned (some 2
+ * outputs of float32 per query, and 5 to 20 MB). */
 #define KVP_PREFIX_MAX_SEQS 16384
 size_t kvp_paged_prefix_decode_attn_workspace_size(const kvp_paged_cache* cache, int h_q, int h_kv);
 int kvp_paged_prefix_decode_attn(const void* q, int64_t q_stride, const kvp_paged_cache* cache,
