@@ -201,6 +201,24 @@ def test_many_rows_and_a_long_prefix(dtype):
     check(*build(rows, leads, 1, 8, 64, 64, DT[dtype], 8, shared))
 
 
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("D,G,ps,seed", [(64, 8, 32, 0), (128, 5, 64, 1), (128, 16, 16, 2), (64, 1, 128, 3)])
+def test_pieces_of_every_kind_in_a_row(dtype, D, G, ps, seed):
+    """Prefixes with fewer and more than 128 queries, own tokens of none, one and several tiles, one after the other in
+    every block's range."""
+    rng = torch.Generator().manual_seed(seed)
+    rows, leads, shared = [], [], []
+    while len(rows) < 260:
+        first, members = len(rows), int(torch.randint(1, 40, (1,), generator=rng))
+        prompt = int(torch.randint(1, 1200, (1,), generator=rng))
+        for _ in range(members):
+            own = int(torch.randint(0, 700, (1,), generator=rng)) if torch.rand(1, generator=rng) < 0.6 else 0
+            rows.append([prompt + own])
+            leads.append(first)
+            shared.append([prompt // ps])
+    check(*build(rows, leads, 1, G, D, ps, DT[dtype], seed, shared))
+
+
 @pytest.mark.parametrize("dtype", ["f16", "f32"])
 def test_infinities_stay_with_their_owner(dtype):
     """An infinite value, or a key of -inf, in the tokens that one sequence has for itself."""

@@ -184,6 +184,26 @@ def test_norm_rope_backward(case, B, S, weight):
     assert torch.equal(a, dq) and torch.equal(b, dk)
 
 
+@pytest.mark.parametrize("dtype,D,Hq,Hkv,S", [("f32", 64, 2, 1, 9001), ("bf16", 128, 1, 1, 4501)])
+def test_more_tokens_than_run_at_once(dtype, D, Hq, Hkv, S):
+    q, k, w, rope, pos, gen = norm_case(dtype, D, Hq, Hkv, dict(rotary_dim=D), 3, S, 4)
+    outs = kvp.kvp_qk_norm_rope(q, k, w[0], w[1], 1e-5, rope, positions=pos)
+    gq, gk = randn(gen, *q.shape, dtype=q.dtype), randn(gen, *k.shape, dtype=q.dtype)
+    grads = kvp.kvp_qk_norm_rope_backward(gq, gk, q, k, w[0], w[1], 1e-5, rope, positions=pos)
+    turned = kvp.kvp_rope(q, rope, positions=pos)
+    p = pos.cpu().numpy()[:, None]
+    close(turned, oracle.rotate(np64(q), p, **spec(rope)), 8 * STEP * mixed(np64(q), rope))
+    for x, g, wt, y, dx, dw in ((q, gq, w[0], outs[0], grads[0], grads[2]), (k, gk, w[1], outs[1], grads[1], grads[3])):
+        x, g, wt = np64(x), np64(g), np64(wt)
+        close(y, oracle.norm_rope(x, wt, 1e-5, p, **spec(rope)), 24 * STEP * mixed(oracle.norm_rope(x, wt, 1e-5), rope))
+        want, want_w = oracle.norm_rope_backward(g, x, wt, 1e-5, p, **spec(rope))
+        r = 1 / np.sqrt((x * x).mean(-1, keepdims=True) + 1e-5)
+        n, dz = np.abs(x * r), mixed(g, rope)
+        wdz = dz * np.abs(wt)
+        close(dx, want, 64 * STEP * r * (wdz + n * (wdz * n).mean(-1, keepdims=True)))
+        close(dw, want_w, (64 + 64 + 40) * STEP * (dz * n).reshape(-1, D).sum(0))
+
+
 def test_gradient_matches_differences():
     q, k, w, rope, pos, gen = norm_case("f32", 64, 2, 1, dict(rotary_dim=32), 1, 3)
     q, k = q.contiguous() / 3, k.contiguous() / 3
