@@ -219,6 +219,18 @@ def test_pieces_of_every_kind_in_a_row(dtype, D, G, ps, seed):
     check(*build(rows, leads, 1, G, D, ps, DT[dtype], seed, shared))
 
 
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("members,G,ps", [(24, 8, 16), (70, 4, 64), (3, 5, 32)])
+def test_members_that_share_less(dtype, members, G, ps):
+    """Every member has its own length in common with the lead."""
+    rng = torch.Generator().manual_seed(members)
+    prompt = 6000
+    pages = prompt // ps
+    cut = [[int(torch.randint(0, pages + 1, (1,), generator=rng)), pages if n % 3 else n % 2 * pages // 2] for n in range(members)]
+    rows = [[prompt + n * 7, prompt + n] for n in range(members)]
+    check(*build(rows, [1] * members, 2, G, 64, ps, DT[dtype], members, cut))
+
+
 @pytest.mark.parametrize("dtype", ["f16", "f32"])
 def test_infinities_stay_with_their_owner(dtype):
     """An infinite value, or a key of -inf, in the tokens that one sequence has for itself."""
