@@ -6,9 +6,11 @@
 // of all items form one sequence, of which every CTA takes an equal range; a CTA's share of an item is a
 // piece.  The sequence has two places for a tile, three for one that meets more than 128 queries (bound by
 // the tensor cores), and before every item GAP places, about what it costs to begin and end one: without
-// those, the CTAs that had the short items at the end took 1.4 times as long as the rest.  A piece that begins an item leaves its partial results (maximum, sum, unnormalised output) at the
-// queries' own places, one that goes on from the CTA before at the CTA's, and the join adds a query's parts
-// in the order of the tiles, so results do not depend on timing.
+// those, the CTAs that had the short items at the end took 1.4 times as long as the rest.
+//
+// A piece that begins an item leaves its partial results (maximum, sum, unnormalised output) at the queries'
+// own places, one that goes on from the CTA before at the CTA's, and the join adds a query's parts in the
+// order of the tiles, so results do not depend on timing.
 #pragma once
 
 #include "kvp_common.cuh"

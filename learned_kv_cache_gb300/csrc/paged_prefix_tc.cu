@@ -2,8 +2,10 @@
 //
 //   S = Q K^T,  P = 2^(c S - m),  l = sum P,  O = P V   for up to 256 queries and 128 keys at a time
 //
-// 4 D flop per query and key against 4 D bytes per key: with few queries bound by HBM, with 256 about as
-// long on the tensor cores (QK^T and two parts of P V: 3072 cycles a tile of D 128) as in HBM (2790).
+// 4 D flop per query and key against 4 D bytes per key: with few queries bound by HBM, with 256 by the tensor
+// cores (QK^T and two parts of P V take 3700 cycles a tile of D 128, its keys and values 2790 in HBM).
+// Measured: 32 rows of 32768 tokens without a family at 6.2 TB/s; 32 sequences on one prompt of 32768 tokens,
+// 32 / 8 heads, with up to 1000 own tokens each in 45 us of the call's 60 (4.5 TB/s).
 //
 //  * One CTA per SM.  Warp 0 copies keys and values: K and V of a tile are a unit each of a ring, one TMA
 //    box per page (or 128 tokens of one) and 64-column half, in the order in which the products use them.

@@ -6,7 +6,9 @@
 //   t = pos * inv_freq of the pair; the values behind rotary_dim pass.
 //   dz = R^T dy,  dw = sum dz n,  dx = (w dz - n mean(w dz n)) / sqrt(mean(x^2) + eps)
 //
-// A few operations per value: bound by HBM (every input read once, every output written once).
+// A few operations per value: bound by HBM (every input read once, every output written once).  Measured,
+// 32 + 8 heads of 128 in bf16, norms and rotation: 131072 tokens 425 us (6.3 TB/s), 8192 tokens 33.5 us, their
+// gradients 49 us (5.1 TB/s); rotation alone of 32768 tokens 112 us (6.0 TB/s).
 //
 //  * Angles.  pos * inv_freq reaches 1e5 radians, of which a float keeps 1e-2.  The host gives each pair's
 //    frequency in turns as a fraction of 2^64, so that the angle is one 64-bit product whose overflow drops
@@ -16,9 +18,10 @@
 //    cosines and sines (8 pairs a lane) and walk over the heads.  Nothing is shared between lanes but sums
 //    over a row, so no warp waits for another (with the angles in shared memory and a few tokens a block,
 //    8192 tokens of 32 + 8 heads took 52 us).
-//  * What keeps HBM busy is bytes on their way: every lane has a ring of its own in shared memory, into which
-//    it copies rows (cp.async) some steps before it uses them, beyond the end of a unit.  As many in
-//    registers would spill, or leave an SM too few warps (gradients of those tokens: 58 us).
+//  * What keeps HBM busy is bytes on their way.  The forward kernels have the next rows in registers; the
+//    gradients, with two sources, copy theirs into a ring of every lane's own in shared memory (cp.async) some
+//    steps before they use them, beyond the end of a unit: as many in registers spill, or leave an SM too few
+//    warps (58 us).  For the forward kernels the ring was slower (485 us of 131072 tokens for 425).
 //  * A lane owns 8 pairs of a row: two vectors of 8 values that lie rotary_dim / 2 apart (halves) or side
 //    by side (interleaved), so pairs never cross lanes and sums over a row are 2 or 3 shuffles.
 //  * Lane groups side by side have tokens side by side: in a tensor laid out by heads their rows touch.
@@ -94,7 +97,8 @@ __device__ __forceinline__ float2 turn_of(int pos, uint64_t step) {
   const uint32_t t = (uint32_t)(((uint64_t)(int64_t)pos * step) >> 32);
   const uint32_t quarter = (t + 0x20000000u) >> 30;
   const float x = (float)(int)(t - (quarter << 30)) * (6.283185307179586f * 0x1p-32f), xx = x * x;
-  const float c = fmaf(xx, fmaf(xx, fmaf(xx, fmaf(xx, fmaf(xx, -1.f / 3628800.f, 1.f / 40320.f), -1.f / 720.f), 1.f / 24.f), -0.5f), 1.f);
+  float c = fmaf(xx, fmaf(xx, -1.f / 3628800.f, 1.f / 40320.f), -1.f / 720.f);
+  c = fmaf(xx, fmaf(xx, fmaf(xx, c, 1.f / 24.f), -0.5f), 1.f);
   const float s = fmaf(x * xx, fmaf(xx, fmaf(xx, fmaf(xx, 1.f / 362880.f, -1.f / 5040.f), 1.f / 120.f), -1.f / 6.f), x);
   // a quarter turn on: (c, s) -> (-s, c)
   const float a = quarter & 1 ? s : c, b = quarter & 1 ? c : s;
@@ -212,12 +216,13 @@ __device__ __forceinline__ void copy4(void* to, const void* from) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
 }
 
-// The rows of a warp's units, one step of every lane group after the other, copied STEPS - 1 steps ahead.
-// SOURCES: x, or x and dy.
-template <typename T, int D, int SOURCES>
+// The rows of a warp's units, one step of every lane group after the other, copied STEPS - 1 steps ahead (of
+// 64 or, in fp32, 128 bytes a lane: 70 or 101 KB a block).  The sources are x and dy.
+template <typename T>
 struct Rows {
+  static constexpr int SOURCES = 2;
   static constexpr int PARTS = 16 * sizeof(T) / 16;        // 16-byte parts of a lane's 16 values
-  static constexpr int STEPS = (SOURCES == 1 ? 48 : 64) / (4 * PARTS * SOURCES) < 3 ? 3 : (SOURCES == 1 ? 48 : 64) / (4 * PARTS * SOURCES);
+  static constexpr int STEPS = PARTS * SOURCES > 4 ? 3 : 4;
   static constexpr int SMEM = STEPS * (PARTS * SOURCES * 16 + 4) * THREADS;
   // [step][part][thread], then the tokens' positions
   uint4* ring;
@@ -226,7 +231,7 @@ struct Rows {
   const Split& split;
   int at0, at1;
   uint32_t u0, stride, all, begin;   // the warp's first unit, from step to step, the last; the lane's within the warp
-  int tensor;                        // units of one tensor only, or -1
+  int tensor;
   // the unit that is being copied
   int h, most, n, slot;
   const T* src[SOURCES];
@@ -238,22 +243,17 @@ struct Rows {
     ring = smem + threadIdx.x;
     ring_pos = reinterpret_cast<int*>(smem + STEPS * PARTS * SOURCES * THREADS) + threadIdx.x;
   }
-  // This lane's unit of the warp's step u, and the tensor's number.
-  __device__ __forceinline__ Unit unit(uint32_t u, int& j) const {
-    const uint32_t id = u + begin;
-    j = tensor >= 0 ? tensor : id >= split.units[0];
-    return Unit(a, split, j ? a.t[1].heads : a.t[0].heads, tensor < 0 && j ? id - split.units[0] : id, id < all);
+  // This lane's unit of the warp's step u.
+  __device__ __forceinline__ Unit unit(uint32_t u) const {
+    return Unit(a, split, tensor ? a.t[1].heads : a.t[0].heads, u + begin, u + begin < all);
   }
   __device__ __forceinline__ void enter() {
-    int j;
-    const Unit x = unit(u0, j);
-    const RopeTensor& z = j ? a.t[1] : a.t[0];
+    const Unit x = unit(u0);
+    const RopeTensor& z = tensor ? a.t[1] : a.t[0];
     hs[0] = z.xs[1];
     src[0] = (const T*)z.x + x.b * z.xs[0] + x.s * z.xs[2] + x.h0 * hs[0];
-    if (SOURCES == 2) {
-      hs[SOURCES - 1] = z.dys[1];
-      src[SOURCES - 1] = (const T*)z.dy + x.b * z.dys[0] + x.s * z.dys[2] + x.h0 * hs[SOURCES - 1];
-    }
+    hs[1] = z.dys[1];
+    src[1] = (const T*)z.dy + x.b * z.dys[0] + x.s * z.dys[2] + x.h0 * hs[1];
     pos = a.positions ? a.positions + x.b * a.position_stride + x.s : nullptr;
     n = x.n;
     most = __reduce_max_sync(0xffffffffu, n);
@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(THREADS, BACK_BLOCKS)
     norm_rope_backward_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ Freqs f,
                               const __grid_constant__ Split split, int split_at, float* __restrict__ part) {
   using L = Lane<D, INTERLEAVED>;
-  using R = Rows<T, D, 2>;
+  using R = Rows<T>;
   extern __shared__ uint4 ring[];
   __shared__ __align__(16) Tables<D> sh;
   __shared__ float sum_sh[THREADS / 32][D];
@@ -400,8 +400,7 @@ __global__ void __launch_bounds__(THREADS, BACK_BLOCKS)
   uint64_t dw[8] = {};
   int slot = 0;
   for (; u0 < all; u0 += stride) {
-    int same;
-    const Unit u = rows.unit(u0, same);
+    const Unit u = rows.unit(u0);
     const int64_t ys = z.ys[1];
     T* out = (T*)z.y + u.b * z.ys[0] + u.s * z.ys[2] + u.h0 * ys;
     // every lane of the warp takes as many steps as any: sums over a row are the whole warp's shuffles
@@ -554,7 +553,7 @@ cudaError_t run_backward(const RopeArgs& a, float* dw0, float* dw1, void* ws, cu
   int blocks, split_at;
   const Split split = back_split(a, D, &blocks, &split_at);
   const auto kern = a.interleaved ? norm_rope_backward_kernel<T, D, true> : norm_rope_backward_kernel<T, D, false>;
-  constexpr int SMEM = Rows<T, D, 2>::SMEM;
+  constexpr int SMEM = Rows<T>::SMEM;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
   if (e != cudaSuccess) return e;
   count_launches(1);
