@@ -569,7 +569,8 @@ __global__ void __launch_bounds__(X_THREADS, 1)
             }
           }
           const float x = fmaxf(top[0], top[1]) * p.c2;
-          if (ptx::bar_red_or(u == u0 || x > m + LAG, pair, 64)) {
+          // (lanes without a query have what was left in shared memory: no say, or results would depend on it)
+          if (ptx::bar_red_or(u == u0 || (tid < nq && x > m + LAG), pair, 64)) {
             (c ? row[g * ROWS].y : row[g * ROWS].x) = x;
             bar_sync(pair, 64);
             const float up = max3(m, x, c ? row[g * ROWS].x : row[g * ROWS].y);

@@ -321,6 +321,23 @@ def test_two_calls_at_once():
     assert all(torch.equal(g, want) for g in got)
 
 
+@pytest.mark.parametrize("dtype", list(DT))
+def test_the_same_again(dtype):
+    """Results to the last bit, whatever the calls between them leave behind."""
+    rows, leads, shared = family(24, 900, lambda n, h: n * 37, 8, 64)
+    q, cache, lead = build(rows, leads, 8, 4, 128, 64, DT[dtype], 6, shared)
+    other, far = q.flip(0) * 30, torch.full_like(lead, -1)
+    want = kvp.kvp_paged_prefix_decode_attn(q, cache, lead, return_lse=True)
+    alone = kvp.kvp_paged_prefix_decode_attn(q, cache, far, return_lse=True)
+    for _ in range(20):
+        kvp.kvp_paged_prefix_decode_attn(other, cache, far)
+        got = kvp.kvp_paged_prefix_decode_attn(q, cache, lead, return_lse=True)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        kvp.kvp_paged_prefix_decode_attn(other, cache, lead)
+        got = kvp.kvp_paged_prefix_decode_attn(q, cache, far, return_lse=True)
+        assert all(torch.equal(a, b) for a, b in zip(got, alone))
+
+
 def test_wrong_leads_cost_time_only():
     rows, leads, shared = family(4, 600, lambda n, h: 20 * n, 1, 64)
     q, cache, lead = build(rows, leads, 1, 4, 64, 64, torch.float16, 6, shared)
