@@ -14,8 +14,9 @@
 //    issue, as long as it ran.  Warp 2 clears the slots behind an item's last token, warp 3 copies the
 //    next piece's queries.  Sixteen warps have the softmax.
 //  * Queries 0..127 and 128..255 are two groups of eight warps.  A thread has a query (a TMEM lane) and 64
-//    of a tile's keys: scores come from TMEM once, and the weights go back in their place as the first
-//    operand of P V.  Outputs stay in TMEM until the piece ends.
+//    of a tile's keys: scores come from TMEM (the second 32 again for their weights: 64 in registers spill),
+//    and the weights go back in their place as the first operand of P V.  Outputs stay in TMEM until the
+//    piece ends.
 //  * More than 128 queries: each group has its own, and both take every tile.  Up to 128: both have the
 //    same, take the tiles in turn, and put their results together when the piece ends; a piece of one tile
 //    is one group's, and the other goes on with the next.  Either way one group's softmax runs beside the
