@@ -676,7 +676,10 @@ int kvp_paged_decode_attn(const void* q, int64_t q_stride, const kvp_paged_cache
  * q, q_stride, sm_scale and lse as in kvp_paged_decode_attn; out [n_rows / h_kv, h_q,
  * head_dim] of the cache's dtype.  G = h_q / h_kv <= 16; at most KVP_PREFIX_MAX_SEQS
  * sequences.  The plan of the work is made on the device: a captured call serves a
- * cache and families that change.  workspace:
+ * cache and families that change.  It has room for some 2^28 tiles of 128 tokens (a
+ * prefix counts once for every 256 queries that read it, fp32 caches 32): a call of
+ * more work than that, seconds of it, gives out 0 and lse -inf everywhere and raises
+ * KVP_ERR_DEVICE_CHECK.  workspace:
  * kvp_paged_prefix_decode_attn_workspace_size() bytes, 256-byte aligned (some 2
  * outputs of float32 per query, and 5 to 20 MB). */
 #define KVP_PREFIX_MAX_SEQS 16384
