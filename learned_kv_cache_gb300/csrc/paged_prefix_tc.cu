@@ -22,11 +22,15 @@
 //    is one group's, and the other goes on with the next.  Either way one group's softmax runs beside the
 //    other's products.
 //  * V lies [key][dim] in memory, so it is the second operand in its MN-major form; nothing is transposed.
-//  * P enters the product as the sum of two 16-bit parts: 16 (bf16) or 22 (f16) bits of every weight, so
-//    that an output is off by its own rounding only; with one part bf16 outputs would be 1.4 times as far
+//  * P enters the product as the sum of two 16-bit parts: 16 (bf16) or 22 (f16) bits of every weight, 1/256 or
+//    1/2048 of the half step that an output is rounded by; with one part bf16 outputs would be 1.4 times as far
 //    off.  The outputs come in the cache's type.
-//  * The running maximum may lag by a factor of 2^8 before the outputs are scaled again: weights reach 2^8,
-//    which f16 holds, and most tiles move nothing.
+//  * f16 weights are kept 2^14 above the softmax's own (their reference is the maximum less 14): a part has
+//    nothing below 2^-24, and beside a sink token that is where all the others' weights lie.  Without that the
+//    tokens 17 nats below a sink lost 20 % of their sum, at 18 nats half or all of it.  (The smaller lag costs
+//    prefixes with 256 queries 1.5 %: 32768 tokens, 8 heads 61.9 -> 62.7 us; the others nothing.)
+//  * The running maximum may lag by a factor of 2^8 (f16: 2^1.5, as weights then reach 2^15.5 of its 2^16)
+//    before the outputs are scaled again, so most tiles move nothing.
 //  * Slots behind the last token of an item may hold anything: their logits become -inf, and their V is
 //    cleared in shared memory (0 * NaN would be NaN).
 #include <type_traits>
@@ -47,7 +51,14 @@ using prefix::TILE;
 constexpr int X_THREADS = 640;
 constexpr int ROWS = 128;                // queries of a group
 constexpr int RUN = 8;                   // sequences whose queries are copied at once
-constexpr float LAG = 8.f;               // log2 of how far the maximum may lag
+
+// Log2 of what weights are kept above the softmax's own, and of how far the maximum may lag.  f16 parts end at
+// 2^-24 and 2^16: what a pair of them leaves is 2^-22 of a weight, and never more than 2^-39 of the row's largest.
+// bf16 has the range of a float.
+template <typename T>
+constexpr float ABOVE = std::is_same<T, __half>::value ? 14.f : 0.f;
+template <typename T>
+constexpr float LAG = std::is_same<T, __half>::value ? 1.5f : 8.f;
 
 template <int D>
 struct Px {
@@ -571,7 +582,7 @@ __global__ void __launch_bounds__(X_THREADS, 1)
           }
           const float x = fmaxf(top[0], top[1]) * p.c2;
           // (lanes without a query have what was left in shared memory: no say, or results would depend on it)
-          if (ptx::bar_red_or(u == u0 || (tid < nq && x > m + LAG), pair, 64)) {
+          if (ptx::bar_red_or(u == u0 || (tid < nq && x > m + LAG<T>), pair, 64)) {
             (c ? row[g * ROWS].y : row[g * ROWS].x) = x;
             bar_sync(pair, 64);
             const float up = max3(m, x, c ? row[g * ROWS].x : row[g * ROWS].y);
@@ -592,7 +603,7 @@ __global__ void __launch_bounds__(X_THREADS, 1)
             }
             m = up;
           }
-          const float off = m == -INFINITY ? 0.f : -m;     // nothing but -inf so far: weights of 0
+          const float off = m == -INFINITY ? 0.f : ABOVE<T> - m;     // nothing but -inf so far: weights of 0
           const uint64_t c2 = pack2(p.c2, p.c2), off2 = pack2(off, off);
           uint64_t sum[2] = {0, 0};
           // 16 scores make way for 8 + 8 columns of weights; the second 32 are read again, 16 ahead (all 64 in
@@ -660,7 +671,7 @@ __global__ void __launch_bounds__(X_THREADS, 1)
             loaded(o);
             if (tid < nq) store_part(out + k, o);
           }
-          if (tid < nq && c == 0) *ml = make_float2(m, l);
+          if (tid < nq && c == 0) *ml = make_float2(m - ABOVE<T>, l);
           bar_sync(pair, 64);
         }
         ptx::tc_fence_before();
@@ -691,7 +702,7 @@ __global__ void __launch_bounds__(X_THREADS, 1)
               o[i] = __float_as_uint(fmaf(__uint_as_float(y[i]), fb, __uint_as_float(o[i]) * fa));
             if (tid < nq) store_part(out + k, o);
           }
-          if (tid < nq && w == 0) *ml = make_float2(M, fmaf(A.y, fa, B.y * fb));
+          if (tid < nq && w == 0) *ml = make_float2(M - ABOVE<T>, fmaf(A.y, fa, B.y * fb));
         }
         ptx::tc_fence_before();
         bar_sync(ALL, 512);                               // both outputs have been read
