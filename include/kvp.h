@@ -681,7 +681,8 @@ int kvp_paged_decode_attn(const void* q, int64_t q_stride, const kvp_paged_cache
  * more work than that, seconds of it, gives out 0 and lse -inf everywhere and raises
  * KVP_ERR_DEVICE_CHECK.  workspace:
  * kvp_paged_prefix_decode_attn_workspace_size() bytes, 256-byte aligned (some 2
- * outputs of float32 per query, and 5 to 20 MB). */
+ * outputs of float32 per query, and 5 to 20 MB; f16 caches for more than 8192 tokens a
+ * row 10 to 20 MB more). */
 #define KVP_PREFIX_MAX_SEQS 16384
 size_t kvp_paged_prefix_decode_attn_workspace_size(const kvp_paged_cache* cache, int h_q, int h_kv);
 int kvp_paged_prefix_decode_attn(const void* q, int64_t q_stride, const kvp_paged_cache* cache,

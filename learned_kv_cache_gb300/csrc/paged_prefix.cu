@@ -761,6 +761,8 @@ size_t layout(const PagedView& c, int G, int h_kv, Params* p, void* ws) {
   p->first_o = (float*)take(2 * R * G * D * 4);
   p->cont_ml = (float2*)take((size_t)p->ctas * p->qt * sizeof(float2));
   p->cont_o = (float*)take((size_t)p->ctas * p->qt * D * 4);
+  const bool keeps = c.dtype == KVP_F16 && c.cap > prefix::SEGMENT * TILE;
+  p->kept = keeps ? (float*)take((size_t)p->ctas * 256 * prefix::kept_row(c.D) * 4) : nullptr;
   return at;
 }
 

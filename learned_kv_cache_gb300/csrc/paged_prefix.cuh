@@ -22,6 +22,9 @@ namespace prefix {
 
 constexpr int TILE = 128;                // keys
 constexpr int GAP = 4;
+constexpr int SEGMENT = 64;              // of a group's f16 tiles that the tensor cores add up (a power of two)
+// Values of a query's kept sums (two groups of 128 queries a CTA): the outputs', and the maximum that they go by.
+__host__ __device__ constexpr int kept_row(int D) { return D + 8; }
 
 // A prefix with some of its queries, or a row's own tokens.
 struct __align__(16) Item {
@@ -67,6 +70,7 @@ struct Params {
   float* first_o;        // [...][D]
   float2* cont_ml;       // [ctas][qt]
   float* cont_o;
+  float* kept;           // [ctas][2][128][kept_row] sums of the segments before (f16 caches whose rows may have any)
   void* out;
   float* lse;
   int* status;

@@ -16,7 +16,13 @@
 //  * Queries 0..127 and 128..255 are two groups of eight warps.  A thread has a query (a TMEM lane) and 64
 //    of a tile's keys: scores come from TMEM (the second 32 again for their weights: 64 in registers spill),
 //    and the weights go back in their place as the first operand of P V.  Outputs stay in TMEM until the
-//    piece ends.
+//    piece, or in f16 a segment of it, ends.
+//  * The tensor cores' running sum drops bits at every step of 16 keys, always towards zero: 0.84 * 2^-24 of it
+//    each as measured, two steps for 16 keys.  131072 tokens in one CTA lost 4e-4 (8e-4 with more than 128
+//    queries): 0.8 to 1.7 of f16's half steps, 0.1 to 0.2 of bf16's.  So an f16 sum takes SEGMENT tiles, which
+//    lose a tenth of a half step, and is then added to fp32 sums in memory, which L2 holds.  It costs rows of
+//    that length 3 to 5 %, and by its instructions every f16 call 1 to 4 % (32 answers 61.1 -> 63.4 us; inside
+//    the loop over the tiles it cost bf16 and f16 as much again), and bf16 does without.
 //  * More than 128 queries: each group has its own, and both take every tile.  Up to 128: both have the
 //    same, take the tiles in turn, and put their results together when the piece ends; a piece of one tile
 //    is one group's, and the other goes on with the next.  Either way one group's softmax runs beside the
@@ -57,6 +63,11 @@ constexpr int RUN = 8;                   // sequences whose queries are copied a
 // bf16 has the range of a float.
 template <typename T>
 constexpr float ABOVE = std::is_same<T, __half>::value ? 14.f : 0.f;
+// Whether a piece's sums are taken in segments, and of how many of a group's tiles.
+template <typename T>
+constexpr bool CUT = std::is_same<T, __half>::value;
+using prefix::SEGMENT;
+
 template <typename T>
 constexpr float LAG = std::is_same<T, __half>::value ? 1.5f : 8.f;
 
@@ -414,7 +425,8 @@ __global__ void __launch_bounds__(X_THREADS, 1)
         qslot = both ? 0 : turn;
         turn ^= !both;
         for (int u = u0; ok && u < u1; ++u, ++li) {
-          const bool first = u - u0 < step, last = u1 - 1 - u < step;
+          const int at = CUT<T> ? (u - u0) & (SEGMENT * step - 1) : u - u0;
+          const bool first = at < step, last = u1 - 1 - u < step || (CUT<T> && at >= (SEGMENT - 1) * step);
           const bool begin = u == u0, end = u == u1 - 1;
           if (both || !(li & 1)) {
             if (ga.pend >= 0) outputs(A, ga, gb);
@@ -543,102 +555,153 @@ __global__ void __launch_bounds__(X_THREADS, 1)
       const int q0 = both ? g * ROWS : 0, nq = min(ROWS, a.it.nq - q0), tokens = a.it.tok1 - a.it.tok0 - 64 * c;
       const bool busy = quad * 32 < nq;                   // (the same in both warps)
       const bool alone = both || tiles == 1;              // a group with its outputs
+      int outs = g ? uses_ob : uses_oa;                   // outputs (a segment's each) that have been waited for
       if (!dry) {
-        uses_oa += both || tiles > 1 || !(li0 & 1);
-        uses_ob += both || tiles > 1 || (li0 & 1);
+        const int na = both ? tiles : (tiles + !(li0 & 1)) >> 1, nb = both ? tiles : tiles - na;   // the groups' tiles
+        uses_oa += CUT<T> ? (na + SEGMENT - 1) / SEGMENT : na > 0;
+        uses_ob += CUT<T> ? (nb + SEGMENT - 1) / SEGMENT : nb > 0;
         li0 += tiles;
       }
       if (u0 >= a.u1) continue;                           // the other group has the piece's only tile
       float m = -INFINITY, l = 0.f;
-      for (int u = u0; u < a.u1; u += step) {
-        if (!dry) ok = ok && wait(bar_s + 8 * g, uses_s++ & 1);
-        const int valid = tokens - u * TILE;
-        if (busy) {
-          ptx::tc_fence_after();
-          uint32_t s[32];
-          float top[2] = {-INFINITY, -INFINITY};
-          {
-            uint32_t y[32];
-            ptx::tmem_ld32(ts, s);
-            ptx::tmem_ld32(ts + 32, y);
-            ptx::tmem_ld_wait();
-            loaded(s);
-            loaded(y);
-            if (p.flip || p.zero || valid < 64) {
-              const float mul = p.zero ? 0.f : p.flip ? -1.f : 1.f;
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                s[i] = i < valid ? __float_as_uint(__uint_as_float(s[i]) * mul) : 0xff800000u;
-                y[i] = i + 32 < valid ? __float_as_uint(__uint_as_float(y[i]) * mul) : 0xff800000u;
-              }
-              tmem_st32(ts + 32, y);
-              tmem_st_wait();
-            }
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              top[0] = max3(top[0], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
-              top[1] = max3(top[1], __uint_as_float(y[i]), __uint_as_float(y[i + 1]));
-            }
-          }
-          const float x = fmaxf(top[0], top[1]) * p.c2;
-          // (lanes without a query have what was left in shared memory: no say, or results would depend on it)
-          if (ptx::bar_red_or(u == u0 || (tid < nq && x > m + LAG<T>), pair, 64)) {
-            (c ? row[g * ROWS].y : row[g * ROWS].x) = x;
-            bar_sync(pair, 64);
-            const float up = max3(m, x, c ? row[g * ROWS].x : row[g * ROWS].y);
-            if (u != u0) {
-              const float f = paged::weight(m, up);
-              l *= f;
-              // the tile before has been added up: the scores' barrier follows its products
+      // This warp's columns of the outputs, and of the sums of the segments before if there are any, to memory or
+      // back into TMEM.  (The maximum that the kept sums go by lies behind them: there is no register for it.)
+      const auto add_kept = [&](bool back, bool any) {
+        float* kept = p.kept + ((size_t)(cta * 2 + g) * ROWS + tid) * prefix::kept_row(D);
+        const float f = any ? paged::weight(kept[D + c], m) : 0.f;
+        kept[D + c] = m;
 #pragma unroll 1
-              for (int k = c * (D / 2); k < (c + 1) * (D / 2); k += 8) {
-                uint32_t o[8];
-                tmem_ld8(to + 128 * g + k, o);
-                ptx::tmem_ld_wait();
-                loaded(o);
+        for (int k = c * (D / 2); k < (c + 1) * (D / 2); k += 32) {
+          uint32_t o[32];
+          float4 x[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                tmem_st8(to + 128 * g + k, o);
-              }
-            }
-            m = up;
+          for (int i = 0; i < 8; ++i)
+            x[i] = any ? *reinterpret_cast<const float4*>(kept + k + 4 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
+          ptx::tmem_ld32(to + 128 * g + k, o);
+          ptx::tmem_ld_wait();
+          loaded(o);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            x[i].x = fmaf(x[i].x, f, __uint_as_float(o[4 * i]));
+            x[i].y = fmaf(x[i].y, f, __uint_as_float(o[4 * i + 1]));
+            x[i].z = fmaf(x[i].z, f, __uint_as_float(o[4 * i + 2]));
+            x[i].w = fmaf(x[i].w, f, __uint_as_float(o[4 * i + 3]));
           }
-          const float off = m == -INFINITY ? 0.f : ABOVE<T> - m;     // nothing but -inf so far: weights of 0
-          const uint64_t c2 = pack2(p.c2, p.c2), off2 = pack2(off, off);
-          uint64_t sum[2] = {0, 0};
-          // 16 scores make way for 8 + 8 columns of weights; the second 32 are read again, 16 ahead (all 64 in
-          // registers would spill)
-          const auto weigh = [&](const uint32_t* x, int k) {
-            uint32_t parts[16];
+          if (back) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              float w0, w1;
-              unpack2(ffma2(pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), c2, off2), w0, w1);
-              const uint64_t w = pack2(fast_exp2(w0), fast_exp2(w1));
-              sum[i & 1] = fadd2(sum[i & 1], w);
-              split(T(), w, parts[i], parts[8 + i]);
+              o[4 * i] = __float_as_uint(x[i].x);
+              o[4 * i + 1] = __float_as_uint(x[i].y);
+              o[4 * i + 2] = __float_as_uint(x[i].z);
+              o[4 * i + 3] = __float_as_uint(x[i].w);
             }
-            tmem_st16(ts + k, parts);
-          };
-          uint32_t y[2][16];
-          weigh(s, 0);
-          tmem_ld16(ts + 32, y[0]);
-          weigh(s + 16, 16);
-          ptx::tmem_ld_wait();
-          loaded(y[0]);
-          tmem_ld16(ts + 48, y[1]);
-          weigh(y[0], 32);
-          ptx::tmem_ld_wait();
-          loaded(y[1]);
-          weigh(y[1], 48);
-          float a0, a1;
-          unpack2(fadd2(sum[0], sum[1]), a0, a1);
-          l += a0 + a1;
-          tmem_st_wait();
-          ptx::tc_fence_before();
+            tmem_st32(to + 128 * g + k, o);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) *reinterpret_cast<float4*>(kept + k + 4 * i) = x[i];
+          }
         }
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar_p + 8 * g);
+        if (back) tmem_st_wait();
+      };
+      int v0 = u0;                                        // first tile of the segment
+      for (;; v0 += SEGMENT * step) {
+        const int v1 = CUT<T> ? min(a.u1, v0 + SEGMENT * step) : a.u1;
+        for (int u = v0; u < v1; u += step) {
+          if (!dry) ok = ok && wait(bar_s + 8 * g, uses_s++ & 1);
+          const int valid = tokens - u * TILE;
+          if (busy) {
+            ptx::tc_fence_after();
+            uint32_t s[32];
+            float top[2] = {-INFINITY, -INFINITY};
+            {
+              uint32_t y[32];
+              ptx::tmem_ld32(ts, s);
+              ptx::tmem_ld32(ts + 32, y);
+              ptx::tmem_ld_wait();
+              loaded(s);
+              loaded(y);
+              if (p.flip || p.zero || valid < 64) {
+                const float mul = p.zero ? 0.f : p.flip ? -1.f : 1.f;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                  s[i] = i < valid ? __float_as_uint(__uint_as_float(s[i]) * mul) : 0xff800000u;
+                  y[i] = i + 32 < valid ? __float_as_uint(__uint_as_float(y[i]) * mul) : 0xff800000u;
+                }
+                tmem_st32(ts + 32, y);
+                tmem_st_wait();
+              }
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                top[0] = max3(top[0], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+                top[1] = max3(top[1], __uint_as_float(y[i]), __uint_as_float(y[i + 1]));
+              }
+            }
+            const float x = fmaxf(top[0], top[1]) * p.c2;
+            // (lanes without a query have what was left in shared memory: no say, or results would depend on it)
+            if (ptx::bar_red_or(u == v0 || (tid < nq && x > m + LAG<T>), pair, 64)) {
+              (c ? row[g * ROWS].y : row[g * ROWS].x) = x;
+              bar_sync(pair, 64);
+              const float up = max3(m, x, c ? row[g * ROWS].x : row[g * ROWS].y);
+              const float f = paged::weight(m, up);
+              l *= f;
+              if (u != v0) {
+                // the tile before has been added up: the scores' barrier follows its products
+#pragma unroll 1
+                for (int k = c * (D / 2); k < (c + 1) * (D / 2); k += 8) {
+                  uint32_t o[8];
+                  tmem_ld8(to + 128 * g + k, o);
+                  ptx::tmem_ld_wait();
+                  loaded(o);
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                  tmem_st8(to + 128 * g + k, o);
+                }
+              }
+              m = up;
+            }
+            const float off = m == -INFINITY ? 0.f : ABOVE<T> - m;     // nothing but -inf so far: weights of 0
+            const uint64_t c2 = pack2(p.c2, p.c2), off2 = pack2(off, off);
+            uint64_t sum[2] = {0, 0};
+            // 16 scores make way for 8 + 8 columns of weights; the second 32 are read again, 16 ahead (all 64 in
+            // registers would spill)
+            const auto weigh = [&](const uint32_t* x, int k) {
+              uint32_t parts[16];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                float w0, w1;
+                unpack2(ffma2(pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), c2, off2), w0, w1);
+                const uint64_t w = pack2(fast_exp2(w0), fast_exp2(w1));
+                sum[i & 1] = fadd2(sum[i & 1], w);
+                split(T(), w, parts[i], parts[8 + i]);
+              }
+              tmem_st16(ts + k, parts);
+            };
+            uint32_t y[2][16];
+            weigh(s, 0);
+            tmem_ld16(ts + 32, y[0]);
+            weigh(s + 16, 16);
+            ptx::tmem_ld_wait();
+            loaded(y[0]);
+            tmem_ld16(ts + 48, y[1]);
+            weigh(y[0], 32);
+            ptx::tmem_ld_wait();
+            loaded(y[1]);
+            weigh(y[1], 48);
+            float a0, a1;
+            unpack2(fadd2(sum[0], sum[1]), a0, a1);
+            l += a0 + a1;
+            tmem_st_wait();
+            ptx::tc_fence_before();
+          }
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bar_p + 8 * g);
+        }
+        if (!CUT<T> || v0 + SEGMENT * step >= a.u1) break;
+        ok = ok && wait(bar_o + 8 * g, outs++ & 1);
+        if (busy) {
+          ptx::tc_fence_after();
+          add_kept(false, v0 != u0);
+        }
       }
       if (dry) {
         dry = false;
@@ -656,8 +719,9 @@ __global__ void __launch_bounds__(X_THREADS, 1)
       }
       float* out = (a.u0 == 0 ? p.first_o : p.cont_o) + slot * D;
       float2* ml = (a.u0 == 0 ? p.first_ml : p.cont_ml) + slot;
-      ok = ok && wait(bar_o + 8 * g, ((g ? uses_ob : uses_oa) - 1) & 1);
+      ok = ok && wait(bar_o + 8 * g, outs & 1);
       ptx::tc_fence_after();
+      if (CUT<T> && busy && v0 != u0) add_kept(true, true);
       if (alone) {
         if (busy) {
           (c ? row[g * ROWS].y : row[g * ROWS].x) = l;
@@ -685,7 +749,9 @@ __global__ void __launch_bounds__(X_THREADS, 1)
           bar_sync(pair, 64);
           if (!c) row[g * ROWS] = make_float2(m, l + row[g * ROWS].y);
         }
+        ptx::tc_fence_before();
         bar_sync(ALL, 512);
+        ptx::tc_fence_after();
         if (busy) {
           const float2 A = row[0], B = row[ROWS];
           const float M = fmaxf(A.x, B.x), fa = paged::weight(A.x, M), fb = paged::weight(B.x, M);
