@@ -179,6 +179,14 @@ def _positions(positions, like):
     return positions.data_ptr(), strides[0] if len(strides) == 2 and B > 1 else 0
 
 
+def _start(start):
+    """(An int that is passed to C as 32 bits would lose the others.)"""
+    start = int(start)
+    if not -1 << 31 <= start < 1 << 31:
+        raise ValueError(f"start must fit 32 bits, got {start}")
+    return start
+
+
 def _rope_ref(rope):
     if rope is None:
         return None
@@ -208,7 +216,7 @@ def kvp_rope(x, rope, positions=None, start=0, inverse=False, out=None, stream=N
     dtype = _code(dtype)
     out, out_ptr, os = _result(out, "out", x, like)
     pos, ps = _positions(positions, like)
-    rc = load().kvp_rope(x_ptr, out_ptr, dtype, B, H, S, D, xs, os, _rope_ref(rope), pos, ps, int(start),
+    rc = load().kvp_rope(x_ptr, out_ptr, dtype, B, H, S, D, xs, os, _rope_ref(rope), pos, ps, _start(start),
                          int(bool(inverse)), _raw_stream(index))
     if rc:
         _check("kvp_rope", rc)
@@ -264,7 +272,7 @@ def kvp_qk_norm_rope(q, k, q_weight=None, k_weight=None, eps=1e-6, rope=None, po
     pos, ps = _positions(positions, like)
     qw, kw, wd = _weights(q_weight, k_weight, like)
     rc = load().kvp_qk_norm_rope(q_ptr, k_ptr, qo_ptr, ko_ptr, dtype, B, Hq, k_like[3], S, D, qs, ks, qos, kos, qw, kw, wd,
-                                 float(eps), _rope_ref(rope), pos, ps, int(start), _raw_stream(index))
+                                 float(eps), _rope_ref(rope), pos, ps, _start(start), _raw_stream(index))
     if rc:
         _check("kvp_qk_norm_rope", rc)
     return q_out, k_out
@@ -305,7 +313,7 @@ def kvp_qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight=None, k_weight=None
             raise ValueError(f"workspace must be on {device}, got {workspace.device}")
     rc = load().kvp_qk_norm_rope_backward(gq_ptr, gk_ptr, q_ptr, k_ptr, dq_ptr, dk_ptr, dwq.data_ptr(), dwk.data_ptr(), dtype,
                                           B, Hq, k_like[3], S, D, gqs, gks, qs, ks, dqs, dks, qw, kw, wd, float(eps),
-                                          _rope_ref(rope), pos, ps, int(start), workspace.data_ptr(), workspace.numel(),
+                                          _rope_ref(rope), pos, ps, _start(start), workspace.data_ptr(), workspace.numel(),
                                           _raw_stream(index))
     if rc:
         _check("kvp_qk_norm_rope_backward", rc)
