@@ -204,7 +204,8 @@ def _code(dtype):
 
 def kvp_rope(x, rope, positions=None, start=0, inverse=False, out=None, stream=None):
     """Rotate x [B, H, S, D] (or [H, S, D]; strided views are read in place) by the positions of its tokens:
-    int32 [S] or [B, S], or start, start + 1, ...  ``inverse`` turns back (the rotation's gradient).  ``out`` may
+    int32 [S] or [B, S], or start, start + 1, ...  ``inverse`` turns back (the rotation's gradient; keys that are
+    moved back to other positions take a ``rope`` of gain 1: they have the rotation's already).  ``out`` may
     be x itself; by default a new dense tensor."""
     x_ptr, xs, like = _rows(x, "x")
     index, dtype, B, H, S, D = like
