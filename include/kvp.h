@@ -465,10 +465,11 @@ int kvp_decode_attn_noalloc(const void* q, const void* kc, const void* vc, int d
  *   a' = gain * (a cos t - b sin t),   b' = gain * (b cos t + a sin t)
  *
  * and the values behind rotary_dim unchanged.  inverse = 1 turns by -t (times gain):
- * the gradient of the rotation, or, with the positions' differences, keys moved back
- * to other positions when an eviction closes up the tokens it keeps.  Angles are
- * exact to 2^-32 of a turn for every 32-bit position, negative ones among them;
- * values are computed in 32 bits and rounded once.
+ * the gradient of the rotation, or, with the positions' differences and a gain of 1
+ * (rotated keys have the gain already), keys moved back to other positions when an
+ * eviction closes up the tokens it keeps.  Whole turns are dropped in fixed point: for
+ * every 32-bit position, negative ones among them, cosine and sine are off by 2^-22 at
+ * most (before the gain); values are computed in 32 bits and rounded once.
  *
  * rope: HOST struct; inv_freq a HOST array of rotary_dim / 2 radians per position in
  * [0, 1e6], which the call has read when it returns.  rotary_dim: a multiple of 16 up

@@ -91,7 +91,7 @@ __device__ __forceinline__ void store8(__half* p, const uint64_t* v) {
 }
 
 // Cosine and sine of pos * step turns.  Within an eighth of a turn of the nearest quarter the Taylor series
-// up to t^10 leave 3e-10 (t^11 / 11! at pi / 4); no branches, as the quarters differ from lane to lane (the
+// up to t^10 leave 1.8e-9 (t^11 / 11! at pi / 4); no branches, as the quarters differ from lane to lane (the
 // library's function and a switch took 3 times the instructions, half of all).
 __device__ __forceinline__ float2 turn_of(int pos, uint64_t step) {
   const uint32_t t = (uint32_t)(((uint64_t)(int64_t)pos * step) >> 32);
@@ -309,7 +309,8 @@ template <typename T, int D, bool NORM, bool INTERLEAVED>
 __global__ void __launch_bounds__(THREADS, FORWARD_BLOCKS)
     rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ Freqs f, const __grid_constant__ Split split) {
   using L = Lane<D, INTERLEAVED>;
-  // rows at a time: twice these in registers (four with norms spill: 457 us of 131072 tokens for 434)
+  // Rows at a time: twice these in registers.  (Norms of 16-bit rows with four: 457 us of 131072 tokens for 434.
+  // With three and two, the norms of pairs of halves spill 12 bytes in 16 bits and 108 in fp32, interleaved 0 and 28.)
   constexpr int U = sizeof(T) == 4 ? 2 : NORM ? 3 : 4;
   __shared__ __align__(16) Tables<D> sh;
   const L lane(a.rotary_dim);
