@@ -661,7 +661,7 @@ int kvp_paged_decode_attn(const void* q, int64_t q_stride, const kvp_paged_cache
 
 /* Decode attention of sequences that share a long prefix: kvp_paged_decode_attn's
  * out and lse, with the pages that several rows hold in common read once for all of
- * them.
+ * them: once for every 256 queries of a KV head (of whole sequences; fp32 caches 32).
  *
  * lead [n_rows / h_kv] int32 (device): the sequence whose leading pages a sequence may
  * share (kvp_paged_fork's src, by sequences), itself or a negative number for one that
@@ -671,7 +671,7 @@ int kvp_paged_decode_attn(const void* q, int64_t q_stride, const kvp_paged_cache
  * are served as they are.  Of the members' shared lengths of a family the one that
  * saves most reads is taken (out of more than 32 members, 32 lengths are looked at),
  * and members that share less read all their tokens themselves.  A sequence whose lead
- * follows a third one reads for itself; a lead >= n_rows / h_kv does too, and raises
+ * follows a third one (a fork of a fork that names the nearer) reads for itself; a lead >= n_rows / h_kv does too, and raises
  * KVP_ERR_DEVICE_CHECK.
  *
  * q, q_stride, sm_scale and lse as in kvp_paged_decode_attn; out [n_rows / h_kv, h_q,

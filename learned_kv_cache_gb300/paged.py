@@ -307,8 +307,10 @@ def kvp_paged_prefix_decode_attn(q, cache, lead, sm_scale=None, out=None, lse=No
                                  stream=None):
     """:func:`kvp_paged_decode_attn` for sequences that share a long prefix: q [N, H_q, D], rows
     r = n * h_kv + h -> out [N, H_q, D] of the cache's dtype (with ``return_lse`` also lse float32
-    [N, H_q]).  lead int32 [N]: the sequence that each one was forked from (itself or negative: none).
-    The leading pages that its rows still hold in common with that sequence's are read once for all."""
+    [N, H_q]).  lead int32 [N]: the sequence that holds each one's prompt (itself or negative: none) and
+    follows nobody itself: a fork of a fork has its lead's lead, or else reads all its tokens for itself.
+    The leading pages that its rows still hold in common with that sequence's are read once for all (for
+    every 256 queries of a KV head; fp32 caches 32)."""
     if _cache(cache)._elsewhere(stream):
         with cache._there(stream):
             return kvp_paged_prefix_decode_attn(q, cache, lead, sm_scale, out, lse, return_lse, workspace)
