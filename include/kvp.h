@@ -675,8 +675,10 @@ int kvp_paged_decode_attn(const void* q, int64_t q_stride, const kvp_paged_cache
  * KVP_ERR_DEVICE_CHECK.
  *
  * q, q_stride and lse as in kvp_paged_decode_attn, sm_scale too but for its product with
- * log2(e), which is rounded to a float here, as a logit is (each 2^-24 of it at most); out
- * [n_rows / h_kv, h_q, head_dim] of the cache's dtype, never KVP_F32 beside a 16-bit cache.  G = h_q / h_kv <= 16; at most KVP_PREFIX_MAX_SEQS
+ * log2(e), which is rounded to a float here, as a logit is (each 2^-24 of it at most); on
+ * the tensor cores a logit loses bits besides: lse is off by 2^-20 of its row's largest
+ * sm_scale * sum |q_i k_i| at most, and by its own sum's 2^-20.  out [n_rows / h_kv, h_q,
+ * head_dim] of the cache's dtype, never KVP_F32 beside a 16-bit cache.  G = h_q / h_kv <= 16; at most KVP_PREFIX_MAX_SEQS
  * sequences.  The plan of the work is made on the device: a captured call serves a
  * cache and families that change.  It has room for some 2^28 tiles of 128 tokens (a
  * prefix counts once for every 256 queries that read it, fp32 caches 32): a call of
