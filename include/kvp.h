@@ -668,25 +668,25 @@ int kvp_paged_decode_attn(const void* q, int64_t q_stride, const kvp_paged_cache
  * follows nobody.  It only says where to look: for every KV head, the pages that the
  * tables of the two rows have in common from the start on, and that both have filled,
  * are the shared prefix, so rows that were evicted or grew on their own since the fork
- * are served as they are.  Of the members' shared lengths of a family the one that
- * saves most reads is taken (out of more than 32 members, 32 lengths are looked at),
- * and members that share less read all their tokens themselves.  A sequence whose lead
- * follows a third one (a fork of a fork that names the nearer) reads for itself; a lead >= n_rows / h_kv does too, and raises
- * KVP_ERR_DEVICE_CHECK.
+ * are served as they are.  Of the members' shared lengths of a family the one that saves
+ * most reads is taken (out of more than 32 members, 32 lengths are looked at), and
+ * members that share less read all their tokens themselves.  A sequence whose lead
+ * follows a third one (a fork of a fork that names the nearer) reads for itself; a lead
+ * >= n_rows / h_kv does too, and raises KVP_ERR_DEVICE_CHECK.
  *
  * q, q_stride and lse as in kvp_paged_decode_attn, sm_scale too but for its product with
- * log2(e), which is rounded to a float here, as a logit is (each 2^-24 of it at most); on
- * the tensor cores a logit loses bits besides: lse is off by 2^-20 of its row's largest
- * sm_scale * sum |q_i k_i| at most, and by its own sum's 2^-20.  out [n_rows / h_kv, h_q,
- * head_dim] of the cache's dtype, never KVP_F32 beside a 16-bit cache.  G = h_q / h_kv <= 16; at most KVP_PREFIX_MAX_SEQS
- * sequences.  The plan of the work is made on the device: a captured call serves a
- * cache and families that change.  It has room for some 2^28 tiles of 128 tokens (a
- * prefix counts once for every 256 queries that read it, fp32 caches 32): a call of
- * more work than that, seconds of it, gives out 0 and lse -inf everywhere and raises
- * KVP_ERR_DEVICE_CHECK.  workspace:
- * kvp_paged_prefix_decode_attn_workspace_size() bytes, 256-byte aligned (some 2
- * outputs of float32 per query, and 5 to 20 MB; f16 caches for more than 8192 tokens a
- * row 10 to 20 MB more). */
+ * log2(e), which is rounded to a float here, as a logit is (each 2^-24 of it at most);
+ * on the tensor cores a logit loses bits besides: lse is off by 2^-20 of its row's
+ * largest sm_scale * sum |q_i k_i| at most, and by its own sum's 2^-20.  out [n_rows /
+ * h_kv, h_q, head_dim] of the cache's dtype, never KVP_F32 beside a 16-bit cache.  G =
+ * h_q / h_kv <= 16; at most KVP_PREFIX_MAX_SEQS sequences.  The plan of the work is made
+ * on the device: a captured call serves a cache and families that change.  It has room
+ * for some 2^28 tiles of 128 tokens (a prefix counts once for every 256 queries that
+ * read it, fp32 caches 32): a call of more work than that, seconds of it, gives out 0
+ * and lse -inf everywhere and raises KVP_ERR_DEVICE_CHECK.  workspace:
+ * kvp_paged_prefix_decode_attn_workspace_size() bytes, 256-byte aligned (some 2 outputs
+ * of float32 per query, and 3 to 20 MB; f16 caches for more than 8192 tokens a row 11 to
+ * 21 MB more). */
 #define KVP_PREFIX_MAX_SEQS 16384
 size_t kvp_paged_prefix_decode_attn_workspace_size(const kvp_paged_cache* cache, int h_q, int h_kv);
 int kvp_paged_prefix_decode_attn(const void* q, int64_t q_stride, const kvp_paged_cache* cache,
