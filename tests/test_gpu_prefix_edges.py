@@ -141,3 +141,57 @@ def test_as_many_sequences_as_a_call_takes(dtype, members):
     rows = [[max(r[0], 70)] if n % members == 0 else r for n, r in enumerate(rows)]
     shared = [[min(rows[n][0], rows[l][0]) // ps if n != l else 0] for n, l in enumerate(leads)]
     check(*build(rows, leads, 1, 2, 64, ps, DT[dtype], 10, shared))
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_some_rows_of_a_cache(dtype):
+    """The rows of four sequences in the middle, on the pages of all."""
+    rows, leads, shared = family(8, 700, lambda i, h: i * 23 + h, 2, 32, first=2)
+    q, cache, _ = build(rows, leads, 2, 4, 64, 32, DT[dtype], 4, shared)
+    check(q[2:6].contiguous(), cache.rows(4, 12), torch.tensor([0, 0, 0, -1], dtype=torch.int32, device="cuda"))
+    check(q[5:], cache.rows(10, 16), torch.tensor([1, 1, 1], dtype=torch.int32, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_pages_past_32_bits(dtype):
+    """Pages whose first value is number 2^31 and more of the pool, in prefixes and own tokens."""
+    ps, D = 1024, 128
+    n_pages = 2 ** 31 // (ps * D) + 40
+    pool = [torch.empty(n_pages, ps, D, dtype=DT[dtype], device="cuda") for _ in range(2)]
+    gen = torch.Generator("cuda").manual_seed(0)
+    for p in pool:
+        p[-40:].normal_(generator=gen)
+    N, G = 9, 4
+    table = torch.zeros(N, 8, dtype=torch.int32)
+    table[:, :3] = torch.tensor([n_pages - 1, n_pages - 17, n_pages - 5])
+    table[:, 3] = n_pages - 30 + torch.arange(N, dtype=torch.int32)
+    cache = kvp.PagedCache(*pool, table.cuda(), torch.full((N,), 3 * ps + 333, dtype=torch.int32, device="cuda"),
+                           torch.ones(n_pages, dtype=torch.int32, device="cuda"),
+                           torch.zeros((n_pages + 31) // 32, dtype=torch.int32, device="cuda"))
+    q = torch.randn(N, G, D, generator=gen, device="cuda").to(DT[dtype])
+    for lead in (torch.zeros(N, dtype=torch.int32), torch.full((N,), -1, dtype=torch.int32)):
+        check(q, cache, lead.cuda())
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_two_captured_calls_take_turns(dtype):
+    """Two graphs of one pool of memory, replayed in turn while the cache grows: each has what it needs of its own."""
+    rows, leads, shared = family(6, 900, lambda i, h: i * 31, 2, 32)
+    q, cache, lead = build(rows, leads, 2, 4, 64, 32, DT[dtype], 4, shared, max_pages=40)
+    other = torch.full_like(lead, -1)
+    kvp.kvp_paged_prefix_decode_attn(q, cache, lead)
+    graphs, outs = [], []
+    for l in (lead, other):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], pool=graphs[0].pool() if outs else None):
+            outs.append(kvp.kvp_paged_prefix_decode_attn(q, cache, l, return_lse=True))
+    for step in range(4):
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for (out, lse), l in zip(outs, (lead, other)):
+            want, want_lse = kvp.kvp_paged_prefix_decode_attn(q, cache, l, return_lse=True)
+            assert torch.equal(out, want) and torch.equal(lse, want_lse)
+        check(q, cache, lead)
+        cache.lens[step] -= 100 * step
+        q.normal_()
